@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libqpack.so")
 
 QP_OK, QP_EINVAL, QP_EUNSUPPORTED, QP_EOVERFLOW, QP_ESIZE, QP_EALIGN, QP_EHIP = 0, -1, -2, -3, -4, -5, -6
 QP_S8, QP_S4, QP_S32, QP_F32 = 1, 2, 3, 4
+QP_BF16, QP_F16, QP_S64 = 5, 6, 7
 QP_PER_TENSOR, QP_PER_CHANNEL, QP_BLOCKWISE, QP_DYNAMIC_PER_ROW = 0, 1, 2, 3
 QP_BLOCKWISE_BF16, QP_BLOCKWISE_ASYM = 4, 5
 QP_ROUND_HALF_EVEN = 0
@@ -105,6 +106,23 @@ SIGNATURES = {
                                      _I32, _I32, _SZ]),
     "qconv2d_s8": (C.c_int, [_QT, _P, _PI, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
                              _I32, _I32, _P, _I64, _QT, _I32, _P, _P, C.c_size_t, _P]),
+    "qgemm_w4_blockwise": (C.c_int, [_P, _I32, _I64, _I64, _I64, _PI, _P, _P, _F, _F, _P, _I32,
+                                     _I64, _P]),
+    "qgemm_w4_experts": (C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _I64, _I64, _PI, _P, _I64, _I64,
+                                   _P, _P, _F, _F, _P, _I32, _I64, _P]),
+    "qgemm_w4_dx_ws_size": (C.c_int, [_I64, _PI, _I64, _SZ]),
+    "qgemm_w4_blockwise_dx": (C.c_int, [_P, _I32, _I64, _I64, _PI, _P, _P, _I64, _P, C.c_size_t,
+                                        _P]),
+    "qgemm_w4_experts_dx": (C.c_int, [_P, _I32, _I64, _I64, _PI, _P, _I64, _I64, _P, _P, _I64, _P,
+                                      C.c_size_t, _P]),
+    "qmoe_sort_ws_size": (C.c_int, [_I64, _I64, _I64, _SZ]),
+    "qmoe_sort": (C.c_int, [_P, _I32, _I64, _I64, _I64, _I64, _P, _P, _P, _P, C.c_size_t, _P]),
+    "qmoe_dispatch": (C.c_int, [_P, _I32, _I64, _I64, _P, _I32, _I64, _I64, _I64, _I64, _P, _I64,
+                                _P, _P, _P, _P, C.c_size_t, _P]),
+    "qmoe_dispatch_grad": (C.c_int, [_P, _I32, _I64, _I64, _I64, _I64, _P, _P, _I64, _P]),
+    "qmoe_combine": (C.c_int, [_P, _I32, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _P]),
+    "qmoe_combine_grad": (C.c_int, [_P, _I64, _P, _I64, _I32, _I64, _I64, _I64, _P, _P, _P, _I64,
+                                    _P, _I64, _P, _I64, _P]),
 }
 
 
@@ -592,3 +610,258 @@ def qconv2d_s8_blockwise_f32(X: torch.Tensor, s_in: float, zp_in: int, blob: tor
                                          _ptr(out), _stream(X.device)),
            "qconv2d_s8_blockwise_f32")
     return out
+
+
+# ---------------------------------------------------------------- weight-only int4
+_FLOAT = {torch.float32: QP_F32, torch.bfloat16: QP_BF16, torch.float16: QP_F16}
+
+
+def _rows(t, what):
+    assert t.dim() == 2 and t.dtype in _FLOAT and (t.stride(1) == 1 or t.shape[1] == 1), \
+        "%s: rows must be 2-D float32, bfloat16 or float16 with unit column stride" % what
+    return _FLOAT[t.dtype]
+
+
+def _ld(t):
+    # the stride of a single row means nothing to torch; the library wants at
+    # least the columns.  Several rows keep theirs (a broadcast one is refused).
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _ints(t, what, dtype=torch.int32):
+    assert t.dtype == dtype and t.is_contiguous(), \
+        "%s must be a contiguous %s tensor" % (what, dtype)
+
+
+def _f32(t, what):
+    assert t is None or (t.dtype == torch.float32 and t.is_contiguous()), \
+        "%s must be a contiguous float32 tensor" % what
+
+
+def pack_s4_experts(w: torch.Tensor, scales: torch.Tensor, group_size=32, scale_dtype="f32",
+                    offsets=None):
+    """Pack the int4 weights of a set of experts, [E, N, K] with scales (and
+    offsets) [E, N, ceil(K/group)]: returns (blobs uint8 [E, bytes], info),
+    expert e's blob at blobs[e]."""
+    assert w.dim() == 3 and w.shape[0] >= 1
+    blobs = info = None
+    for e in range(w.shape[0]):
+        off = None if offsets is None else offsets[e]
+        if blobs is None:
+            blob, info = pack_s4(w[e], scales[e], group_size, scale_dtype, off)
+            blobs = _alloc_bytes(w.shape[0] * blob.numel(), w.device).view(w.shape[0], -1)
+            blobs[0].copy_(blob)
+        else:
+            pack_s4(w[e], scales[e], group_size, scale_dtype, off, into=(blobs[e], info))
+    return blobs, info
+
+
+def qgemm_w4_blockwise(X: torch.Tensor, blob: torch.Tensor, info: PackedInfo, bias=None,
+                       clamp_lo=-float("inf"), clamp_hi=float("inf"), out=None, out_dtype=None):
+    """Y = clamp(X @ W^T + bias): float rows (f32, bf16 or f16, not quantized)
+    times an int4 blob; outputs in X's type or `out_dtype` float32."""
+    dt = _rows(X, "X")
+    M, K = X.shape
+    if out is None:
+        out = torch.empty((M, info.N), dtype=out_dtype or X.dtype, device=X.device)
+    odt = _rows(out, "out")
+    assert tuple(out.shape) == (M, info.N), "out must be [M, N]"
+    _f32(bias, "bias")
+    assert bias is None or bias.numel() == info.N, "bias must hold N values"
+    _check(_lib.qgemm_w4_blockwise(_ptr(X), dt, M, K, _ld(X), C.byref(info), _ptr(blob), _ptr(bias),
+                                   clamp_lo, clamp_hi, _ptr(out), odt, _ld(out),
+                                   _stream(X.device)), "qgemm_w4_blockwise")
+    return out
+
+
+def _experts(blobs, offsets):
+    assert blobs.dim() == 2 and blobs.dtype == torch.uint8 and blobs.stride(1) == 1, \
+        "blobs must be uint8 [experts, bytes] (pack_s4_experts)"
+    _ints(offsets, "offsets")
+    assert offsets.numel() == blobs.shape[0] + 1, "offsets must hold experts + 1 values"
+
+
+def qgemm_w4_experts(X: torch.Tensor, blobs: torch.Tensor, info: PackedInfo, offsets: torch.Tensor,
+                     bias=None, rows=None, row_div=1, clamp_lo=-float("inf"),
+                     clamp_hi=float("inf"), out=None, out_dtype=None):
+    """The product with rows [offsets[e], offsets[e+1]) on expert e's weights
+    and bias [E, N].  ``rows`` [M] int32 with ``row_div``: row r reads
+    X[rows[r] // row_div] (slot_of_row and top_k: no sorted copy needed)."""
+    dt = _rows(X, "X")
+    _experts(blobs, offsets)
+    K = X.shape[1]
+    if rows is not None:
+        _ints(rows, "rows")
+    M = X.shape[0] if rows is None else rows.numel()
+    if out is None:
+        out = torch.empty((M, info.N), dtype=out_dtype or X.dtype, device=X.device)
+    odt = _rows(out, "out")
+    assert tuple(out.shape) == (M, info.N), "out must be [M, N]"
+    _f32(bias, "bias")
+    E = blobs.shape[0]
+    assert bias is None or bias.numel() == E * info.N, "bias must hold experts x N values"
+    _check(_lib.qgemm_w4_experts(_ptr(X), dt, X.shape[0], K, _ld(X), _ptr(rows), row_div, M,
+                                 C.byref(info), _ptr(blobs), blobs.stride(0), E, _ptr(offsets),
+                                 _ptr(bias), clamp_lo, clamp_hi, _ptr(out), odt, _ld(out),
+                                 _stream(X.device)), "qgemm_w4_experts")
+    return out
+
+
+def qgemm_w4_dx_ws_size(M: int, info: PackedInfo, experts=1) -> int:
+    n = C.c_size_t()
+    _check(_lib.qgemm_w4_dx_ws_size(M, C.byref(info), experts, C.byref(n)), "qgemm_w4_dx_ws_size")
+    return n.value
+
+
+def _dx_buffers(dY, info, experts, out, ws):
+    M, N = dY.shape
+    assert N == info.N, "dY must have N columns"
+    if out is None:
+        out = torch.empty((M, info.K), dtype=dY.dtype, device=dY.device)
+    assert tuple(out.shape) == (M, info.K) and out.dtype == dY.dtype, "out must be [M, K] like dY"
+    _rows(out, "out")
+    if ws is None:
+        n = qgemm_w4_dx_ws_size(M, info, experts)
+        ws = _alloc_bytes(n, dY.device) if n else None
+    return out, ws
+
+
+def qgemm_w4_blockwise_dx(dY: torch.Tensor, blob: torch.Tensor, info: PackedInfo, out=None,
+                          ws=None):
+    """The gradient of qgemm_w4_blockwise to its rows: dX = dY @ W."""
+    dt = _rows(dY, "dY")
+    out, ws = _dx_buffers(dY, info, 1, out, ws)
+    _check(_lib.qgemm_w4_blockwise_dx(_ptr(dY), dt, dY.shape[0], _ld(dY), C.byref(info), _ptr(blob),
+                                      _ptr(out), _ld(out), _ptr(ws),
+                                      0 if ws is None else ws.numel(), _stream(dY.device)),
+           "qgemm_w4_blockwise_dx")
+    return out
+
+
+def qgemm_w4_experts_dx(dY: torch.Tensor, blobs: torch.Tensor, info: PackedInfo,
+                        offsets: torch.Tensor, out=None, ws=None):
+    """The gradient of qgemm_w4_experts to its (sorted) rows."""
+    dt = _rows(dY, "dY")
+    _experts(blobs, offsets)
+    E = blobs.shape[0]
+    out, ws = _dx_buffers(dY, info, E, out, ws)
+    _check(_lib.qgemm_w4_experts_dx(_ptr(dY), dt, dY.shape[0], _ld(dY), C.byref(info), _ptr(blobs),
+                                    blobs.stride(0), E, _ptr(offsets), _ptr(out), _ld(out),
+                                    _ptr(ws), 0 if ws is None else ws.numel(),
+                                    _stream(dY.device)), "qgemm_w4_experts_dx")
+    return out
+
+
+# ---------------------------------------------------------------- rows by expert
+def _ids(ids):
+    assert ids.dim() == 2 and ids.dtype in (torch.int32, torch.int64) and \
+        (ids.stride(1) == 1 or ids.shape[1] == 1), \
+        "ids must be int32 or int64 [tokens, top_k] with unit column stride"
+    return QP_S32 if ids.dtype == torch.int32 else QP_S64
+
+
+def qmoe_sort_ws_size(T: int, top_k: int, experts: int) -> int:
+    n = C.c_size_t()
+    _check(_lib.qmoe_sort_ws_size(T, top_k, experts, C.byref(n)), "qmoe_sort_ws_size")
+    return n.value
+
+
+def _sort_buffers(ids, experts, ws):
+    T, k = ids.shape
+    dev = ids.device
+    if ws is None:
+        n = qmoe_sort_ws_size(T, k, experts)
+        ws = _alloc_bytes(n, dev) if n else None
+    return (torch.empty(experts + 1, dtype=torch.int32, device=dev),
+            torch.empty((T, k), dtype=torch.int32, device=dev),
+            torch.empty(T * k, dtype=torch.int32, device=dev), ws)
+
+
+def qmoe_sort(ids: torch.Tensor, experts: int, ws=None):
+    """Slots sorted by expert: (offsets [experts+1], row_of_slot [T, top_k],
+    slot_of_row [T*top_k]), int32; ids outside [0, experts) are dropped."""
+    idt = _ids(ids)
+    T, k = ids.shape
+    offsets, ros, sor, ws = _sort_buffers(ids, experts, ws)
+    _check(_lib.qmoe_sort(_ptr(ids), idt, T, k, _ld(ids), experts, _ptr(offsets), _ptr(ros),
+                          _ptr(sor), _ptr(ws), 0 if ws is None else ws.numel(),
+                          _stream(ids.device)), "qmoe_sort")
+    return offsets, ros, sor
+
+
+def qmoe_dispatch(X: torch.Tensor, ids: torch.Tensor, experts: int, out=None, ws=None):
+    """qmoe_sort and the rows of X [T, H] in sorted order: (Xs [T*top_k, H],
+    offsets, row_of_slot, slot_of_row)."""
+    dt, idt = _rows(X, "X"), _ids(ids)
+    T, k = ids.shape
+    H = X.shape[1]
+    assert X.shape[0] == T, "X and ids must have one row per token"
+    if out is None:
+        out = torch.empty((T * k, H), dtype=X.dtype, device=X.device)
+    assert tuple(out.shape) == (T * k, H) and _rows(out, "out") == dt, \
+        "out must be [T*top_k, H] of X's type"
+    offsets, ros, sor, ws = _sort_buffers(ids, experts, ws)
+    _check(_lib.qmoe_dispatch(_ptr(X), dt, H, _ld(X), _ptr(ids), idt, T, k, _ld(ids), experts,
+                              _ptr(out), _ld(out), _ptr(offsets), _ptr(ros), _ptr(sor), _ptr(ws),
+                              0 if ws is None else ws.numel(), _stream(X.device)),
+           "qmoe_dispatch")
+    return out, offsets, ros, sor
+
+
+def qmoe_dispatch_grad(dXs: torch.Tensor, row_of_slot: torch.Tensor, out=None):
+    """dX [T, H]: every token's sorted-row gradients summed."""
+    dt = _rows(dXs, "dXs")
+    _ints(row_of_slot, "row_of_slot")
+    T, k = row_of_slot.shape
+    H = dXs.shape[1]
+    assert dXs.shape[0] == T * k, "dXs must have a row per slot"
+    if out is None:
+        out = torch.empty((T, H), dtype=dXs.dtype, device=dXs.device)
+    assert tuple(out.shape) == (T, H) and _rows(out, "out") == dt, "out must be [T, H] like dXs"
+    _check(_lib.qmoe_dispatch_grad(_ptr(dXs), dt, T, k, H, _ld(dXs), _ptr(row_of_slot), _ptr(out),
+                                   _ld(out), _stream(dXs.device)), "qmoe_dispatch_grad")
+    return out
+
+
+def _combine_args(Z, row_of_slot, weights):
+    dt = _rows(Z, "Z")
+    _ints(row_of_slot, "row_of_slot")
+    T, k = row_of_slot.shape
+    assert Z.shape[0] == T * k, "Z must have a row per slot"
+    assert weights.dtype == torch.float32 and tuple(weights.shape) == (T, k) and \
+        (weights.stride(1) == 1 or k == 1), "weights must be float32 [T, top_k]"
+    return dt, T, k, Z.shape[1]
+
+
+def qmoe_combine(Z: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tensor, out=None):
+    """Y [T, H]: every token's rows of Z weighted and summed."""
+    dt, T, k, H = _combine_args(Z, row_of_slot, weights)
+    if out is None:
+        out = torch.empty((T, H), dtype=Z.dtype, device=Z.device)
+    assert tuple(out.shape) == (T, H) and _rows(out, "out") == dt, "out must be [T, H] like Z"
+    _check(_lib.qmoe_combine(_ptr(Z), dt, T, k, H, _ld(Z), _ptr(row_of_slot), _ptr(weights),
+                             _ld(weights), _ptr(out), _ld(out), _stream(Z.device)),
+           "qmoe_combine")
+    return out
+
+
+def qmoe_combine_grad(dY: torch.Tensor, Z: torch.Tensor, row_of_slot: torch.Tensor,
+                      slot_of_row: torch.Tensor, weights: torch.Tensor, out=None,
+                      out_weights=None):
+    """Gradients of qmoe_combine: (dZ [T*top_k, H], dweights f32 [T, top_k])."""
+    dt, T, k, H = _combine_args(Z, row_of_slot, weights)
+    assert _rows(dY, "dY") == dt and tuple(dY.shape) == (T, H), "dY must be [T, H] like Z"
+    _ints(slot_of_row, "slot_of_row")
+    assert slot_of_row.numel() == T * k, "slot_of_row must hold a value per slot"
+    if out is None:
+        out = torch.empty((T * k, H), dtype=Z.dtype, device=Z.device)
+    assert tuple(out.shape) == (T * k, H) and _rows(out, "out") == dt, "out must be like Z"
+    if out_weights is None:
+        out_weights = torch.empty((T, k), dtype=torch.float32, device=Z.device)
+    assert out_weights.dtype == torch.float32 and tuple(out_weights.shape) == (T, k) and \
+        (out_weights.stride(1) == 1 or k == 1), "out_weights must be float32 [T, top_k]"
+    _check(_lib.qmoe_combine_grad(_ptr(dY), _ld(dY), _ptr(Z), _ld(Z), dt, T, k, H,
+                                  _ptr(row_of_slot), _ptr(slot_of_row), _ptr(weights),
+                                  _ld(weights), _ptr(out), _ld(out), _ptr(out_weights),
+                                  _ld(out_weights), _stream(Z.device)), "qmoe_combine_grad")
+    return out, out_weights

@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libqpack.so")
 FLOORS_SRC = "floors.hip"
 FLOORS_LIB = os.path.join(HERE, "libqpfloors.so")
 SOURCES = ["status.cpp", "pack.hip", "quant.hip", "im2col.hip", "gemm_s8.hip", "conv.hip",
-           "conv_implicit.hip", "a8w4.hip", "a8w8b.hip", "unpack.hip"]
+           "conv_implicit.hip", "a8w4.hip", "a8w8b.hip", "unpack.hip", "moe.hip", "w4.hip",
+           "w4_dx.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
@@ -31,10 +32,12 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 
 
 # Per-file code-generation options.  The A8W4 kernels rescale every MFMA
-# result on the VALU right away, and the implicit-GEMM convolution keeps
-# few accumulators, so their MFMAs write VGPRs (no AGPR copies).
+# result on the VALU right away (the weight-only int4 products likewise), and
+# the implicit-GEMM convolution keeps few accumulators, so their MFMAs write
+# VGPRs (no AGPR copies).
 EXTRA = {"a8w4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"],
-         "conv_implicit.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]}
+         "conv_implicit.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"],
+         "w4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]}
 
 
 def _compile(src: str, obj: str) -> None:

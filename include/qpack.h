@@ -45,7 +45,16 @@ typedef enum {
   QP_EHIP = -6           /* the HIP runtime reported an error             */
 } qp_status;
 
-typedef enum { QP_S8 = 1, QP_S4 = 2, QP_S32 = 3, QP_F32 = 4 } qp_dtype;
+typedef enum {
+  QP_S8 = 1,
+  QP_S4 = 2,
+  QP_S32 = 3,
+  QP_F32 = 4,
+  /* rows of the float operators (qgemm_w4_*, qmoe_*) only */
+  QP_BF16 = 5,
+  QP_F16 = 6,
+  QP_S64 = 7 /* expert ids */
+} qp_dtype;
 
 typedef enum {
   QP_PER_TENSOR = 0,
@@ -546,6 +555,129 @@ qp_status qconv2d_s8_blockwise_f32(const qp_qtensor* x, const int8_t* X, const q
                                    int32_t pad_l, int32_t pad_b, int32_t pad_r, int32_t dil_h,
                                    int32_t dil_w, const float* bias_dev, float clamp_lo,
                                    float clamp_hi, float* Y, hipStream_t stream);
+
+/*
+ * qgemm_w4_blockwise -- Y = clamp(X x deq(W)^T + bias, lo, hi): float rows, not
+ * quantized, times packed int4 weights with group scales.
+ *   y[m,n] = sum_g s[n,g] sum_{k in g} x[m,k] q[n,k]
+ *            (+ o[n,g] sum_{k in g} x[m,k] for the asymmetric format)
+ *   with x in its own type (f32 rows keep f32 accuracy), q exact, f32 sums
+ *   and one rounding to y_dtype at the end; any M >= 0 from one token up.
+ *   X        device rows of `dtype` (QP_F32, QP_BF16 or QP_F16), [M][ldx],
+ *            ldx >= K, aligned to their elements only.
+ *   w, packedW_dev  an int4 blob from qpack_weights of any format and group
+ *            size (K must match).
+ *   bias     device f32 [N] or NULL, added before the clamp.
+ *   Y        device [M][ldy], ldy >= N, y_dtype = dtype or QP_F32.
+ * A row with an infinity or a NaN gives what the sum gives; other rows are
+ * not touched by it.  Run to run the same bits.
+ * Errors: QP_EINVAL on shapes, types, NaN or reversed bounds; QP_EALIGN.
+ */
+qp_status qgemm_w4_blockwise(const void* X, int32_t dtype, int64_t M, int64_t K, int64_t ldx,
+                             const qp_packed_info* w, const void* packedW_dev, const float* bias,
+                             float clamp_lo, float clamp_hi, void* Y, int32_t y_dtype, int64_t ldy,
+                             hipStream_t stream);
+
+/*
+ * qgemm_w4_experts -- the same product with the rows grouped by expert: rows
+ * [offsets[e], offsets[e+1]) use the weights and bias of expert e (as
+ * qmoe_sort orders them).  One launch; the counts stay on the device.
+ *   packedW_dev  expert e's blob at byte e*expert_stride, all described by
+ *            `w`; expert_stride a multiple of 256, >= w->total_bytes.
+ *   offsets  device int32 [experts+1], rising, offsets[0] = 0; values outside
+ *            [0, M] are taken as the nearest bound.  An expert may have no
+ *            rows.  Rows from offsets[experts] on are stored as zeros.
+ *   rows     device int32 [M] or NULL: row r reads row rows[r]/row_div of X
+ *            (with slot_of_row and row_div = top_k: tokens without a sorted
+ *            copy); where that is no row of X's x_rows rows, r reads zeros.
+ *            NULL: row r reads row r, and x_rows >= M.
+ *   bias     device f32 [experts][N] or NULL.
+ */
+qp_status qgemm_w4_experts(const void* X, int32_t dtype, int64_t x_rows, int64_t K, int64_t ldx,
+                           const int32_t* rows, int64_t row_div, int64_t M,
+                           const qp_packed_info* w, const void* packedW_dev, int64_t expert_stride,
+                           int64_t experts, const int32_t* offsets, const float* bias,
+                           float clamp_lo, float clamp_hi, void* Y, int32_t y_dtype, int64_t ldy,
+                           hipStream_t stream);
+
+/*
+ * qgemm_w4_blockwise_dx, qgemm_w4_experts_dx -- the products' gradients to
+ * their rows (without bias and clamp):
+ *   dX[m,k] = sum_n dY[m,n] * (s[n,g(k)] q[n,k] (+ o[n,g(k)]))
+ *   dY       device [M][lddy], lddy >= N;  dX  device [M][lddx], lddx >= K,
+ *            both of `dtype`.
+ *   offsets  as qgemm_w4_experts; rows of no expert get zeros.
+ *   ws       device workspace of qgemm_w4_dx_ws_size bytes (0: may be NULL),
+ *            256-byte aligned.  experts = 1 for the dense product.
+ * Each term dY * W is formed to within 2^-15 of itself (2^-22 for f32 rows),
+ * sums are f32.  A row of dY with an infinity or a NaN gives infinities or
+ * NaNs in that row of dX, not always which of the two the sum would give.
+ */
+qp_status qgemm_w4_dx_ws_size(int64_t M, const qp_packed_info* w, int64_t experts, size_t* bytes);
+qp_status qgemm_w4_blockwise_dx(const void* dY, int32_t dtype, int64_t M, int64_t lddy,
+                                const qp_packed_info* w, const void* packedW_dev, void* dX,
+                                int64_t lddx, void* ws, size_t ws_bytes, hipStream_t stream);
+qp_status qgemm_w4_experts_dx(const void* dY, int32_t dtype, int64_t M, int64_t lddy,
+                              const qp_packed_info* w, const void* packedW_dev,
+                              int64_t expert_stride, int64_t experts, const int32_t* offsets,
+                              void* dX, int64_t lddx, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+
+/*
+ * Rows of tokens sorted by expert and back.  T tokens choose top_k experts
+ * each; slot s = t*top_k + j is one choice.  A slot whose id is negative or
+ * >= experts is dropped.
+ *
+ * qmoe_sort -- the kept slots in (expert, slot) order are the rows:
+ *   ids          device int32 or int64 (ids_dtype QP_S32 or QP_S64) [T][ldids].
+ *   offsets      device int32 [experts+1]: the first row of every expert, and
+ *                the number of kept slots.
+ *   row_of_slot  device int32 [T*top_k], -1 for dropped slots.
+ *   slot_of_row  device int32 [T*top_k], -1 for the rows past the kept ones.
+ *   ws           device workspace of qmoe_sort_ws_size bytes (0 up to 2048
+ *                slots; then ws may be NULL).
+ *   At most 512 experts and 2^30 slots, else QP_EUNSUPPORTED.  T = 0 writes
+ *   offsets only.  Integer work: the same result in any run.
+ *
+ * qmoe_dispatch -- qmoe_sort, and Xs[r] = X[slot_of_row[r]/top_k] for every
+ *   row, zeros for the rows past the kept ones.
+ *   X   device rows of `dtype` (QP_F32, QP_BF16, QP_F16), [T][ldx];
+ *   Xs  device [T*top_k][ldxs].
+ *
+ * qmoe_dispatch_grad -- dX[t] = sum_j dXs[row_of_slot[t,j]] over kept slots.
+ *
+ * qmoe_combine -- Y[t] = sum_j weights[t,j] * Z[row_of_slot[t,j]] over kept
+ *   slots, in f32, j ascending, one rounding to `dtype`; a token without kept
+ *   slots gets zeros.  weights device f32 [T][ldw]; Z [T*top_k][ldz].
+ *
+ * qmoe_combine_grad -- dZ[row_of_slot[t,j]] = weights[t,j] * dY[t] (zeros for
+ *   rows without a slot) and dweights[t,j] = <dY[t], Z[row_of_slot[t,j]]>
+ *   (0 for dropped slots), f32 [T][lddw].
+ *
+ * Rows are aligned to their elements only; row maps outside [0, T*top_k) count
+ * as dropped.  What a dropped slot's weight or a row without a slot holds
+ * (NaN, infinities) has no effect.
+ */
+qp_status qmoe_sort_ws_size(int64_t T, int64_t top_k, int64_t experts, size_t* bytes);
+qp_status qmoe_sort(const void* ids, int32_t ids_dtype, int64_t T, int64_t top_k, int64_t ldids,
+                    int64_t experts, int32_t* offsets, int32_t* row_of_slot, int32_t* slot_of_row,
+                    void* ws, size_t ws_bytes, hipStream_t stream);
+qp_status qmoe_dispatch(const void* X, int32_t dtype, int64_t H, int64_t ldx, const void* ids,
+                        int32_t ids_dtype, int64_t T, int64_t top_k, int64_t ldids,
+                        int64_t experts, void* Xs, int64_t ldxs, int32_t* offsets,
+                        int32_t* row_of_slot, int32_t* slot_of_row, void* ws, size_t ws_bytes,
+                        hipStream_t stream);
+qp_status qmoe_dispatch_grad(const void* dXs, int32_t dtype, int64_t T, int64_t top_k, int64_t H,
+                             int64_t lddxs, const int32_t* row_of_slot, void* dX, int64_t lddx,
+                             hipStream_t stream);
+qp_status qmoe_combine(const void* Z, int32_t dtype, int64_t T, int64_t top_k, int64_t H,
+                       int64_t ldz, const int32_t* row_of_slot, const float* weights, int64_t ldw,
+                       void* Y, int64_t ldy, hipStream_t stream);
+qp_status qmoe_combine_grad(const void* dY, int64_t lddy, const void* Z, int64_t ldz,
+                            int32_t dtype, int64_t T, int64_t top_k, int64_t H,
+                            const int32_t* row_of_slot, const int32_t* slot_of_row,
+                            const float* weights, int64_t ldw, void* dZ, int64_t lddz,
+                            float* dweights, int64_t lddw, hipStream_t stream);
 
 #ifdef __cplusplus
 }
