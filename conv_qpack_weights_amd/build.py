@@ -23,7 +23,7 @@ FLOORS_SRC = "floors.hip"
 FLOORS_LIB = os.path.join(HERE, "libqpfloors.so")
 SOURCES = ["status.cpp", "pack.hip", "quant.hip", "im2col.hip", "gemm_s8.hip", "conv.hip",
            "conv_implicit.hip", "a8w4.hip", "a8w8b.hip", "unpack.hip", "moe.hip", "w4.hip",
-           "w4_dx.hip"]
+           "w4_f32.hip", "w4_bf16.hip", "w4_f16.hip", "w4_dx.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
@@ -37,7 +37,9 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 # VGPRs (no AGPR copies).
 EXTRA = {"a8w4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"],
          "conv_implicit.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"],
-         "w4.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]}
+         "w4_f32.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"],
+         "w4_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"],
+         "w4_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=true"]}
 
 
 def _compile(src: str, obj: str) -> None:

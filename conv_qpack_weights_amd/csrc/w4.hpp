@@ -208,7 +208,10 @@ __device__ __forceinline__ float nib_f32(uint32_t x) {
 // q/16 has at most four significant bits, so both types hold it exactly.
 template <typename V>
 __device__ __forceinline__ V w4_unpack(uint32_t w) {
-  const uint32_t h = w >> 4;
+  uint32_t h = w >> 4;
+  // (kept as one shift: the compiler would shift out each high nibble instead
+  // of selecting bytes inside the conversion)
+  asm("" : "+v"(h));
   float f[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -237,7 +240,41 @@ __device__ __forceinline__ void w4_store(void* Y, int32_t dtype, int64_t at, flo
     static_cast<f16_t*>(Y)[at] = from_f32<f16_t>(y);
 }
 
+// The first n of eight neighbouring outputs.
+__device__ __forceinline__ void w4_store8(void* Y, int32_t dtype, int64_t at, const float (&y)[8],
+                                          int n) {
+  if (dtype == QP_F32) {
+    float* p = static_cast<float*>(Y) + at;
+    const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
+    store_piece(p, lo, n);
+    if (n > 4) store_piece(p + 4, hi, n - 4);
+  } else if (dtype == QP_BF16) {
+    store_piece(static_cast<bf16_t*>(Y) + at, y, n);
+  } else {
+    store_piece(static_cast<f16_t*>(Y) + at, y, n);
+  }
+}
+
+struct W4Args {
+  W4View w;
+  W4Rows rows;
+  const void* X;
+  int64_t ldx;
+  const float* bias;   // [experts][N] or null
+  float lo, hi;
+  void* Y;
+  int32_t y_dtype;
+  int64_t ldy;
+};
+
 // ---- host side -------------------------------------------------------------
+// The shapes of the kernels (16-row fragments, 16-channel tiles of a workgroup),
+// see w4_choose.
+enum W4Shape { kRows1x1, kRows1x2, kRows1x3, kRows1x4, kRows2x3, kRows2x4, kTile4x8, kTile8x8 };
+qp_status run_w4_f32(const W4Args& a, int32_t format, W4Shape shape, hipStream_t stream);
+qp_status run_w4_bf16(const W4Args& a, int32_t format, W4Shape shape, hipStream_t stream);
+qp_status run_w4_f16(const W4Args& a, int32_t format, W4Shape shape, hipStream_t stream);
+
 W4View w4_view(const qp_packed_info* w, const void* packed, int64_t expert_stride);
 qp_status w4_check_weights(const char* what, const qp_packed_info* w, const void* packed,
                            int64_t experts, int64_t expert_stride);

@@ -1,0 +1,8 @@
+// w4_f32.hip -- the weight-only int4 products' kernels for f32 rows.
+#include "w4_kernels.hpp"
+
+namespace qp {
+qp_status run_w4_f32(const W4Args& a, int32_t format, W4Shape shape, hipStream_t stream) {
+  return run_w4_type<float>(a, format, shape, stream);
+}
+}  // namespace qp
