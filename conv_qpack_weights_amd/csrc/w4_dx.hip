@@ -642,7 +642,8 @@ DxPlan dx_plan(int64_t M, int64_t experts, int64_t N, int64_t K) {
 double dx_tile_cost(int64_t M, int64_t experts, int64_t N, int64_t K) {
   const double groups = dx_row_tiles(M, experts, 128) * (double)ceil_div(K, 256);
   const double pairs = (double)(int64_t)(groups / 512.0), rest = groups - pairs * 512.0;
-  return (pairs * 255.0 + (rest <= 0.0 ? 0.0 : rest <= 256.0 ? 155.0 : 255.0)) * (double)N / 4096.0;
+  return 3.0 +
+         (pairs * 255.0 + (rest <= 0.0 ? 0.0 : rest <= 256.0 ? 155.0 : 255.0)) * (double)N / 4096.0;
 }
 
 int64_t dx_ws_bytes(int64_t M, int64_t experts, int64_t N, int64_t K) {

@@ -117,6 +117,40 @@ def test_larger_shapes(qp, dtype, M, N, K, group):
            dtype, "dx", 2.0 ** -22 if dtype == "f32" else 2.0 ** -15)
 
 
+# the kernels for many rows: 128-row tiles, cut at every edge
+@pytest.mark.parametrize("dtype,kind,group,counts,N,K", [
+    ("bf16", "f32", 32, [700, 0, 1300, 129], 1100, 1090),
+    ("f16", "f32", 128, [700, 0, 1300, 129], 1100, 1090),
+    ("bf16", "asym", 64, [513, 1000], 1030, 1217),
+    ("bf16", "bf16", 32, [2100, 1, 1900], 517, 4100),
+    ("f32", "f32", 32, [600, 90], 300, 700)])
+def test_many_rows(qp, dtype, kind, group, counts, N, K):
+    import torch
+    E, M = len(counts), sum(counts) + 3
+    c = Case(qp, E, N, K, group, kind)
+    print("w4 many rows", dtype, kind, group, counts, N, K, flush=True)
+    first = np.concatenate([[0], np.cumsum(counts)])
+    offsets = torch.tensor(first, dtype=torch.int32).cuda()
+    perm = c.rng.permutation(M).astype(np.int32)
+    X, x = c.rows(M, K, dtype)
+    dY, dy = c.rows(M, N, dtype)
+    asym = 0.04 if kind == "asym" else 0.0   # q and the offset are summed apart
+    want, A = np.zeros((M, N)), np.zeros((M, N))
+    wmap, Amap = np.zeros((M, N)), np.zeros((M, N))
+    dwant, dA = np.zeros((M, K)), np.zeros((M, K))
+    for e in range(E):
+        r = slice(first[e], first[e + 1])
+        W, aW = c.W[e], np.abs(c.W[e])
+        want[r], A[r] = x[r] @ W.T, np.abs(x[r]) @ (aW + asym).T
+        wmap[r], Amap[r] = x[perm[r]] @ W.T, np.abs(x[perm[r]]) @ (aW + asym).T
+        dwant[r], dA[r] = dy[r] @ W, np.abs(dy[r]) @ aW
+    _close(qp.qgemm_w4_experts(X, c.blobs, c.info, offsets), want, A, K, dtype, "y")
+    _close(qp.qgemm_w4_experts(X, c.blobs, c.info, offsets, rows=torch.from_numpy(perm).cuda()),
+           wmap, Amap, K, dtype, "y through the map")
+    _close(qp.qgemm_w4_experts_dx(dY, c.blobs, c.info, offsets), dwant, dA, N, dtype, "dx",
+           2.0 ** -22 if dtype == "f32" else 2.0 ** -15)
+
+
 COUNTS = [
     [0, 0, 5, 0],              # one expert with rows
     [1, 1, 1, 1],
