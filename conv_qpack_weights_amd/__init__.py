@@ -630,24 +630,24 @@ _FLOAT = {torch.float32: QP_F32, torch.bfloat16: QP_BF16, torch.float16: QP_F16}
 
 
 def _rows(t, what):
+    """The type's number, the shape and the row stride of a tensor of rows."""
     dt = _FLOAT.get(t.dtype)
-    assert dt is not None and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1), \
-        "%s: rows must be 2-D float32, bfloat16 or float16 with unit column stride" % what
-    return dt
-
-
-def _out(t, shape, dtype, like, what):
-    """The output `t` checked, or a new one; with its type's number."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device), _FLOAT[dtype]
-    assert tuple(t.shape) == shape, "%s must have the shape %s" % (what, list(shape))
-    return t, _rows(t, what)
-
-
-def _ld(t):
+    assert dt is not None and t.dim() == 2, "%s: rows must be 2-D float32, bfloat16 or float16" % what
+    M, n = t.shape
+    ld, one = t.stride()
+    assert one == 1 or n == 1, "%s: rows must have unit column stride" % what
     # the stride of a single row means nothing to torch; the library wants at
     # least the columns.  Several rows keep theirs (a broadcast one is refused).
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return dt, M, n, ld if M > 1 else max(ld, n)
+
+
+def _out(t, M, n, dtype, like, what):
+    """The output `t` checked, or a new one; its type's number and row stride."""
+    if t is None:
+        return torch.empty((M, n), dtype=dtype, device=like.device), _FLOAT[dtype], n
+    dt, m, k, ld = _rows(t, what)
+    assert m == M and k == n, "%s must have the shape [%d, %d]" % (what, M, n)
+    return t, dt, ld
 
 
 def _ints(t, what, dtype=torch.int32):
@@ -682,14 +682,14 @@ def qgemm_w4_blockwise(X: torch.Tensor, blob: torch.Tensor, info: PackedInfo, bi
                        clamp_lo=-float("inf"), clamp_hi=float("inf"), out=None, out_dtype=None):
     """Y = clamp(X @ W^T + bias): float rows (f32, bf16 or f16, not quantized)
     times an int4 blob; outputs in X's type or `out_dtype` float32."""
-    dt = _rows(X, "X")
-    M, K = X.shape
-    out, odt = _out(out, (M, info.N), out_dtype or X.dtype, X, "out")
-    _f32(bias, "bias")
-    assert bias is None or bias.numel() == info.N, "bias must hold N values"
-    _check(_lib.qgemm_w4_blockwise(_ptr(X), dt, M, K, _ld(X), C.byref(info), _ptr(blob), _ptr(bias),
-                                   clamp_lo, clamp_hi, _ptr(out), odt, _ld(out),
-                                   _stream_of(X)), "qgemm_w4_blockwise")
+    dt, M, K, ldx = _rows(X, "X")
+    out, odt, ldy = _out(out, M, info.N, out_dtype or X.dtype, X, "out")
+    if bias is not None:
+        _f32(bias, "bias")
+        assert bias.numel() == info.N, "bias must hold N values"
+    _check(_lib.qgemm_w4_blockwise(_ptr(X), dt, M, K, ldx, C.byref(info), _ptr(blob), _ptr(bias),
+                                   clamp_lo, clamp_hi, _ptr(out), odt, ldy, _stream_of(X)),
+           "qgemm_w4_blockwise")
     return out
 
 
@@ -697,7 +697,9 @@ def _experts(blobs, offsets):
     assert blobs.dim() == 2 and blobs.dtype == torch.uint8 and blobs.stride(1) == 1, \
         "blobs must be uint8 [experts, bytes] (pack_s4_experts)"
     _ints(offsets, "offsets")
-    assert offsets.numel() == blobs.shape[0] + 1, "offsets must hold experts + 1 values"
+    E = blobs.shape[0]
+    assert offsets.numel() == E + 1, "offsets must hold experts + 1 values"
+    return E
 
 
 def qgemm_w4_experts(X: torch.Tensor, blobs: torch.Tensor, info: PackedInfo, offsets: torch.Tensor,
@@ -706,19 +708,19 @@ def qgemm_w4_experts(X: torch.Tensor, blobs: torch.Tensor, info: PackedInfo, off
     """The product with rows [offsets[e], offsets[e+1]) on expert e's weights
     and bias [E, N].  ``rows`` [M] int32 with ``row_div``: row r reads
     X[rows[r] // row_div] (slot_of_row and top_k: no sorted copy needed)."""
-    dt = _rows(X, "X")
-    _experts(blobs, offsets)
-    K = X.shape[1]
+    dt, x_rows, K, ldx = _rows(X, "X")
+    E = _experts(blobs, offsets)
+    M = x_rows
     if rows is not None:
         _ints(rows, "rows")
-    M = X.shape[0] if rows is None else rows.numel()
-    out, odt = _out(out, (M, info.N), out_dtype or X.dtype, X, "out")
-    _f32(bias, "bias")
-    E = blobs.shape[0]
-    assert bias is None or bias.numel() == E * info.N, "bias must hold experts x N values"
-    _check(_lib.qgemm_w4_experts(_ptr(X), dt, X.shape[0], K, _ld(X), _ptr(rows), row_div, M,
+        M = rows.numel()
+    out, odt, ldy = _out(out, M, info.N, out_dtype or X.dtype, X, "out")
+    if bias is not None:
+        _f32(bias, "bias")
+        assert bias.numel() == E * info.N, "bias must hold experts x N values"
+    _check(_lib.qgemm_w4_experts(_ptr(X), dt, x_rows, K, ldx, _ptr(rows), row_div, M,
                                  C.byref(info), _ptr(blobs), blobs.stride(0), E, _ptr(offsets),
-                                 _ptr(bias), clamp_lo, clamp_hi, _ptr(out), odt, _ld(out),
+                                 _ptr(bias), clamp_lo, clamp_hi, _ptr(out), odt, ldy,
                                  _stream_of(X)), "qgemm_w4_experts")
     return out
 
@@ -730,48 +732,45 @@ def qgemm_w4_dx_ws_size(M: int, info: PackedInfo, experts=1) -> int:
 
 
 def _dx_buffers(dY, info, experts, out, ws):
-    M, N = dY.shape
+    dt, M, N, lddy = _rows(dY, "dY")
     assert N == info.N, "dY must have N columns"
-    out, _ = _out(out, (M, info.K), dY.dtype, dY, "out")
-    assert out.dtype == dY.dtype, "out must be of dY's type"
+    out, odt, lddx = _out(out, M, info.K, dY.dtype, dY, "out")
+    assert odt == dt, "out must be of dY's type"
     if ws is None:
         n = qgemm_w4_dx_ws_size(M, info, experts)
         ws = _alloc_bytes(n, dY.device) if n else None
-    return out, ws
+    return dt, M, lddy, out, lddx, ws, 0 if ws is None else ws.numel()
 
 
 def qgemm_w4_blockwise_dx(dY: torch.Tensor, blob: torch.Tensor, info: PackedInfo, out=None,
                           ws=None):
     """The gradient of qgemm_w4_blockwise to its rows: dX = dY @ W."""
-    dt = _rows(dY, "dY")
-    out, ws = _dx_buffers(dY, info, 1, out, ws)
-    _check(_lib.qgemm_w4_blockwise_dx(_ptr(dY), dt, dY.shape[0], _ld(dY), C.byref(info), _ptr(blob),
-                                      _ptr(out), _ld(out), _ptr(ws),
-                                      0 if ws is None else ws.numel(), _stream_of(dY)),
-           "qgemm_w4_blockwise_dx")
+    dt, M, lddy, out, lddx, ws, n = _dx_buffers(dY, info, 1, out, ws)
+    _check(_lib.qgemm_w4_blockwise_dx(_ptr(dY), dt, M, lddy, C.byref(info), _ptr(blob), _ptr(out),
+                                      lddx, _ptr(ws), n, _stream_of(dY)), "qgemm_w4_blockwise_dx")
     return out
 
 
 def qgemm_w4_experts_dx(dY: torch.Tensor, blobs: torch.Tensor, info: PackedInfo,
                         offsets: torch.Tensor, out=None, ws=None):
     """The gradient of qgemm_w4_experts to its (sorted) rows."""
-    dt = _rows(dY, "dY")
-    _experts(blobs, offsets)
-    E = blobs.shape[0]
-    out, ws = _dx_buffers(dY, info, E, out, ws)
-    _check(_lib.qgemm_w4_experts_dx(_ptr(dY), dt, dY.shape[0], _ld(dY), C.byref(info), _ptr(blobs),
-                                    blobs.stride(0), E, _ptr(offsets), _ptr(out), _ld(out),
-                                    _ptr(ws), 0 if ws is None else ws.numel(),
+    E = _experts(blobs, offsets)
+    dt, M, lddy, out, lddx, ws, n = _dx_buffers(dY, info, E, out, ws)
+    _check(_lib.qgemm_w4_experts_dx(_ptr(dY), dt, M, lddy, C.byref(info), _ptr(blobs),
+                                    blobs.stride(0), E, _ptr(offsets), _ptr(out), lddx, _ptr(ws), n,
                                     _stream_of(dY)), "qgemm_w4_experts_dx")
     return out
 
 
 # ---------------------------------------------------------------- rows by expert
 def _ids(ids):
-    assert ids.dim() == 2 and ids.dtype in (torch.int32, torch.int64) and \
-        (ids.stride(1) == 1 or ids.shape[1] == 1), \
-        "ids must be int32 or int64 [tokens, top_k] with unit column stride"
-    return QP_S32 if ids.dtype == torch.int32 else QP_S64
+    """The type's number, tokens, choices and token stride of the ids."""
+    assert ids.dim() == 2 and ids.dtype in (torch.int32, torch.int64), \
+        "ids must be int32 or int64 [tokens, top_k]"
+    T, k = ids.shape
+    ld, one = ids.stride()
+    assert one == 1 or k == 1, "ids must have unit column stride"
+    return QP_S32 if ids.dtype == torch.int32 else QP_S64, T, k, ld if T > 1 else max(ld, k)
 
 
 def qmoe_sort_ws_size(T: int, top_k: int, experts: int) -> int:
@@ -780,78 +779,72 @@ def qmoe_sort_ws_size(T: int, top_k: int, experts: int) -> int:
     return n.value
 
 
-def _sort_buffers(ids, experts, ws):
-    T, k = ids.shape
-    dev = ids.device
+def _sort_buffers(ids, T, k, experts, ws):
+    """Offsets, row of slot, slot of row (one allocation) and the workspace."""
+    S = T * k
     if ws is None:
         n = qmoe_sort_ws_size(T, k, experts)
-        ws = _alloc_bytes(n, dev) if n else None
-    return (torch.empty(experts + 1, dtype=torch.int32, device=dev),
-            torch.empty((T, k), dtype=torch.int32, device=dev),
-            torch.empty(T * k, dtype=torch.int32, device=dev), ws)
+        ws = _alloc_bytes(n, ids.device) if n else None
+    offsets, ros, sor = torch.empty(experts + 1 + 2 * S, dtype=torch.int32,
+                                    device=ids.device).split_with_sizes((experts + 1, S, S))
+    return offsets, ros.view(T, k), sor, ws, 0 if ws is None else ws.numel()
 
 
 def qmoe_sort(ids: torch.Tensor, experts: int, ws=None):
     """Slots sorted by expert: (offsets [experts+1], row_of_slot [T, top_k],
     slot_of_row [T*top_k]), int32; ids outside [0, experts) are dropped."""
-    idt = _ids(ids)
-    T, k = ids.shape
-    offsets, ros, sor, ws = _sort_buffers(ids, experts, ws)
-    _check(_lib.qmoe_sort(_ptr(ids), idt, T, k, _ld(ids), experts, _ptr(offsets), _ptr(ros),
-                          _ptr(sor), _ptr(ws), 0 if ws is None else ws.numel(),
-                          _stream_of(ids)), "qmoe_sort")
+    idt, T, k, ldi = _ids(ids)
+    offsets, ros, sor, ws, n = _sort_buffers(ids, T, k, experts, ws)
+    _check(_lib.qmoe_sort(_ptr(ids), idt, T, k, ldi, experts, _ptr(offsets), _ptr(ros), _ptr(sor),
+                          _ptr(ws), n, _stream_of(ids)), "qmoe_sort")
     return offsets, ros, sor
 
 
 def qmoe_dispatch(X: torch.Tensor, ids: torch.Tensor, experts: int, out=None, ws=None):
     """qmoe_sort and the rows of X [T, H] in sorted order: (Xs [T*top_k, H],
     offsets, row_of_slot, slot_of_row)."""
-    dt, idt = _rows(X, "X"), _ids(ids)
-    T, k = ids.shape
-    H = X.shape[1]
-    assert X.shape[0] == T, "X and ids must have one row per token"
-    out, odt = _out(out, (T * k, H), X.dtype, X, "out")
+    dt, M, H, ldx = _rows(X, "X")
+    idt, T, k, ldi = _ids(ids)
+    assert M == T, "X and ids must have one row per token"
+    out, odt, ldo = _out(out, T * k, H, X.dtype, X, "out")
     assert odt == dt, "out must be of X's type"
-    offsets, ros, sor, ws = _sort_buffers(ids, experts, ws)
-    _check(_lib.qmoe_dispatch(_ptr(X), dt, H, _ld(X), _ptr(ids), idt, T, k, _ld(ids), experts,
-                              _ptr(out), _ld(out), _ptr(offsets), _ptr(ros), _ptr(sor), _ptr(ws),
-                              0 if ws is None else ws.numel(), _stream_of(X)),
-           "qmoe_dispatch")
+    offsets, ros, sor, ws, n = _sort_buffers(ids, T, k, experts, ws)
+    _check(_lib.qmoe_dispatch(_ptr(X), dt, H, ldx, _ptr(ids), idt, T, k, ldi, experts, _ptr(out),
+                              ldo, _ptr(offsets), _ptr(ros), _ptr(sor), _ptr(ws), n,
+                              _stream_of(X)), "qmoe_dispatch")
     return out, offsets, ros, sor
 
 
 def qmoe_dispatch_grad(dXs: torch.Tensor, row_of_slot: torch.Tensor, out=None):
     """dX [T, H]: every token's sorted-row gradients summed."""
-    dt = _rows(dXs, "dXs")
+    dt, S, H, ld = _rows(dXs, "dXs")
     _ints(row_of_slot, "row_of_slot")
     T, k = row_of_slot.shape
-    H = dXs.shape[1]
-    assert dXs.shape[0] == T * k, "dXs must have a row per slot"
-    out, odt = _out(out, (T, H), dXs.dtype, dXs, "out")
+    assert S == T * k, "dXs must have a row per slot"
+    out, odt, ldo = _out(out, T, H, dXs.dtype, dXs, "out")
     assert odt == dt, "out must be of dXs's type"
-    _check(_lib.qmoe_dispatch_grad(_ptr(dXs), dt, T, k, H, _ld(dXs), _ptr(row_of_slot), _ptr(out),
-                                   _ld(out), _stream_of(dXs)), "qmoe_dispatch_grad")
+    _check(_lib.qmoe_dispatch_grad(_ptr(dXs), dt, T, k, H, ld, _ptr(row_of_slot), _ptr(out), ldo,
+                                   _stream_of(dXs)), "qmoe_dispatch_grad")
     return out
 
 
 def _combine_args(Z, row_of_slot, weights):
-    dt = _rows(Z, "Z")
+    dt, S, H, ldz = _rows(Z, "Z")
     _ints(row_of_slot, "row_of_slot")
     T, k = row_of_slot.shape
-    assert Z.shape[0] == T * k, "Z must have a row per slot"
-    assert weights.dtype == torch.float32 and tuple(weights.shape) == (T, k) and \
-        (weights.stride(1) == 1 or k == 1), "weights must be float32 [T, top_k]"
-    return dt, T, k, Z.shape[1]
+    assert S == T * k, "Z must have a row per slot"
+    wdt, m, n, ldw = _rows(weights, "weights")
+    assert wdt == QP_F32 and m == T and n == k, "weights must be float32 [T, top_k]"
+    return dt, T, k, H, ldz, ldw
 
 
 def qmoe_combine(Z: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tensor, out=None):
     """Y [T, H]: every token's rows of Z weighted and summed."""
-    dt, T, k, H = _combine_args(Z, row_of_slot, weights)
-    out, odt = _out(out, (T, H), Z.dtype, Z, "out")
+    dt, T, k, H, ldz, ldw = _combine_args(Z, row_of_slot, weights)
+    out, odt, ldo = _out(out, T, H, Z.dtype, Z, "out")
     assert odt == dt, "out must be of Z's type"
-    _check(_lib.qmoe_combine(_ptr(Z), dt, T, k, H, _ld(Z), _ptr(row_of_slot), _ptr(weights),
-                             _ld(weights), _ptr(out), _ld(out), _stream_of(Z)),
-           "qmoe_combine")
+    _check(_lib.qmoe_combine(_ptr(Z), dt, T, k, H, ldz, _ptr(row_of_slot), _ptr(weights), ldw,
+                             _ptr(out), ldo, _stream_of(Z)), "qmoe_combine")
     return out
 
 
@@ -859,18 +852,16 @@ def qmoe_combine_grad(dY: torch.Tensor, Z: torch.Tensor, row_of_slot: torch.Tens
                       slot_of_row: torch.Tensor, weights: torch.Tensor, out=None,
                       out_weights=None):
     """Gradients of qmoe_combine: (dZ [T*top_k, H], dweights f32 [T, top_k])."""
-    dt, T, k, H = _combine_args(Z, row_of_slot, weights)
-    assert _rows(dY, "dY") == dt and tuple(dY.shape) == (T, H), "dY must be [T, H] like Z"
+    dt, T, k, H, ldz, ldw = _combine_args(Z, row_of_slot, weights)
+    gdt, m, n, lddy = _rows(dY, "dY")
+    assert gdt == dt and m == T and n == H, "dY must be [T, H] like Z"
     _ints(slot_of_row, "slot_of_row")
     assert slot_of_row.numel() == T * k, "slot_of_row must hold a value per slot"
-    out, odt = _out(out, (T * k, H), Z.dtype, Z, "out")
+    out, odt, ldo = _out(out, T * k, H, Z.dtype, Z, "out")
     assert odt == dt, "out must be of Z's type"
-    if out_weights is None:
-        out_weights = torch.empty((T, k), dtype=torch.float32, device=Z.device)
-    assert out_weights.dtype == torch.float32 and tuple(out_weights.shape) == (T, k) and \
-        (out_weights.stride(1) == 1 or k == 1), "out_weights must be float32 [T, top_k]"
-    _check(_lib.qmoe_combine_grad(_ptr(dY), _ld(dY), _ptr(Z), _ld(Z), dt, T, k, H,
-                                  _ptr(row_of_slot), _ptr(slot_of_row), _ptr(weights),
-                                  _ld(weights), _ptr(out), _ld(out), _ptr(out_weights),
-                                  _ld(out_weights), _stream_of(Z)), "qmoe_combine_grad")
+    out_weights, wdt, lddw = _out(out_weights, T, k, torch.float32, Z, "out_weights")
+    assert wdt == QP_F32, "out_weights must be float32"
+    _check(_lib.qmoe_combine_grad(_ptr(dY), lddy, _ptr(Z), ldz, dt, T, k, H, _ptr(row_of_slot),
+                                  _ptr(slot_of_row), _ptr(weights), ldw, _ptr(out), ldo,
+                                  _ptr(out_weights), lddw, _stream_of(Z)), "qmoe_combine_grad")
     return out, out_weights

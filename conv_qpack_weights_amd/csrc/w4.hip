@@ -24,8 +24,8 @@ struct ShapeCost {
   double first, more;
 };
 constexpr ShapeCost kShapes[] = {
-    {kRows1x1, 1, 1, 7.5, 4.1},  {kRows1x2, 1, 2, 8.5, 4.9},   {kRows1x3, 1, 3, 10.8, 6.1},
-    {kRows1x4, 1, 4, 11.5, 6.5}, {kRows2x3, 2, 3, 14.3, 10.4}, {kRows2x4, 2, 4, 15.0, 12.1},
+    {kRows1x1, 1, 1, 7.5, 4.1},   {kRows1x2, 1, 2, 8.4, 4.8},   {kRows1x3, 1, 3, 9.5, 5.6},
+    {kRows1x4, 1, 4, 10.3, 6.5},  {kRows2x3, 2, 3, 13.2, 11.0}, {kRows2x4, 2, 4, 14.4, 12.1},
     {kTile4x8, 4, 8, 42.0, 21.7}, {kTile8x8, 8, 8, 59.0, 42.0},
 };
 
@@ -49,9 +49,7 @@ W4Shape w4_choose(const W4Args& a, int32_t dtype) {
     }
     const double groups = tiles * (double)ceil_div(a.w.Npad / 16, s.tiles);
     const double rounds = groups <= 256.0 ? 0.0 : (double)(int64_t)((groups + 255.0) / 256.0) - 1.0;
-    // a single row is one line of X for all the lanes
-    const double more = s.shape == kRows1x1 && a.rows.M == 1 ? 2.0 : s.more;
-    const double cost = s.first + more * rounds;
+    const double cost = s.first + s.more * rounds;
     if (cost < least) {
       least = cost;
       best = s.shape;

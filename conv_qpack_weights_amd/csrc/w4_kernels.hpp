@@ -120,14 +120,22 @@ __device__ __forceinline__ void w4_step(const W4Stage<T, kKind, kFM, kTiles>& st
 // nobody else's, so LDS would only add a hop), and the waves' sums meet in LDS
 // in a fixed order.
 template <typename T, int kKind, bool kOne, int kFM, int kTiles, int kWaves, int kAhead>
-__global__ __launch_bounds__(kWaves * 64) void w4_rows_kernel(W4Args a, uint32_t col_groups) {
+__global__ __launch_bounds__(kWaves * 64) void w4_rows_kernel(W4Args a, uint32_t row_slots) {
   __shared__ f32x4 red[kWaves][kFM * kTiles][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t slot = blockIdx.x / col_groups;
+  // Workgroups go round the 8 XCDs in launch order: give each XCD a run of
+  // tiles with the row tiles of a channel group next to each other, so that an
+  // expert's weights cross the fabric once for all its row tiles.
+  uint32_t id = blockIdx.x;
+  {
+    const uint32_t n = gridDim.x, per = n / 8, rest = n % 8, x = id % 8;
+    id = x * per + (x < rest ? x : rest) + id / 8;
+  }
+  const uint32_t group = id / row_slots, slot = id - group * row_slots;
   const W4Tile tile = w4_find_tile<16 * kFM>(a.rows, slot);
   if (tile.expert < 0) return;
-  const int64_t n0 = (int64_t)(blockIdx.x - slot * col_groups) * kTiles * 16;
+  const int64_t n0 = (int64_t)group * kTiles * 16;
   if (a.rows.offsets && tile.expert == a.rows.experts) {  // rows of no expert
     for (int64_t i = threadIdx.x; i < (tile.r1 - tile.r0) * 16 * kTiles; i += kWaves * 64) {
       const int64_t r = tile.r0 + i / (16 * kTiles), n = n0 + i % (16 * kTiles);
@@ -186,14 +194,18 @@ __global__ __launch_bounds__(kWaves * 64) void w4_rows_kernel(W4Args a, uint32_t
     Stage st[kAhead];
 #pragma unroll
     for (int p = 0; p < kAhead; ++p) load(st[p], b0 + p < b1 ? b0 + p : b1 - 1);
-    for (int64_t b = b0; b < b1; b += kAhead) {
+    int64_t b = b0;
+    for (; b + kAhead < b1; b += kAhead) {
 #pragma unroll
       for (int p = 0; p < kAhead; ++p) {
-        if (b + p < b1) w4_step<T, kKind, kOne, kFM, kTiles>(st[p], acc);
+        w4_step<T, kKind, kOne, kFM, kTiles>(st[p], acc);
         const int64_t nb = b + p + kAhead;
         load(st[p], nb < b1 ? nb : b1 - 1);
       }
     }
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p)  // (no load behind a branch: its join would wait)
+      if (b + p < b1) w4_step<T, kKind, kOne, kFM, kTiles>(st[p], acc);
   }
   if (wave == kWaves - 1 && full * 128 < a.w.K) {
     Stage st;
@@ -239,7 +251,7 @@ qp_status launch_rows(const W4Args& a, hipStream_t stream) {
              "qgemm_w4: more than 2^31 workgroups");
   hipLaunchKernelGGL((w4_rows_kernel<T, kKind, kOne, kFM, kTiles, kWaves, kAhead>),
                      dim3((unsigned)(slots * groups)), dim3(kWaves * 64), 0, stream, a,
-                     (uint32_t)groups);
+                     (uint32_t)slots);
   return check_launch("qgemm_w4 (few rows)");
 }
 
