@@ -9,6 +9,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -644,7 +645,8 @@ def _rows(t, what):
 def _out(t, M, n, dtype, like, what):
     """The output `t` checked, or a new one; its type's number and row stride."""
     if t is None:
-        return torch.empty((M, n), dtype=dtype, device=like.device), _FLOAT[dtype], n
+        t = like.new_empty((M, n)) if dtype is like.dtype else like.new_empty((M, n), dtype=dtype)
+        return t, _FLOAT[dtype], n
     dt, m, k, ld = _rows(t, what)
     assert m == M and k == n, "%s must have the shape [%d, %d]" % (what, M, n)
     return t, dt, ld
@@ -773,6 +775,7 @@ def _ids(ids):
     return QP_S32 if ids.dtype == torch.int32 else QP_S64, T, k, ld if T > 1 else max(ld, k)
 
 
+@functools.lru_cache(maxsize=256)
 def qmoe_sort_ws_size(T: int, top_k: int, experts: int) -> int:
     n = C.c_size_t()
     _check(_lib.qmoe_sort_ws_size(T, top_k, experts, C.byref(n)), "qmoe_sort_ws_size")
@@ -785,8 +788,8 @@ def _sort_buffers(ids, T, k, experts, ws):
     if ws is None:
         n = qmoe_sort_ws_size(T, k, experts)
         ws = _alloc_bytes(n, ids.device) if n else None
-    offsets, ros, sor = torch.empty(experts + 1 + 2 * S, dtype=torch.int32,
-                                    device=ids.device).split_with_sizes((experts + 1, S, S))
+    offsets, ros, sor = ids.new_empty(experts + 1 + 2 * S, dtype=torch.int32).split_with_sizes(
+        (experts + 1, S, S))
     return offsets, ros.view(T, k), sor, ws, 0 if ws is None else ws.numel()
 
 

@@ -65,22 +65,25 @@ struct Piece {
   }
 };
 
-// The n <= 16/sizeof(T) elements at p; the rest of the piece is zero.
+// The first n elements at p (none for n <= 0), the rest of the piece zero; p[0]
+// must be readable in any case.  A cut piece's elements are loaded without a
+// branch each, so that they come in together.
 template <typename T>
 __device__ __forceinline__ Piece<T> load_piece(const T* p, int n) {
   Piece<T> r;
   if (n >= Piece<T>::kPer) {
     r.v = *reinterpret_cast<const u32x4_any*>(p);
   } else {
+    T e[Piece<T>::kPer];
+#pragma unroll
+    for (int i = 0; i < Piece<T>::kPer; ++i) e[i] = p[i < n ? i : 0];
     r.v = typename Piece<T>::vec{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < Piece<T>::kPer; ++i) {
-      if (i < n) {
-        if constexpr (sizeof(T) == 4)
-          r.v[i] = __builtin_bit_cast(uint32_t, p[i]);
-        else
-          r.v[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[i]) << (16 * (i & 1));
-      }
+      if constexpr (sizeof(T) == 4)
+        r.v[i] = i < n ? __builtin_bit_cast(uint32_t, e[i]) : 0u;
+      else
+        r.v[i / 2] |= (i < n ? (uint32_t)__builtin_bit_cast(uint16_t, e[i]) : 0u) << (16 * (i & 1));
     }
   }
   return r;

@@ -45,13 +45,31 @@ __device__ __forceinline__ int32_t slot_key(const Ids& ids, uint32_t s) {
   return id >= 0 && id < ids.experts ? (int32_t)id : ids.experts;
 }
 
-// One row of `bytes` bytes, 16 bytes a lane and step, at any alignment of the
-// elements (2 or 4 bytes): the part of a row that piece `part` of `parts`
-// covers, lanes side by side.
+// Rows are moved 16 bytes a lane at any alignment of the elements (2 or 4
+// bytes).  A row's last piece starts early enough to end with the row, over
+// elements that the piece before it also brings (the same values twice); only
+// rows shorter than a piece go element by element.
 template <int ES>
 struct RowPiece {
+  static constexpr int kPer = 16 / ES;
   using vec = u32x4_any;
   using elem = std::conditional_t<ES == 2, uint16_t, uint32_t>;
+
+  // the piece that begins at element e, or where the row's last one does
+  __device__ static __forceinline__ int64_t start(int64_t e, int64_t row_elems) {
+    return e + kPer > row_elems && e < row_elems ? row_elems - kPer : e;
+  }
+  // a row shorter than a piece, by one lane
+  __device__ static __forceinline__ void short_row(const uint8_t* src, uint8_t* dst, bool kept,
+                                                   int64_t row_elems) {
+    elem v[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+      v[q] = reinterpret_cast<const elem*>(src)[q < row_elems ? q : 0];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+      if (q < row_elems) reinterpret_cast<elem*>(dst)[q] = kept ? v[q] : 0;
+  }
 };
 
 // ---- the sort and the copy in one launch, few slots ------------------------
@@ -71,7 +89,7 @@ __global__ __launch_bounds__(kSmallThreads) void moe_small_kernel(
     int64_t row_elems, uint8_t* __restrict__ Xs, int64_t ldxs_bytes, int32_t* __restrict__ offsets,
     int32_t* __restrict__ row_of_slot, int32_t* __restrict__ slot_of_row) {
   using RP = RowPiece<ES>;
-  constexpr int kPer = 16 / ES;
+  constexpr int kPer = RP::kPer;
   __shared__ int32_t keys[kSmallSlots];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (blockIdx.x >= slot_blocks) {  // offsets: a thread per expert (one block column only)
@@ -95,8 +113,8 @@ __global__ __launch_bounds__(kSmallThreads) void moe_small_kernel(
     src = X + (int64_t)(s / (uint32_t)ids.top_k) * ldx_bytes;
 #pragma unroll
     for (int i = 0; i < kSmallVecs; ++i) {
-      const int64_t e = e0 + (int64_t)i * 64 * kPer;
-      if (e + kPer <= row_elems) v[i] = *reinterpret_cast<const typename RP::vec*>(src + e * ES);
+      const int64_t e = RP::start(e0 + (int64_t)i * 64 * kPer, row_elems);
+      if (e >= 0 && e < row_elems) v[i] = *reinterpret_cast<const typename RP::vec*>(src + e * ES);
     }
   }
   int32_t mine = 0;
@@ -124,16 +142,16 @@ __global__ __launch_bounds__(kSmallThreads) void moe_small_kernel(
   }
   if constexpr (kCopy) {
     uint8_t* dst = Xs + (int64_t)row * ldxs_bytes;
+    if (row_elems < kPer) {
+      if (lane == 0) RP::short_row(src, dst, kept, row_elems);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kSmallVecs; ++i) {
-      const int64_t e = e0 + (int64_t)i * 64 * kPer;
-      if (e + kPer <= row_elems) {
+      const int64_t e = RP::start(e0 + (int64_t)i * 64 * kPer, row_elems);
+      if (e >= 0 && e < row_elems) {
         typename RP::vec zero = {0, 0, 0, 0};
         *reinterpret_cast<typename RP::vec*>(dst + e * ES) = kept ? v[i] : zero;
-      } else {
-        for (int64_t q = e; q < row_elems; ++q)
-          reinterpret_cast<typename RP::elem*>(dst)[q] =
-              kept ? reinterpret_cast<const typename RP::elem*>(src)[q] : 0;
       }
     }
   }
@@ -275,7 +293,7 @@ __global__ __launch_bounds__(256) void moe_copy_kernel(
     const int32_t* __restrict__ row_all, const int32_t* __restrict__ total_rows,
     uint8_t* __restrict__ Xs, int64_t ldxs_bytes) {
   using RP = RowPiece<ES>;
-  constexpr int kPer = 16 / ES;
+  constexpr int kPer = RP::kPer;
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
@@ -284,24 +302,24 @@ __global__ __launch_bounds__(256) void moe_copy_kernel(
   typename RP::vec v[kCopyVecs];
 #pragma unroll
   for (int i = 0; i < kCopyVecs; ++i) {
-    const int64_t e = e0 + (int64_t)i * 64 * kPer;
-    if (e + kPer <= row_elems) v[i] = *reinterpret_cast<const typename RP::vec*>(src + e * ES);
+    const int64_t e = RP::start(e0 + (int64_t)i * 64 * kPer, row_elems);
+    if (e >= 0 && e < row_elems) v[i] = *reinterpret_cast<const typename RP::vec*>(src + e * ES);
   }
   const int32_t total = *total_rows;
   for (int j = 0; j < top_k; ++j) {
     const int32_t row = row_all[t * top_k + j];
     const bool kept = row < total;
     uint8_t* dst = Xs + (int64_t)row * ldxs_bytes;
+    if (row_elems < kPer) {
+      if (lane == 0) RP::short_row(src, dst, kept, row_elems);
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < kCopyVecs; ++i) {
-      const int64_t e = e0 + (int64_t)i * 64 * kPer;
-      if (e + kPer <= row_elems) {
+      const int64_t e = RP::start(e0 + (int64_t)i * 64 * kPer, row_elems);
+      if (e >= 0 && e < row_elems) {
         typename RP::vec zero = {0, 0, 0, 0};
         *reinterpret_cast<typename RP::vec*>(dst + e * ES) = kept ? v[i] : zero;
-      } else {
-        for (int64_t q = e; q < row_elems; ++q)
-          reinterpret_cast<typename RP::elem*>(dst)[q] =
-              kept ? reinterpret_cast<const typename RP::elem*>(src)[q] : 0;
       }
     }
   }
@@ -321,9 +339,11 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t t = i / pieces;
   if (t >= T) return;
-  const int64_t h = (i - t * pieces) * kPer;
+  // a row's last piece ends with the row, over elements of the one before it
+  int64_t h = (i - t * pieces) * kPer;
+  if (h + kPer > H) h = H < kPer ? 0 : H - kPer;
   const int64_t S = T * top_k;
-  const int n = H - h < kPer ? (int)(H - h) : kPer;
+  const int n = H < kPer ? (int)H : kPer;
   float acc[kPer];
 #pragma unroll
   for (int q = 0; q < kPer; ++q) acc[q] = 0.0f;
@@ -390,8 +410,12 @@ __global__ __launch_bounds__(256) void moe_combine_grad_kernel(
         bare[j] = slot_of_row[s] < 0;
       }
     }
-    for (int64_t h = (int64_t)threadIdx.x * kPer; h < H; h += 256 * kPer) {
-      const int n = H - h < kPer ? (int)(H - h) : kPer;
+    for (int64_t h0 = (int64_t)threadIdx.x * kPer; h0 < H; h0 += 256 * kPer) {
+      // a row's last piece ends with the row: its first `again` elements are the
+      // piece before's too, and count once in the dot products
+      const int64_t h = h0 + kPer <= H ? h0 : H < kPer ? 0 : H - kPer;
+      const int again = (int)(h0 - h);
+      const int n = H < kPer ? (int)H : kPer;
       Piece<T_> z[kRowsAhead];
       const Piece<T_> g = load_piece(dy + h, n);
 #pragma unroll
@@ -405,7 +429,8 @@ __global__ __launch_bounds__(256) void moe_combine_grad_kernel(
           for (int q = 0; q < kPer; ++q) {
             const float gq = g.get(q);
             out[q] = w[j] * gq;
-            dot[j] = __builtin_fmaf(gq, z[j].get(q), dot[j]);
+            const float d = __builtin_fmaf(gq, z[j].get(q), dot[j]);
+            dot[j] = q < again ? dot[j] : d;
           }
           store_piece(dZ + row[j] * lddz + h, out, n);
         }
