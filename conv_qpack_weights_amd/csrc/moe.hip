@@ -79,11 +79,10 @@ struct RowPiece {
 // on its way to registers meanwhile.  Blocks past the slots' own
 // write the offsets.  Measured for 16 tokens x 2 of 8 experts, rows of 4096
 // bf16: see the table at the launcher.
-constexpr int kSmallSlots = 2048;
-constexpr int kSmallThreads = 256;
+constexpr int kSmallSlots = 4096;
 constexpr int kSmallVecs = 4;  // 16-byte pieces of a row a lane holds
 
-template <int ES, bool kCopy>
+template <int ES, bool kCopy, int kSmallThreads>
 __global__ __launch_bounds__(kSmallThreads) void moe_small_kernel(
     Ids ids, uint32_t S, uint32_t slot_blocks, const uint8_t* __restrict__ X, int64_t ldx_bytes,
     int64_t row_elems, uint8_t* __restrict__ Xs, int64_t ldxs_bytes, int32_t* __restrict__ offsets,
@@ -200,29 +199,33 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t s0 = blockIdx.x * chunk;
 
-  // own chunk: counts per wave and key
-  for (int i = threadIdx.x; i < kSortWaves * E1; i += kSortThreads) at[i / E1][i % E1] = 0;
-  __syncthreads();
+  // What comes from memory first, all at once: the wave's first 64 keys, and the
+  // counts of the chunks before this one and of all chunks -- E2 threads side by
+  // side on the keys (a power of two >= E1), the rest of the threads on further
+  // chunks.
   const uint32_t per_wave = chunk / kSortWaves;
   const uint32_t w0 = s0 + wave * per_wave;
-  for (uint32_t i = lane; i < per_wave; i += 64)
-    if (w0 + i < S) atomicAdd(&at[wave][slot_key(ids, w0 + i)], 1);
-
-  // the chunks before this one, and all chunks: E2 threads side by side on
-  // the keys (a power of two >= E1), the rest of the threads on further chunks
+  const int32_t key0 = w0 + lane < S ? slot_key(ids, w0 + lane) : 0;
   int E2 = 1;
   while (E2 < E1) E2 *= 2;
   const int parts = kSortThreads / E2;
   const int e = threadIdx.x & (E2 - 1), part = threadIdx.x / E2;
   int32_t prev = 0, all = 0;
   if (e < E1) {
-#pragma unroll 8
+#pragma unroll 16
     for (uint32_t b = part; b < gridDim.x; b += parts) {
       const int32_t c = counts[(int64_t)b * E1 + e];
       all += c;
       prev += b < blockIdx.x ? c : 0;
     }
   }
+
+  // own chunk: counts per wave and key
+  for (int i = threadIdx.x; i < kSortWaves * E1; i += kSortThreads) at[i / E1][i % E1] = 0;
+  __syncthreads();
+  if (w0 + lane < S) atomicAdd(&at[wave][key0], 1);
+  for (uint32_t i = 64 + lane; i < per_wave; i += 64)
+    if (w0 + i < S) atomicAdd(&at[wave][slot_key(ids, w0 + i)], 1);
   before[threadIdx.x] = prev;
   before[kSortThreads + threadIdx.x] = all;
   __syncthreads();
@@ -261,7 +264,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(
   for (uint32_t i = 0; i < per_wave; i += 64) {
     const uint32_t s = w0 + i + lane;
     const bool live = s < S;
-    const int32_t key = live ? slot_key(ids, s) : 0;
+    const int32_t key = i == 0 ? key0 : live ? slot_key(ids, s) : 0;
     uint64_t same = __ballot(live);
     for (int b = 0; b < bits; ++b) {
       const uint64_t ones = __ballot((key >> b) & 1);
@@ -505,19 +508,31 @@ size_t sort_ws_bytes(int64_t S, int64_t experts) {
   return (size_t)(round_up(nb * (experts + 1) * 4, 256) + round_up(S * 4, 256));
 }
 
-template <int ES, bool kCopy>
-qp_status launch_small(const Ids& ids, int64_t S, const void* X, int64_t ldx, int64_t H, void* Xs,
+template <int ES, bool kCopy, int kSmallThreads>
+qp_status launch_small_of(const Ids& ids, int64_t S, const void* X, int64_t ldx, int64_t H, void* Xs,
                        int64_t ldxs, int32_t* offsets, int32_t* row_of_slot, int32_t* slot_of_row,
                        hipStream_t stream) {
   const int64_t slot_blocks = ceil_div(S, kSmallThreads / 64);
   const int64_t ofs_blocks = ceil_div(ids.experts + 1, kSmallThreads);
   const int64_t parts = kCopy ? ceil_div(H * ES, kSmallVecs * 64 * 16) : 1;
-  hipLaunchKernelGGL((moe_small_kernel<ES, kCopy>), dim3((unsigned)(slot_blocks + ofs_blocks),
-                                                         (unsigned)parts),
+  hipLaunchKernelGGL((moe_small_kernel<ES, kCopy, kSmallThreads>),
+                     dim3((unsigned)(slot_blocks + ofs_blocks), (unsigned)parts),
                      dim3(kSmallThreads), 0, stream, ids, (uint32_t)S, (uint32_t)slot_blocks,
                      static_cast<const uint8_t*>(X), ldx * ES, H, static_cast<uint8_t*>(Xs),
                      ldxs * ES, offsets, row_of_slot, slot_of_row);
   return check_launch("qmoe sort (few slots)");
+}
+
+// Up to 64 slots every wave reads the ids itself; above, the waves of a large
+// workgroup share them in LDS.
+template <int ES, bool kCopy>
+qp_status launch_small(const Ids& ids, int64_t S, const void* X, int64_t ldx, int64_t H, void* Xs,
+                       int64_t ldxs, int32_t* offsets, int32_t* row_of_slot, int32_t* slot_of_row,
+                       hipStream_t stream) {
+  return S <= 64 ? launch_small_of<ES, kCopy, 256>(ids, S, X, ldx, H, Xs, ldxs, offsets,
+                                                   row_of_slot, slot_of_row, stream)
+                 : launch_small_of<ES, kCopy, 1024>(ids, S, X, ldx, H, Xs, ldxs, offsets,
+                                                    row_of_slot, slot_of_row, stream);
 }
 
 // X null: the sort alone.

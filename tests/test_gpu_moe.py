@@ -74,6 +74,7 @@ def _close(got, want, tol, dtype, what):
 MODES = ["all kept", "some dropped", "all dropped", "one expert"]
 # tokens, choices, experts: below, at and above every switch of the sort
 ROUTES = [(1, 1, 1), (1, 8, 512), (3, 2, 5), (32, 2, 8), (33, 2, 64), (17, 16, 65), (1024, 2, 7),
+          (2048, 2, 31), (4097, 1, 9), (16400, 1, 40), (262145, 1, 17), (131100, 3, 90),
           (1025, 2, 128), (2048, 1, 1), (700, 3, 512), (4099, 5, 33), (70000, 4, 64)]
 
 
@@ -104,7 +105,9 @@ def test_sort(qp, T, k, E, mode):
 CASES = [(1, 1, 1, 64, "all kept"), (16, 2, 8, 4096, "all kept"), (7, 3, 5, 1, "some dropped"),
          (40, 2, 4, 1101, "some dropped"), (9, 4, 3, 8, "all dropped"), (5, 9, 16, 333, "some dropped"),
          (3, 20, 32, 130, "all kept"), (1500, 2, 64, 257, "some dropped"),
-         (2100, 4, 100, 1024, "all kept"), (64, 8, 8, 8200, "one expert")]
+         (2100, 4, 100, 1024, "all kept"), (64, 8, 8, 8200, "one expert"),
+         (5000, 3, 17, 5, "some dropped"), (90000, 3, 20, 9, "some dropped"),
+         (140001, 2, 6, 4, "some dropped")]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
