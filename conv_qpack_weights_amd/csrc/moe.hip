@@ -13,8 +13,11 @@
 //
 // What bounds them: the row copies move T*H + S*H elements (S = T*top_k) and
 // are bound by HBM; every one of them walks the tokens, so that a token's own
-// row crosses the memory once and its top_k rows once each.  The sort reads S
-// ids and writes 2*S integers: a launch and a few dependent loads.
+// row crosses the memory once and its top_k rows once each.  8192 tokens x 8,
+// rows of 4096 16-bit elements (604 MB): the copy 117 us, the weighted sum 120 us,
+// 5.0-5.2 TB/s, what a plain 1 GiB device copy reaches on the same card (5.1).
+// The sort reads S ids and writes 2*S integers: a launch and a few dependent
+// loads (65536 slots, 128 experts: 4.8 + 9.3 us).
 #include <type_traits>
 
 #include "dev_util.hpp"
@@ -74,11 +77,11 @@ struct RowPiece {
 
 // ---- the sort and the copy in one launch, few slots ------------------------
 // A wave per slot finds the slot's row by counting: ids below its own, and
-// equal ids before it.  64 ids a step, one ballot each; up to kSmallSlots
+// equal ids before it, 64 ids a step and a ballot each; up to kSmallSlots
 // slots that is at most 64 steps on ids that sit in LDS.  The token's row is
 // on its way to registers meanwhile.  Blocks past the slots' own
-// write the offsets.  Measured for 16 tokens x 2 of 8 experts, rows of 4096
-// bf16: see the table at the launcher.
+// write the offsets.  16 tokens x 2 of 8 experts, rows of 4096 bf16: 3.3 us, of
+// which an empty launch is about 2 (three launches took 12).
 constexpr int kSmallSlots = 4096;
 constexpr int kSmallVecs = 4;  // 16-byte pieces of a row a lane holds
 
@@ -157,6 +160,9 @@ __global__ __launch_bounds__(kSmallThreads) void moe_small_kernel(
 }
 
 // ---- the sort of many slots ------------------------------------------------
+// (The two launches with 64 to 256 slots a chunk, and the rows copied by the
+// block that ranked them, measured slower from 12000 slots on: 65536 slots with
+// rows of 8 KB 205 us against 131.)
 // Two launches over chunks of the slots: every block counts its chunk's keys;
 // then every block adds up the counts of the chunks before its own (and of
 // all chunks, for the experts' first rows), and ranks its slots in order.
@@ -288,7 +294,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(
 }
 
 // Row copies of many slots: a wave per token and piece of the row; the piece
-// is read once and stored to the token's top_k rows.
+// is read once and stored to the token's top_k rows (604 MB in 117 us).
 constexpr int kCopyVecs = 4;
 template <int ES>
 __global__ __launch_bounds__(256) void moe_copy_kernel(
@@ -330,7 +336,9 @@ __global__ __launch_bounds__(256) void moe_copy_kernel(
 
 // ---- the way back ----------------------------------------------------------
 // Y[t] = sum_j w[t,j] * Z[row(t,j)] (kWeighted) or without the weights: a
-// thread per 16 bytes of a token's row, up to kRowsAhead rows in flight.
+// thread per 16 bytes of a token's row, up to kRowsAhead rows in flight
+// (604 MB in 120 us; the sum of a token's gradients, 4099 x 4 rows of 1101 f32,
+// 90 MB in 15.7 us, part of it from the cache).
 constexpr int kRowsAhead = 8;
 
 template <typename T_, bool kWeighted>
@@ -382,7 +390,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(
 // read once per kRowsAhead slots; every Z row once; the dot products are
 // summed in a fixed order (a thread's pieces, the wave's lanes, the waves).
 // Rows of dZ that no slot has are zeroed by the token whose slots have the
-// same numbers.
+// same numbers.  4096 tokens x 8, rows of 4096 bf16 (571 MB): 112 us, 5.1 TB/s.
 template <typename T_>
 __global__ __launch_bounds__(256) void moe_combine_grad_kernel(
     const T_* __restrict__ dY, int64_t lddy, const T_* __restrict__ Z, int64_t ldz, int64_t T,

@@ -115,10 +115,15 @@ __device__ __forceinline__ void w4_step(const W4Stage<T, kKind, kFM, kTiles>& st
 
 // ---- few rows: the waves of a workgroup share out K --------------------------
 // A workgroup owns kTiles 16-channel tiles and 16*kFM rows; each wave takes a
-// run of 128-K blocks, keeps kAhead of them in flight in registers (weights,
+// run of 128-K blocks with kAhead of them in flight in registers (weights,
 // scales and the rows' pieces, all straight from memory: a wave's rows are
 // nobody else's, so LDS would only add a hop), and the waves' sums meet in LDS
-// in a fixed order.
+// in a fixed order.  Bound by the weights' way from memory and, above some eight
+// rows, by the vector instructions (17 a word to unpack, 4 a group and tile to
+// rescale): 1 x 4096 x 4096 5.0 us (10.5 MB; a read of the same bytes takes 3.4),
+// 16 x 11008 x 4096 f16 9.5 us (24.5 MB), 64 tokens x 2 of 16 experts of
+// 11008 x 4096 98 us (454 MB, 4.6 TB/s).  kAhead = 1: two and four blocks in
+// flight cost waves a SIMD and measured 1-15% slower at every shape.
 template <typename T, int kKind, bool kOne, int kFM, int kTiles, int kWaves, int kAhead>
 __global__ __launch_bounds__(kWaves * 64) void w4_rows_kernel(W4Args a, uint32_t row_slots) {
   __shared__ f32x4 red[kWaves][kFM * kTiles][64];
@@ -257,15 +262,18 @@ qp_status launch_rows(const W4Args& a, hipStream_t stream) {
 
 // ---- many rows: tiles of 16*kFM rows x 64*kFN channels -----------------------
 // Four waves side by side on the channels, each 16*kFM x 16*kFN outputs in
-// registers.  The rows' 128-K block goes through LDS in operand order (a
-// kilobyte per 16 rows and 32 K, lane l's 16 bytes at 16*l: no bank conflicts
-// either way), double buffered, and serves all four waves; the weights come
-// straight from memory, each wave its own, one block ahead.
+// registers.  The rows go through LDS in operand order, 64 K at a time, double
+// buffered, and serve all four waves; the weights come straight from memory,
+// each wave its own, half a block ahead.
 //
 // What bounds it with groups of 32: per 16x16x32 MFMA (16 cycles of the matrix
-// unit) the group's rescale is 4 fused multiply-adds (16 cycles of the vector
-// unit), and a weight word costs about 17 vector instructions to unpack, used
-// kFM times; so the vector unit is the limit and more rows a wave are better.
+// unit) the group's rescale is 4 fused multiply-adds and a weight word costs 13
+// vector instructions to unpack, used kFM times; the two units hardly overlap
+// on this part.  8192 rows x 11008 x 4096 over 8 experts: 925 us, 798 TFLOP/s;
+// of the cycles the matrix unit is busy 37%, vector instructions issue 63%
+// (a library product of bf16 matrices of 8192: 1275 TFLOP/s).  128 x 128 tiles
+// at three waves a SIMD; 128 x 256 (spills), 64 x 256 and two waves a SIMD
+// measured 1540, 1100 and 1130 us where this took 1050.
 template <typename T, int kKind, bool kOne, int kFM, int kFN, int kOcc>
 __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t row_slots,
                                                          uint32_t col_groups) {
