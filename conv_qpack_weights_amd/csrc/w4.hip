@@ -140,7 +140,7 @@ extern "C" qp_status qgemm_w4_blockwise(const void* X, int32_t dtype, int64_t M,
   clear_error();
   const char* what = "qgemm_w4_blockwise";
   QP_REQUIRE(M >= 0, QP_EINVAL, "%s: M is negative", what);
-  QP_REQUIRE(M <= INT32_MAX, QP_EUNSUPPORTED, "%s: more than 2^31-1 rows", what);
+  QP_REQUIRE(M <= kW4MaxRows, QP_EUNSUPPORTED, "%s: more than 2^30 rows", what);
   qp_status st = w4_check_weights(what, w, packedW_dev, 1, 0);
   if (st) return st;
   QP_REQUIRE(K == w->K, QP_EINVAL, "%s: the rows have K=%lld but the weights K=%lld", what,
@@ -166,7 +166,7 @@ extern "C" qp_status qgemm_w4_experts(const void* X, int32_t dtype, int64_t x_ro
   clear_error();
   const char* what = "qgemm_w4_experts";
   QP_REQUIRE(M >= 0 && x_rows >= 0, QP_EINVAL, "%s: a row count is negative", what);
-  QP_REQUIRE(M <= INT32_MAX, QP_EUNSUPPORTED, "%s: more than 2^31-1 rows", what);
+  QP_REQUIRE(M <= kW4MaxRows, QP_EUNSUPPORTED, "%s: more than 2^30 rows", what);
   qp_status st = w4_check_weights(what, w, packedW_dev, experts, expert_stride);
   if (st) return st;
   QP_REQUIRE(K == w->K, QP_EINVAL, "%s: the rows have K=%lld but the weights K=%lld", what,

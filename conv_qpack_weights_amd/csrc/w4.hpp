@@ -42,6 +42,8 @@ struct W4Rows {
   int64_t map_div, x_rows;
 };
 
+constexpr int64_t kW4MaxRows = INT64_C(1) << 30;  // row numbers and tile counts in 32 bits
+
 struct W4Tile {
   int32_t expert;   // == experts: rows of no expert (stored as zeros); -1: nothing
   int64_t r0, r1;   // rows
@@ -111,6 +113,8 @@ __device__ __forceinline__ int64_t w4_source_row(const W4Rows& rows, int64_t r) 
 // The MFMA operands of 8 consecutive row elements: as they are for bf16 and
 // f16; an f32 value is cut into three bf16 whose sum it is exactly (8 + 8 + 8
 // bits of its 24), so the product keeps f32 accuracy at three MFMAs.
+// load_n: the first n elements, the rest zero; the pointer must be readable for
+// one element even where n <= 0.
 template <typename T>
 struct XFrag;
 

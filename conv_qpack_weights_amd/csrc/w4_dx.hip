@@ -441,9 +441,11 @@ __global__ __launch_bounds__(256, 2) void w4_dx_tile_kernel(W4DxArgs a, uint32_t
       const int n = left > 8 ? 8 : left < 0 ? 0 : (int)left;
 #pragma unroll
       for (int i = 0; i < kMine; ++i)
-        y[i].x.load_n(reinterpret_cast<const T*>(ybase + (n > 0 ? s * (32 * sizeof(T)) : 0) +
-                                                 yoff[i]),
-                      n);
+        // (a lane with nothing left points at its row's first element)
+        y[i].x.load_n(
+            reinterpret_cast<const T*>(ybase + yoff[i] + (n > 0 ? s * (int64_t)(32 * sizeof(T))
+                                                                : -quad * (int64_t)(8 * sizeof(T)))),
+            n);
     };
     float s16[8];
     uint32_t d[8];
@@ -688,7 +690,7 @@ qp_status dx_entry(const char* what, const void* dY, int32_t dtype, int64_t M, i
                    int64_t experts, const int32_t* offsets, void* dX, int64_t lddx, void* ws,
                    size_t ws_bytes, hipStream_t stream) {
   QP_REQUIRE(M >= 0, QP_EINVAL, "%s: M is negative", what);
-  QP_REQUIRE(M <= INT32_MAX, QP_EUNSUPPORTED, "%s: more than 2^31-1 rows", what);
+  QP_REQUIRE(M <= kW4MaxRows, QP_EUNSUPPORTED, "%s: more than 2^30 rows", what);
   qp_status st = w4_check_weights(what, w, packed, experts, expert_stride);
   if (st || M == 0) return st;
   if ((st = w4_check_float(what, "dY", dY, dtype, lddy, w->N))) return st;
@@ -712,7 +714,7 @@ extern "C" qp_status qgemm_w4_dx_ws_size(int64_t M, const qp_packed_info* w, int
                                          size_t* bytes) {
   using namespace qp;
   clear_error();
-  QP_REQUIRE(w && bytes && M >= 0 && M <= INT32_MAX && experts >= 1 && w->N > 0 && w->K > 0,
+  QP_REQUIRE(w && bytes && M >= 0 && M <= kW4MaxRows && experts >= 1 && w->N > 0 && w->K > 0,
              QP_EINVAL, "qgemm_w4_dx_ws_size: bad argument");
   *bytes = M == 0 ? 0 : (size_t)dx_ws_bytes(M, experts, w->N, w->K);
   return QP_OK;

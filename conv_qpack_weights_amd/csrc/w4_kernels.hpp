@@ -346,7 +346,8 @@ __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t r
   auto fetch_cut = [&](XFrag<T> (&x)[kBatch], int batch, int64_t u) {
     const int64_t left = a.w.K - (u * 64 + k_in);
     const int n = left > 8 ? 8 : left < 0 ? 0 : (int)left;
-    const uint8_t* base = xbase + (n > 0 ? u * (64 * sizeof(T)) : 0);
+    // (a lane with nothing left points at its row's first element)
+    const uint8_t* base = xbase + (n > 0 ? u * (int64_t)(64 * sizeof(T)) : -k_in * (int64_t)sizeof(T));
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
       x[j].load_n(reinterpret_cast<const T*>(base + xoff[batch * kBatch + j]), n);

@@ -570,7 +570,8 @@ qp_status qconv2d_s8_blockwise_f32(const qp_qtensor* x, const int8_t* X, const q
  *   bias     device f32 [N] or NULL, added before the clamp.
  *   Y        device [M][ldy], ldy >= N, y_dtype = dtype or QP_F32.
  * A row with an infinity or a NaN gives what the sum gives; other rows are
- * not touched by it.  Run to run the same bits.
+ * not touched by it.  Run to run the same bits.  Outputs of this and the
+ * following operators must not overlap their inputs.
  * Errors: QP_EINVAL on shapes, types, NaN or reversed bounds; QP_EALIGN.
  */
 qp_status qgemm_w4_blockwise(const void* X, int32_t dtype, int64_t M, int64_t K, int64_t ldx,
