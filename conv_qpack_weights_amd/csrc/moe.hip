@@ -192,8 +192,24 @@ __global__ __launch_bounds__(kSortThreads) void moe_count_kernel(Ids ids, uint32
   for (int e = threadIdx.x; e < E1; e += kSortThreads) counts[(int64_t)blockIdx.x * E1 + e] = n[e];
 }
 
+// The lanes whose key is this lane's, among the live ones: a ballot a key bit.
+__device__ __forceinline__ uint64_t same_key(bool live, int32_t key, int bits) {
+  uint64_t same = __ballot(live);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t ones = __ballot((key >> b) & 1);
+    same &= (key >> b) & 1 ? ones : ~ones;
+  }
+  return same;
+}
+
 // row_all[s]: the row of every slot, rows past offsets[experts] for dropped
-// ones (null: not wanted).
+// ones (null: not wanted).  kSelf: every block counts all the slots itself (a
+// launch less, but the count grows with the slots).  Alone, called in a row /
+// replayed in a graph: 5000 slots of 256 experts 10.1 / 6.9 us, with the
+// counting launch 13.5 / 7.9; 12000 of 64 experts 10.8 / 9.3 against 13.0 / 7.0.
+constexpr int kSelfSlots = 8192;
+
+template <bool kSelf>
 __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(
     Ids ids, uint32_t S, uint32_t chunk, const int32_t* __restrict__ counts,
     int32_t* __restrict__ offsets, int32_t* __restrict__ row_of_slot,
@@ -216,8 +232,9 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(
   while (E2 < E1) E2 *= 2;
   const int parts = kSortThreads / E2;
   const int e = threadIdx.x & (E2 - 1), part = threadIdx.x / E2;
+  const int bits = 32 - __builtin_clz((unsigned)ids.experts);  // keys 0 .. experts
   int32_t prev = 0, all = 0;
-  if (e < E1) {
+  if (!kSelf && e < E1) {
 #pragma unroll 16
     for (uint32_t b = part; b < gridDim.x; b += parts) {
       const int32_t c = counts[(int64_t)b * E1 + e];
@@ -232,12 +249,45 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(
   if (w0 + lane < S) atomicAdd(&at[wave][key0], 1);
   for (uint32_t i = 64 + lane; i < per_wave; i += 64)
     if (w0 + i < S) atomicAdd(&at[wave][slot_key(ids, w0 + i)], 1);
-  before[threadIdx.x] = prev;
-  before[kSortThreads + threadIdx.x] = all;
+  if constexpr (kSelf) {
+    // (chunks start at multiples of 64: a wave's slots are all before it or none)
+    constexpr int kEach = kSelfSlots / kSortThreads;
+    int32_t keys[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const uint32_t s = j * kSortThreads + threadIdx.x;
+      keys[j] = s < S ? slot_key(ids, s) : -1;
+    }
+    before[threadIdx.x] = before[kSortThreads + threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const uint32_t i = j * kSortThreads + wave * 64;
+      if (i >= S) break;
+      const int32_t key = keys[j];
+      const bool live = key >= 0;
+      // few keys: one addition a key and wave, since lanes of one key queue up
+      // (8000 slots of 2 experts 7.8 us, a lane each 12.6; of 14 experts 9.0 and
+      // 7.8, unless most slots go to one; 5000 of 256 experts 9.8 and 6.9)
+      if (bits <= 4) {
+        const uint64_t same = same_key(live, key, bits);
+        if (live && __builtin_ctzll(same) == lane) {
+          atomicAdd(&before[kSortThreads + key], __popcll(same));
+          if (i < s0) atomicAdd(&before[key], __popcll(same));
+        }
+      } else if (live) {
+        atomicAdd(&before[kSortThreads + key], 1);
+        if (i < s0) atomicAdd(&before[key], 1);
+      }
+    }
+  } else {
+    before[threadIdx.x] = prev;
+    before[kSortThreads + threadIdx.x] = all;
+  }
   __syncthreads();
   prev = all = 0;
   if (threadIdx.x < (unsigned)E1) {
-    for (int p = 0; p < parts; ++p) {
+    for (int p = 0; p < (kSelf ? 1 : parts); ++p) {
       prev += before[p * E2 + threadIdx.x];
       all += before[kSortThreads + p * E2 + threadIdx.x];
     }
@@ -266,16 +316,11 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(
 
   // rank the slots in order
   volatile int32_t* mine = at[wave];
-  const int bits = 32 - __builtin_clz((unsigned)ids.experts);  // keys 0 .. experts
   for (uint32_t i = 0; i < per_wave; i += 64) {
     const uint32_t s = w0 + i + lane;
     const bool live = s < S;
     const int32_t key = i == 0 ? key0 : live ? slot_key(ids, s) : 0;
-    uint64_t same = __ballot(live);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t ones = __ballot((key >> b) & 1);
-      same &= (key >> b) & 1 ? ones : ~ones;
-    }
+    const uint64_t same = same_key(live, key, bits);
     const int rank = __popcll(same & ((UINT64_C(1) << lane) - 1));
     int32_t row = 0;
     if (live) row = mine[key] + rank;
@@ -563,13 +608,19 @@ qp_status run_sort(const Ids& ids, int64_t T, const void* X, int32_t dtype, int6
   int32_t* row_all = X ? reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) +
                                                     round_up(nb * (ids.experts + 1) * 4, 256))
                        : nullptr;
-  hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)nb), dim3(kSortThreads), 0, stream, ids,
-                     (uint32_t)S, (uint32_t)chunk, counts);
-  qp_status st = check_launch("qmoe sort (counts)");
-  if (st) return st;
-  hipLaunchKernelGGL(moe_place_kernel, dim3((unsigned)nb), dim3(kSortThreads), 0, stream, ids,
-                     (uint32_t)S, (uint32_t)chunk, (const int32_t*)counts, offsets, row_of_slot,
-                     slot_of_row, row_all);
+  qp_status st;
+  if (S <= kSelfSlots) {
+    hipLaunchKernelGGL((moe_place_kernel<true>), dim3((unsigned)nb), dim3(kSortThreads), 0, stream,
+                       ids, (uint32_t)S, (uint32_t)chunk, (const int32_t*)nullptr, offsets,
+                       row_of_slot, slot_of_row, row_all);
+  } else {
+    hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)nb), dim3(kSortThreads), 0, stream, ids,
+                       (uint32_t)S, (uint32_t)chunk, counts);
+    if ((st = check_launch("qmoe sort (counts)"))) return st;
+    hipLaunchKernelGGL((moe_place_kernel<false>), dim3((unsigned)nb), dim3(kSortThreads), 0, stream,
+                       ids, (uint32_t)S, (uint32_t)chunk, (const int32_t*)counts, offsets,
+                       row_of_slot, slot_of_row, row_all);
+  }
   st = check_launch("qmoe sort (rows)");
   if (st || !X) return st;
   const dim3 grid((unsigned)ceil_div(T, 4), (unsigned)ceil_div(H * es, kCopyVecs * 64 * 16));

@@ -75,7 +75,8 @@ MODES = ["all kept", "some dropped", "all dropped", "one expert"]
 # tokens, choices, experts: below, at and above every switch of the sort
 ROUTES = [(1, 1, 1), (1, 8, 512), (3, 2, 5), (32, 2, 8), (33, 2, 64), (17, 16, 65), (1024, 2, 7),
           (2048, 2, 31), (4097, 1, 9), (16400, 1, 40), (262145, 1, 17), (131100, 3, 90),
-          (1025, 2, 128), (2048, 1, 1), (700, 3, 512), (4099, 5, 33), (70000, 4, 64)]
+          (1025, 2, 128), (2048, 1, 1), (700, 3, 512), (4099, 5, 33), (70000, 4, 64),
+          (4096, 2, 512), (8192, 1, 3), (2731, 3, 33), (5461, 1, 16)]
 
 
 @pytest.mark.parametrize("mode", MODES)
