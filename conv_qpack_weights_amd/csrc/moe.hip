@@ -31,6 +31,9 @@ namespace {
 
 constexpr int kMaxExperts = 512;   // the ranking kernel keeps 16 x (experts+1) counters in LDS
 constexpr int64_t kMaxSlots = INT64_C(1) << 30;
+// Workgroups of 256 threads a launch: a launch has fewer than 2^32 threads along
+// x.  Calls that need more (tens of millions of tokens) take several launches.
+constexpr int64_t kMaxBlocks = INT64_C(1) << 23;
 
 struct Ids {
   const void* p;
@@ -345,11 +348,11 @@ template <int ES>
 __global__ __launch_bounds__(256) void moe_copy_kernel(
     const uint8_t* __restrict__ X, int64_t ldx_bytes, int64_t row_elems, int64_t T, int32_t top_k,
     const int32_t* __restrict__ row_all, const int32_t* __restrict__ total_rows,
-    uint8_t* __restrict__ Xs, int64_t ldxs_bytes) {
+    uint8_t* __restrict__ Xs, int64_t ldxs_bytes, int64_t first) {
   using RP = RowPiece<ES>;
   constexpr int kPer = RP::kPer;
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t t = first + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
   const int64_t e0 = ((int64_t)blockIdx.y * kCopyVecs * 64 + lane) * kPer;
   const uint8_t* src = X + t * ldx_bytes;
@@ -390,9 +393,9 @@ template <typename T_, bool kWeighted>
 __global__ __launch_bounds__(256) void moe_combine_kernel(
     const T_* __restrict__ Z, int64_t ldz, int64_t T, int32_t top_k, int64_t H,
     const int32_t* __restrict__ row_of_slot, const float* __restrict__ weights, int64_t ldw,
-    T_* __restrict__ Y, int64_t ldy, uint32_t pieces) {
+    T_* __restrict__ Y, int64_t ldy, uint32_t pieces, int64_t first) {
   constexpr int kPer = 16 / sizeof(T_);
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t t = i / pieces;
   if (t >= T) return;
   // a row's last piece ends with the row, over elements of the one before it
@@ -441,10 +444,10 @@ __global__ __launch_bounds__(256) void moe_combine_grad_kernel(
     const T_* __restrict__ dY, int64_t lddy, const T_* __restrict__ Z, int64_t ldz, int64_t T,
     int32_t top_k, int64_t H, const int32_t* __restrict__ row_of_slot,
     const int32_t* __restrict__ slot_of_row, const float* __restrict__ weights, int64_t ldw,
-    T_* __restrict__ dZ, int64_t lddz, float* __restrict__ dW, int64_t lddw) {
+    T_* __restrict__ dZ, int64_t lddz, float* __restrict__ dW, int64_t lddw, int64_t first) {
   constexpr int kPer = 16 / sizeof(T_);
   __shared__ float part[4][kRowsAhead];
-  const int64_t t = blockIdx.x;
+  const int64_t t = first + blockIdx.x;
   const int64_t S = T * top_k;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const T_* dy = dY + t * lddy;
@@ -623,17 +626,21 @@ qp_status run_sort(const Ids& ids, int64_t T, const void* X, int32_t dtype, int6
   }
   st = check_launch("qmoe sort (rows)");
   if (st || !X) return st;
-  const dim3 grid((unsigned)ceil_div(T, 4), (unsigned)ceil_div(H * es, kCopyVecs * 64 * 16));
-  if (es == 2)
-    hipLaunchKernelGGL((moe_copy_kernel<2>), grid, dim3(256), 0, stream,
-                       static_cast<const uint8_t*>(X), ldx * 2, H, T, ids.top_k,
-                       (const int32_t*)row_all, (const int32_t*)(offsets + ids.experts),
-                       static_cast<uint8_t*>(Xs), ldxs * 2);
-  else
-    hipLaunchKernelGGL((moe_copy_kernel<4>), grid, dim3(256), 0, stream,
-                       static_cast<const uint8_t*>(X), ldx * 4, H, T, ids.top_k,
-                       (const int32_t*)row_all, (const int32_t*)(offsets + ids.experts),
-                       static_cast<uint8_t*>(Xs), ldxs * 4);
+  const int64_t parts = ceil_div(H * es, kCopyVecs * 64 * 16);
+  for (int64_t t = 0; t < T; t += 4 * kMaxBlocks) {
+    const dim3 grid((unsigned)ceil_div(T - t < 4 * kMaxBlocks ? T - t : 4 * kMaxBlocks, 4),
+                    (unsigned)parts);
+    if (es == 2)
+      hipLaunchKernelGGL((moe_copy_kernel<2>), grid, dim3(256), 0, stream,
+                         static_cast<const uint8_t*>(X), ldx * 2, H, T, ids.top_k,
+                         (const int32_t*)row_all, (const int32_t*)(offsets + ids.experts),
+                         static_cast<uint8_t*>(Xs), ldxs * 2, t);
+    else
+      hipLaunchKernelGGL((moe_copy_kernel<4>), grid, dim3(256), 0, stream,
+                         static_cast<const uint8_t*>(X), ldx * 4, H, T, ids.top_k,
+                         (const int32_t*)row_all, (const int32_t*)(offsets + ids.experts),
+                         static_cast<uint8_t*>(Xs), ldxs * 4, t);
+  }
   return check_launch("qmoe dispatch (copy)");
 }
 
@@ -664,10 +671,12 @@ qp_status launch_combine(const void* Z, int64_t ldz, int64_t T, int64_t top_k, i
                          int64_t ldy, hipStream_t stream) {
   const int64_t pieces = ceil_div(H * (int64_t)sizeof(T_), 16);
   const int64_t blocks = ceil_div(T * pieces, 256);
-  QP_REQUIRE(blocks < (INT64_C(1) << 31), QP_EUNSUPPORTED, "qmoe: more than 2^31 workgroups");
-  hipLaunchKernelGGL((moe_combine_kernel<T_, kWeighted>), dim3((unsigned)blocks), dim3(256), 0,
-                     stream, static_cast<const T_*>(Z), ldz, T, (int32_t)top_k, H, row_of_slot,
-                     weights, ldw, static_cast<T_*>(Y), ldy, (uint32_t)pieces);
+  for (int64_t b = 0; b < blocks; b += kMaxBlocks) {
+    const int64_t n = blocks - b < kMaxBlocks ? blocks - b : kMaxBlocks;
+    hipLaunchKernelGGL((moe_combine_kernel<T_, kWeighted>), dim3((unsigned)n), dim3(256), 0, stream,
+                       static_cast<const T_*>(Z), ldz, T, (int32_t)top_k, H, row_of_slot, weights,
+                       ldw, static_cast<T_*>(Y), ldy, (uint32_t)pieces, b * 256);
+  }
   return check_launch("qmoe combine");
 }
 
@@ -690,10 +699,13 @@ qp_status launch_combine_grad(const void* dY, int64_t lddy, const void* Z, int64
                               int64_t top_k, int64_t H, const int32_t* row_of_slot,
                               const int32_t* slot_of_row, const float* weights, int64_t ldw,
                               void* dZ, int64_t lddz, float* dW, int64_t lddw, hipStream_t stream) {
-  hipLaunchKernelGGL((moe_combine_grad_kernel<T_>), dim3((unsigned)T), dim3(256), 0, stream,
-                     static_cast<const T_*>(dY), lddy, static_cast<const T_*>(Z), ldz, T,
-                     (int32_t)top_k, H, row_of_slot, slot_of_row, weights, ldw,
-                     static_cast<T_*>(dZ), lddz, dW, lddw);
+  for (int64_t t = 0; t < T; t += kMaxBlocks) {
+    const int64_t n = T - t < kMaxBlocks ? T - t : kMaxBlocks;
+    hipLaunchKernelGGL((moe_combine_grad_kernel<T_>), dim3((unsigned)n), dim3(256), 0, stream,
+                       static_cast<const T_*>(dY), lddy, static_cast<const T_*>(Z), ldz, T,
+                       (int32_t)top_k, H, row_of_slot, slot_of_row, weights, ldw,
+                       static_cast<T_*>(dZ), lddz, dW, lddw, t);
+  }
   return check_launch("qmoe combine gradient");
 }
 

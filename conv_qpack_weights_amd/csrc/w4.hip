@@ -31,10 +31,7 @@ constexpr ShapeCost kShapes[] = {
     {kTile4x8, 4, 8, 42.0, 21.7}, {kTile8x8, 8, 8, 59.0, 42.0},
 };
 
-W4Shape w4_choose(const W4Args& a, int32_t dtype) {
-  const int64_t es = elem_bytes(dtype);
-  // the tile kernels address their rows by 32-bit offsets from one base
-  const int64_t span = (a.rows.map ? a.rows.x_rows : 128) * a.ldx * es;
+W4Shape w4_choose(const W4Args& a) {
   const double experts = a.rows.offsets ? (double)(a.rows.experts < a.rows.M ? a.rows.experts
                                                                              : a.rows.M)
                                         : 1.0;
@@ -42,7 +39,6 @@ W4Shape w4_choose(const W4Args& a, int32_t dtype) {
   W4Shape best = kRows1x1;
   double least = 1e300;
   for (const ShapeCost& s : kShapes) {
-    if (s.rows >= 4 && span >= (INT64_C(1) << 32)) continue;
     // row tiles of an expert: its last one is half empty on average
     double tiles = (double)ceil_div(a.rows.M, 16 * s.rows);
     if (experts > 1.0) {
@@ -61,7 +57,7 @@ W4Shape w4_choose(const W4Args& a, int32_t dtype) {
 }
 
 qp_status run_w4(const W4Args& a, int32_t dtype, int32_t format, hipStream_t stream) {
-  const W4Shape shape = w4_choose(a, dtype);
+  const W4Shape shape = w4_choose(a);
   if (dtype == QP_F32) return run_w4_f32(a, format, shape, stream);
   if (dtype == QP_BF16) return run_w4_bf16(a, format, shape, stream);
   return run_w4_f16(a, format, shape, stream);

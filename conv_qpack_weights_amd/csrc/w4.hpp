@@ -271,6 +271,14 @@ struct W4Args {
   int64_t ldy;
 };
 
+// Orders a wave's LDS accesses before it and after it (a wave's own complete in
+// order; this keeps the compiler from moving them).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---- host side -------------------------------------------------------------
 // The shapes of the kernels (16-row fragments, 16-channel tiles of a workgroup),
 // see w4_choose.

@@ -112,12 +112,17 @@ struct YFrag<float> {
   }
 };
 
-// The words and scales of a lane's eight channels in a 32-channel step.
+// The words and scales of a lane's eight channels in a 32-channel step; the
+// scales stay as they come from memory (a conversion would wait for the load).
 template <int kKind>
 struct DxWeights {
   uint32_t d[8];
-  float s[8];
+  uint32_t s[8];
   float o[kKind == 2 ? 8 : 1];
+  // a channel's scale, times the 16 that its q/16 lacks
+  __device__ __forceinline__ float s16(int r) const {
+    return __builtin_bit_cast(float, kKind == 1 ? s[r] << 16 : s[r]) * 16.0f;
+  }
 };
 
 // Where a lane finds them: lane (c, h) takes word c of the block -- 32-K number
@@ -149,10 +154,9 @@ struct DxSource {
     for (int r = 0; r < 8; ++r) {
       w.d[r] = *reinterpret_cast<const uint32_t*>(qp + r * 64);
       if constexpr (kKind == 1) {
-        const uint32_t u = *reinterpret_cast<const uint16_t*>(sp + r * 8);
-        w.s[r] = __builtin_bit_cast(float, u << 16);
+        w.s[r] = *reinterpret_cast<const uint16_t*>(sp + r * 8);
       } else {
-        w.s[r] = *reinterpret_cast<const float*>(sp + r * 16);
+        w.s[r] = *reinterpret_cast<const uint32_t*>(sp + r * 16);
       }
       if constexpr (kKind == 2)
         w.o[r] = *reinterpret_cast<const float*>(o + 2 * step * s_step + s_lane + r * 16);
@@ -182,7 +186,7 @@ __device__ __forceinline__ void dx_prepare(const DxWeights<kKind>& w, uint32_t (
   for (int r = 0; r < 8; ++r) {
     hi[r] = w.d[r] >> 4;
     asm("" : "+v"(hi[r]));  // (one shift; the conversions then select bytes)
-    s16[r] = w.s[r] * 16.0f;
+    s16[r] = w.s16(r);
   }
 }
 
@@ -462,7 +466,7 @@ __global__ __launch_bounds__(256, 2) void w4_dx_tile_kernel(W4DxArgs a, uint32_t
       }
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        s16[r] = w.s[r] * 16.0f;
+        s16[r] = w.s16(r);
         d[r] = w.d[r] >> (rg * 4);
         asm("" : "+v"(d[r]));
       }
@@ -566,8 +570,8 @@ template <typename T, int kKind, int kMT>
 qp_status launch_dx_tile(const W4DxArgs& a, hipStream_t stream) {
   const int64_t slots = w4_tile_slots(a.rows, 32 * kMT);
   const int64_t pairs = ceil_div(a.w.K, 256);
-  QP_REQUIRE(slots * pairs < (INT64_C(1) << 31), QP_EUNSUPPORTED,
-             "qgemm_w4 gradient: more than 2^31 workgroups");
+  QP_REQUIRE(slots * pairs * 256 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
+             "qgemm_w4 gradient: rows and K for more than 2^32 threads");
   constexpr size_t kLds = sizeof(DxLds<T, kKind, kMT>);
   const auto kern = w4_dx_tile_kernel<T, kKind, kMT>;
   // raise the kernel's LDS limit once per device (threads may race to set it;
@@ -592,8 +596,8 @@ qp_status launch_dx_rows(const W4DxArgs& a, int64_t splits, float* part, hipStre
   constexpr int kWaves = 8;
   const int64_t slots = w4_tile_slots(a.rows, 16 * kMT);
   const int64_t blocks = slots * splits * ceil_div(a.w.K, 128);
-  QP_REQUIRE(blocks < (INT64_C(1) << 31), QP_EUNSUPPORTED,
-             "qgemm_w4 gradient: more than 2^31 workgroups");
+  QP_REQUIRE(blocks * kWaves * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
+             "qgemm_w4 gradient: rows and K for more than 2^32 threads");
   hipLaunchKernelGGL((w4_dx_rows_kernel<T, kKind, kMT, kWaves>), dim3((unsigned)blocks),
                      dim3(kWaves * 64), 0, stream, a, (uint32_t)splits, part);
   qp_status st = check_launch("qgemm_w4 gradient (few rows)");

@@ -14,64 +14,76 @@ namespace {
 
 // The four 32-K scales (or offsets) of a channel's 128-K block: groups of 32
 // have one each; a group of 64 serves two; larger groups have one in all
-// (kOne), returned in the first place.  p: the channel tile's scales (the same
-// for the whole wave), ch: the lane's channel of 16.
+// (kOne).  They are kept as they come from memory until a step needs them: the
+// picking apart would wait for the load right behind it.
 template <bool kBf16, bool kOne>
-__device__ __forceinline__ f32x4 w4_scales(const uint8_t* p, int64_t b, int32_t group, int ch) {
-  constexpr uint32_t ES = kBf16 ? 2 : 4;
-  auto one = [&](int64_t g) -> float {
-    const uint8_t* at = p + ((g / 4) * 64 + (g & 3)) * ES + (uint32_t)ch * (4 * ES);
-    if constexpr (kBf16) {
-      const uint32_t u = *reinterpret_cast<const uint16_t*>(at);
-      return __builtin_bit_cast(float, u << 16);
+struct W4Scales {
+  using Raw = std::conditional_t<kOne, uint32_t, std::conditional_t<kBf16, u32x2, u32x4>>;
+  Raw v;
+
+  // p: the channel tile's scales (the same for the whole wave), ch: the lane's
+  // channel of 16
+  __device__ __forceinline__ void load(const uint8_t* p, int64_t b, int32_t group, int ch) {
+    constexpr uint32_t ES = kBf16 ? 2 : 4;
+    if constexpr (kOne) {
+      const int64_t g = (uint32_t)b / ((uint32_t)group / 128);
+      const uint8_t* at = p + ((g / 4) * 64 + (g & 3)) * ES + (uint32_t)ch * (4 * ES);
+      if constexpr (kBf16)
+        v = *reinterpret_cast<const uint16_t*>(at);
+      else
+        v = *reinterpret_cast<const uint32_t*>(at);
     } else {
-      return *reinterpret_cast<const float*>(at);
+      // the quad that holds the block's scales
+      v = *reinterpret_cast<const Raw*>(p + (group == 64 ? b >> 1 : b) * (64 * ES) +
+                                        (uint32_t)ch * (4 * ES));
     }
-  };
-  f32x4 s;
-  if constexpr (kOne) {
-    s[0] = one((uint32_t)b / ((uint32_t)group / 128));
-    s[1] = s[2] = s[3] = s[0];
-  } else {
-    // the quad that holds the block's scales, picked apart without a branch (a
-    // branch around a load makes its join wait for the load)
-    const bool wide = group == 64, odd = wide && (b & 1);
-    const uint8_t* at = p + (wide ? b >> 1 : b) * (64 * ES) + (uint32_t)ch * (4 * ES);
-    f32x4 v;
-    if constexpr (kBf16) {
-      const u32x2 u = *reinterpret_cast<const u32x2*>(at);
-      const uint32_t lo = u.x, hi = u.y;
-      v[0] = __builtin_bit_cast(float, lo << 16);
-      v[1] = __builtin_bit_cast(float, lo & 0xffff0000u);
-      v[2] = __builtin_bit_cast(float, hi << 16);
-      v[3] = __builtin_bit_cast(float, hi & 0xffff0000u);
-    } else {
-      v = *reinterpret_cast<const f32x4*>(at);
-    }
-    s[0] = odd ? v[2] : v[0];
-    s[1] = wide ? s[0] : v[1];
-    s[2] = odd ? v[3] : wide ? v[1] : v[2];
-    s[3] = wide ? s[2] : v[3];
   }
-  return s;
-}
+  // of block b: without a branch
+  __device__ __forceinline__ void pick(int64_t b, int32_t group, float (&s)[kOne ? 1 : 4]) const {
+    if constexpr (kOne) {
+      s[0] = __builtin_bit_cast(float, kBf16 ? v << 16 : v);
+    } else {
+      f32x4 q;
+      if constexpr (kBf16) {
+        const uint32_t lo = v.x, hi = v.y;
+        q[0] = __builtin_bit_cast(float, lo << 16);
+        q[1] = __builtin_bit_cast(float, lo & 0xffff0000u);
+        q[2] = __builtin_bit_cast(float, hi << 16);
+        q[3] = __builtin_bit_cast(float, hi & 0xffff0000u);
+      } else {
+        q = __builtin_bit_cast(f32x4, v);
+      }
+      const bool wide = group == 64, odd = wide && (b & 1);
+      s[0] = odd ? q[2] : q[0];
+      s[1] = wide ? s[0] : q[1];
+      s[2] = odd ? q[3] : wide ? q[1] : q[2];
+      s[3] = wide ? s[2] : q[3];
+    }
+  }
+};
 
 // One block's operands of a wave: kTiles channel tiles, kFM row fragments.
-template <typename T, int kKind, int kFM, int kTiles>
+template <typename T, int kKind, bool kOne, int kFM, int kTiles>
 struct W4Stage {
   u32x4 q[kTiles];
-  f32x4 s[kTiles];
-  f32x4 o[kKind == 2 ? kTiles : 1];
+  W4Scales<kKind == 1, kOne> s[kTiles];
+  W4Scales<false, kOne> o[kKind == 2 ? kTiles : 1];
   XFrag<T> x[kFM][4];
 };
 
 template <typename T, int kKind, bool kOne, int kFM, int kTiles>
-__device__ __forceinline__ void w4_step(const W4Stage<T, kKind, kFM, kTiles>& st,
-                                        f32x4 (&acc)[kFM][kTiles]) {
+__device__ __forceinline__ void w4_step(const W4Stage<T, kKind, kOne, kFM, kTiles>& st,
+                                        int64_t b, int32_t group, f32x4 (&acc)[kFM][kTiles]) {
   using V = typename XFrag<T>::vec;
   constexpr int NP = XFrag<T>::kPieces;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
   f32x4 p[kFM][kTiles], sum[kFM];
+  float s[kTiles][kOne ? 1 : 4], o[kKind == 2 ? kTiles : 1][kOne ? 1 : 4];
+#pragma unroll
+  for (int c = 0; c < kTiles; ++c) {
+    st.s[c].pick(b, group, s[c]);
+    if constexpr (kKind == 2) st.o[c].pick(b, group, o[c]);
+  }
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     V wv[kTiles];
@@ -104,8 +116,8 @@ __device__ __forceinline__ void w4_step(const W4Stage<T, kKind, kFM, kTiles>& st
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float a = acc[f][c][i];
-            a = __builtin_fmaf(st.s[c][t], p[f][c][i], a);
-            if constexpr (kKind == 2) a = __builtin_fmaf(st.o[c][t], sum[f][i], a);
+            a = __builtin_fmaf(s[c][kOne ? 0 : t], p[f][c][i], a);
+            if constexpr (kKind == 2) a = __builtin_fmaf(o[c][kOne ? 0 : t], sum[f][i], a);
             acc[f][c][i] = a;
           }
       }
@@ -169,17 +181,16 @@ __global__ __launch_bounds__(kWaves * 64) void w4_rows_kernel(W4Args a, uint32_t
 
   const int64_t t0 = n0 / 16;
   const int64_t last_tile = a.w.Npad / 16 - 1;
-  using Stage = W4Stage<T, kKind, kFM, kTiles>;
+  using Stage = W4Stage<T, kKind, kOne, kFM, kTiles>;
   auto load_weights = [&](Stage& st, int64_t b) {
 #pragma unroll
     for (int c = 0; c < kTiles; ++c) {
       const int64_t tc = t0 + c < last_tile ? t0 + c : last_tile;
       st.q[c] = *reinterpret_cast<const u32x4*>(blob + a.w.data_off + (tc * a.w.nblk + b) * 1024 +
                                                 (uint32_t)(ch * 64 + quad * 16));
-      st.s[c] = w4_scales<kKind == 1, kOne>(
-          blob + a.w.scale_off + tc * a.w.G4 * (kKind == 1 ? 128 : 256), b, a.w.group, ch);
+      st.s[c].load(blob + a.w.scale_off + tc * a.w.G4 * (kKind == 1 ? 128 : 256), b, a.w.group, ch);
       if constexpr (kKind == 2)
-        st.o[c] = w4_scales<false, kOne>(blob + a.w.offs_off + tc * a.w.G4 * 256, b, a.w.group, ch);
+        st.o[c].load(blob + a.w.offs_off + tc * a.w.G4 * 256, b, a.w.group, ch);
     }
   };
   auto load = [&](Stage& st, int64_t b) {
@@ -203,14 +214,14 @@ __global__ __launch_bounds__(kWaves * 64) void w4_rows_kernel(W4Args a, uint32_t
     for (; b + kAhead < b1; b += kAhead) {
 #pragma unroll
       for (int p = 0; p < kAhead; ++p) {
-        w4_step<T, kKind, kOne, kFM, kTiles>(st[p], acc);
+        w4_step<T, kKind, kOne, kFM, kTiles>(st[p], b + p, a.w.group, acc);
         const int64_t nb = b + p + kAhead;
         load(st[p], nb < b1 ? nb : b1 - 1);
       }
     }
 #pragma unroll
     for (int p = 0; p < kAhead; ++p)  // (no load behind a branch: its join would wait)
-      if (b + p < b1) w4_step<T, kKind, kOne, kFM, kTiles>(st[p], acc);
+      if (b + p < b1) w4_step<T, kKind, kOne, kFM, kTiles>(st[p], b + p, a.w.group, acc);
   }
   if (wave == kWaves - 1 && full * 128 < a.w.K) {
     Stage st;
@@ -223,7 +234,7 @@ __global__ __launch_bounds__(kWaves * 64) void w4_rows_kernel(W4Args a, uint32_t
         const int n = left > 8 ? 8 : left < 0 ? 0 : (int)left;
         st.x[f][t].load_n(xr[f] + (n > 0 ? full * 128 + t * 32 : -8 * quad), n);
       }
-    w4_step<T, kKind, kOne, kFM, kTiles>(st, acc);
+    w4_step<T, kKind, kOne, kFM, kTiles>(st, full, a.w.group, acc);
   }
 
 #pragma unroll
@@ -252,8 +263,8 @@ __global__ __launch_bounds__(kWaves * 64) void w4_rows_kernel(W4Args a, uint32_t
 template <typename T, int kKind, bool kOne, int kFM, int kTiles, int kWaves, int kAhead>
 qp_status launch_rows(const W4Args& a, hipStream_t stream) {
   const int64_t groups = ceil_div(a.w.Npad / 16, kTiles), slots = w4_tile_slots(a.rows, 16 * kFM);
-  QP_REQUIRE(slots * groups < (INT64_C(1) << 31), QP_EUNSUPPORTED,
-             "qgemm_w4: more than 2^31 workgroups");
+  QP_REQUIRE(slots * groups * kWaves * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
+             "qgemm_w4: rows and channels for more than 2^32 threads");
   hipLaunchKernelGGL((w4_rows_kernel<T, kKind, kOne, kFM, kTiles, kWaves, kAhead>),
                      dim3((unsigned)(slots * groups)), dim3(kWaves * 64), 0, stream, a,
                      (uint32_t)slots);
@@ -316,21 +327,20 @@ __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t r
   // side in memory (whole lines), a wave eight rows at a time.  In LDS piece c
   // (of 8) of row r sits in the operand order of fragment r/16 and 32-K number
   // c/4, but at place (r%16) ^ c of its 16: otherwise the eight lanes that write
-  // one row would meet in the same banks.  Offsets from one base fit 32 bits
-  // (the host sends rows that span more elsewhere).
+  // one row would meet in the same banks.
   constexpr int kMine = kFM / 2;
   const uint8_t* xbase = static_cast<const uint8_t*>(a.X);
   if (!a.rows.map) xbase += tile.r0 * a.ldx * sizeof(T);
   const int piece_in = lane & 7, row8 = wave * 8 + (lane >> 3);
   const int k_in = piece_in * 8;
-  uint32_t xoff[kMine];
+  int64_t xoff[kMine];
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
     int64_t r = tile.r0 + j * 32 + row8;
     r = r < tile.r1 ? r : tile.r1 - 1;
     int64_t x = a.rows.map ? w4_source_row(a.rows, r) : r - tile.r0;
     x = x < 0 ? 0 : x;
-    xoff[j] = (uint32_t)((x * a.ldx + k_in) * sizeof(T));
+    xoff[j] = (x * a.ldx + k_in) * (int64_t)sizeof(T);
   }
   // (row8/16 and c/4 pick the kilobyte, fragments 2j and 2j + 1)
   const int place = ((row8 >> 4) * 2 + (piece_in >> 2)) * 64 + (piece_in & 3) * 16 +
@@ -366,25 +376,38 @@ __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t r
 
   const int64_t t0 = n0 / 16, last_tile = a.w.Npad / 16 - 1;
   struct Scales {
-    f32x4 s[kFN];
-    f32x4 o[kKind == 2 ? kFN : 1];
+    float s[kFN][kOne ? 1 : 4];
+    float o[kKind == 2 ? kFN : 1][kOne ? 1 : 4];
+  };
+  struct RawScales {
+    W4Scales<kKind == 1, kOne> s[kFN];
+    W4Scales<false, kOne> o[kKind == 2 ? kFN : 1];
   };
   auto load_q = [&](u32x4 (&q)[kFN], int64_t b) {
+    uint32_t at = ch * 64 + quad * 16;
+    asm volatile("" : "+v"(at));
 #pragma unroll
     for (int c = 0; c < kFN; ++c) {
       const int64_t tc = t0 + c < last_tile ? t0 + c : last_tile;
-      q[c] = *reinterpret_cast<const u32x4*>(blob + a.w.data_off + (tc * a.w.nblk + b) * 1024 +
-                                             (uint32_t)(ch * 64 + quad * 16));
+      q[c] = *reinterpret_cast<const u32x4*>(blob + a.w.data_off + (tc * a.w.nblk + b) * 1024 + at);
     }
   };
-  auto load_s = [&](Scales& w, int64_t b) {
+  auto load_s = [&](RawScales& w, int64_t b) {
+    int ch = lane & 15;
+    asm volatile("" : "+v"(ch));
 #pragma unroll
     for (int c = 0; c < kFN; ++c) {
       const int64_t tc = t0 + c < last_tile ? t0 + c : last_tile;
-      w.s[c] = w4_scales<kKind == 1, kOne>(
-          blob + a.w.scale_off + tc * a.w.G4 * (kKind == 1 ? 128 : 256), b, a.w.group, ch);
+      w.s[c].load(blob + a.w.scale_off + tc * a.w.G4 * (kKind == 1 ? 128 : 256), b, a.w.group, ch);
       if constexpr (kKind == 2)
-        w.o[c] = w4_scales<false, kOne>(blob + a.w.offs_off + tc * a.w.G4 * 256, b, a.w.group, ch);
+        w.o[c].load(blob + a.w.offs_off + tc * a.w.G4 * 256, b, a.w.group, ch);
+    }
+  };
+  auto pick_s = [&](Scales& w, const RawScales& raw, int64_t b) {
+#pragma unroll
+    for (int c = 0; c < kFN; ++c) {
+      raw.s[c].pick(b, a.w.group, w.s[c]);
+      if constexpr (kKind == 2) raw.o[c].pick(b, a.w.group, w.o[c]);
     }
   };
 
@@ -430,7 +453,8 @@ __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t r
   // the unpacking and the reads in front and spills.
   XFrag<T> x[kBatch];
   u32x4 q[kFN], qn[kFN];
-  Scales w, wn;
+  Scales w;
+  RawScales wn;
   constexpr int kT = kOne ? 2 : 1;  // 32-K steps with one rescale
   V wv[2][kT][kFN];                 // the words of this step and the next
   auto unpack_first = [&](auto half) {
@@ -447,24 +471,25 @@ __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t r
     constexpr bool kMore = decltype(more)::value;
     constexpr int kRounds = 2 / kT, kSteps = kRounds * kFM;
     Sums d[2];
-    Operand ahead[3][kT];
+    constexpr int kReads = kOne ? 2 : 3;
+    Operand ahead[kReads][kT];
     auto read = [&](int i) {
       if (i < kSteps) {
 #pragma unroll
         for (int t = 0; t < kT; ++t)
-          operand(ahead[i % 3][t], buf, i % kFM, kOne ? t : i / kFM);
+          operand(ahead[i % kReads][t], buf, i % kFM, kOne ? t : i / kFM);
       }
     };
     if constexpr (kMore) fetch(x, 0, next);
     read(0);
-    read(1);
+    if (kReads > 2) read(1);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int round = i / kFM, f = i % kFM;
       // which unpacked words: rounds alternate; the whole unit for kOne
       const int now = kOne ? H : round & 1;
       __builtin_amdgcn_sched_barrier(0);
-      read(i + 2);
+      read(i + kReads - 1);
       if (kMore && i == kSteps / 2) {
         stage(x, 0, buf ^ 1);
         fetch(x, 1, next);
@@ -477,14 +502,14 @@ __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t r
 #pragma unroll
         for (int t = 0; t < kT; ++t)
 #pragma unroll
-          for (int n = 0; n < NP; ++n) p = mfma32(ahead[i % 3][t].v[n], wv[now][t][c], p);
+          for (int n = 0; n < NP; ++n) p = mfma32(ahead[i % kReads][t].v[n], wv[now][t][c], p);
         d[i & 1].p[c] = p;
         if (kKind == 2 && c == 0) {
           f32x4 o = zero;
 #pragma unroll
           for (int t = 0; t < kT; ++t)
 #pragma unroll
-            for (int n = 0; n < NP; ++n) o = mfma32(ahead[i % 3][t].v[n], ones, o);
+            for (int n = 0; n < NP; ++n) o = mfma32(ahead[i % kReads][t].v[n], ones, o);
           d[i & 1].sum = o;
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -525,7 +550,8 @@ __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t r
   const int64_t units = a.w.K / 64, pairs = units / 2;
   if (pairs > 0) {
     load_q(q, 0);
-    load_s(w, 0);
+    load_s(wn, 0);
+    pick_s(w, wn, 0);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       fetch(x, i, 0);
@@ -543,14 +569,15 @@ __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t r
       load_q(qn, nb);
       load_s(wn, nb);
       unit(Half1{}, true_type{}, 1, 2 * nb);
-      w = wn;
+      pick_s(w, wn, nb);
 #pragma unroll
       for (int c = 0; c < kFN; ++c) q[c] = qn[c];
     }
   }
   if (units * 64 < a.w.K || (units & 1)) {  // the last, cut or half, block
     load_q(q, pairs);
-    load_s(w, pairs);
+    load_s(wn, pairs);
+    pick_s(w, wn, pairs);
     unpack_first(Half0{});
     for (int64_t u = 2 * pairs; u * 64 < a.w.K; ++u) {
       __syncthreads();
@@ -588,7 +615,7 @@ __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t r
     for (int c = 0; c < kFN; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) out[(4 * quad + i) * kOutLd + c * 16 + ch] = acc[f][c][i];
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
 #pragma unroll
     for (int h = 0; h < 16; h += kRowsPass) {
       const int64_t r = tile.r0 + f * 16 + h + row_in;
@@ -607,7 +634,7 @@ __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t r
         w4_store8(a.Y, a.y_dtype, r * a.ldy + col, y, n);
       }
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
   }
 }
 
@@ -615,8 +642,8 @@ template <typename T, int kKind, bool kOne, int kFM, int kFN, int kOcc>
 qp_status launch_tile(const W4Args& a, hipStream_t stream) {
   const int64_t slots = w4_tile_slots(a.rows, 16 * kFM);
   const int64_t groups = ceil_div(a.w.N, 64 * kFN);
-  QP_REQUIRE(slots * groups < (INT64_C(1) << 31), QP_EUNSUPPORTED,
-             "qgemm_w4: more than 2^31 workgroups");
+  QP_REQUIRE(slots * groups * 256 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
+             "qgemm_w4: rows and channels for more than 2^32 threads");
   hipLaunchKernelGGL((w4_tile_kernel<T, kKind, kOne, kFM, kFN, kOcc>), dim3((unsigned)(slots * groups)),
                      dim3(256), 0, stream, a, (uint32_t)slots, (uint32_t)groups);
   return check_launch("qgemm_w4 (many rows)");

@@ -572,7 +572,9 @@ qp_status qconv2d_s8_blockwise_f32(const qp_qtensor* x, const int8_t* X, const q
  * A row with an infinity or a NaN gives what the sum gives; other rows are
  * not touched by it.  Run to run the same bits.  Outputs of this and the
  * following operators must not overlap their inputs.
- * Errors: QP_EINVAL on shapes, types, NaN or reversed bounds; QP_EALIGN.
+ * Errors: QP_EINVAL on shapes, types, NaN or reversed bounds; QP_EALIGN;
+ * QP_EUNSUPPORTED above 2^30 rows or where a launch would pass 2^32 threads
+ * (16 rows by 64 channels take 512 at most).
  */
 qp_status qgemm_w4_blockwise(const void* X, int32_t dtype, int64_t M, int64_t K, int64_t ldx,
                              const qp_packed_info* w, const void* packedW_dev, const float* bias,

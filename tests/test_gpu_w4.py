@@ -289,6 +289,31 @@ def test_large_f32_values_keep_their_accuracy(qp):
            "f32", "y")
 
 
+@pytest.mark.parametrize("M", [200, 4096])  # few rows and many
+def test_rows_far_apart(qp, M):
+    """Mapped rows of a table past 4 GiB."""
+    import torch
+    N, K, ldx, E = 512, 100, 8192, 2
+    c = Case(qp, E, N, K, 32, "f32", seed=M)
+    table = torch.empty((1 << 18) + 64, ldx, dtype=torch.bfloat16, device="cuda")
+    x_rows = table.shape[0]
+    pick = c.rng.choice(x_rows // 2, M, replace=False) * 2   # every other row, the last ones too
+    pick[0], pick[-1] = x_rows - 1, 1
+    X, x = c.rows(M, K, "bf16")
+    where = torch.from_numpy(pick).cuda()
+    table[where, :K] = X
+    cut = M // 3
+    offsets = torch.tensor([0, cut, M], dtype=torch.int32, device="cuda")
+    print("rows far apart", M, flush=True)
+    Y = qp.qgemm_w4_experts(table[:, :K], c.blobs, c.info, offsets,
+                            rows=where.to(torch.int32), row_div=1)
+    want = np.concatenate([x[:cut] @ c.W[0].T, x[cut:] @ c.W[1].T])
+    mag = np.concatenate([abs(x[:cut]) @ abs(c.W[0]).T, abs(x[cut:]) @ abs(c.W[1]).T])
+    tol = (K / 32 + 64) * 2.0 ** -24 * mag + ROUND["bf16"] * np.abs(want) * 1.01
+    got = Y.double().cpu().numpy()
+    assert np.isfinite(got).all() and (np.abs(got - want) <= tol).all()
+
+
 def test_empty_and_one(qp):
     import torch
     c = Case(qp, 2, 48, 64, 32, "f32")
