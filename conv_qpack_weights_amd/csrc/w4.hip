@@ -17,7 +17,7 @@ namespace {
 // order).  Measured with bf16 rows, groups of 32, 4096 and 11008 channels, 1 to
 // 1024 rows, four copies of the weights in turn: e.g. 16 x 11008 rows1x1 15.6,
 // 1x2 13.1, 1x3 9.5, 1x4 10.4 us; 64 x 11008 48.6, 32.8, 26.2, 23.3 and rows2x3
-// 24.4; 512 x 4096 rows2x4 52, tile4x8 49, tile8x8 61.  Over all shapes and rows
+// 24.4; 512 x 4096 rows2x4 52, tile4x8 45, tile8x8 61.  Over all shapes and rows
 // swept, and over 8 and 16 experts, the best was at most a fifth faster than the
 // one chosen.  (Same order for f32 rows, at twice the times.)
 struct ShapeCost {

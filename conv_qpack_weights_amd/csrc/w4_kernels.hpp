@@ -280,11 +280,17 @@ qp_status launch_rows(const W4Args& a, hipStream_t stream) {
 // What bounds it with groups of 32: per 16x16x32 MFMA (16 cycles of the matrix
 // unit) the group's rescale is 4 fused multiply-adds and a weight word costs 13
 // vector instructions to unpack, used kFM times; the two units hardly overlap
-// on this part.  8192 rows x 11008 x 4096 over 8 experts: 925 us, 798 TFLOP/s;
-// of the cycles the matrix unit is busy 37%, vector instructions issue 63%
+// on this part.  8192 rows x 11008 x 4096 over 8 experts: 903 us, 817 TFLOP/s;
+// of the cycles the matrix unit is busy 38%, vector instructions issue 65%
 // (a library product of bf16 matrices of 8192: 1275 TFLOP/s).  128 x 128 tiles
 // at three waves a SIMD; 128 x 256 (spills), 64 x 256 and two waves a SIMD
-// measured 1540, 1100 and 1130 us where this took 1050.
+// measured 1540, 1100 and 1130 us where this took 1050.  Every register counts
+// (168 a lane at three waves): the weights' and scales' addresses are a scalar
+// base and one lane offset, made anew each block so that they are not kept as
+// 64-bit pointers (11 reloads of spilled registers a block without).  Groups of
+// 128 on take one rescale per 64 K: 1024 x 11008 x 4096 f16 107 us (119 with
+// those reloads); the MFMAs of a tile spread out between the other tile's changed
+// nothing.
 template <typename T, int kKind, bool kOne, int kFM, int kFN, int kOcc>
 __global__ __launch_bounds__(256, kOcc) void w4_tile_kernel(W4Args a, uint32_t row_slots,
                                                          uint32_t col_groups) {

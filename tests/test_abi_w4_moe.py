@@ -49,6 +49,7 @@ def test_dense_product_refusals(qp):
     for kw, code, needle in [
             (dict(M=-1), qp.QP_EINVAL, "negative"),
             (dict(M=1 << 31), qp.QP_EUNSUPPORTED, "rows"),
+            (dict(M=(1 << 30) + 1), qp.QP_EUNSUPPORTED, "rows"),
             (dict(K=128), qp.QP_EINVAL, "K=128"),
             (dict(ldx=128), qp.QP_EINVAL, "stride of X"),
             (dict(ldy=69), qp.QP_EINVAL, "stride of Y"),
@@ -68,6 +69,15 @@ def test_dense_product_refusals(qp):
     i8.format = 1
     _refused(qp, _dense(qp, i8), qp.QP_EINVAL, "int4 blob")
     assert _dense(qp, i, M=0, X=None, Y=None) == qp.QP_OK  # nothing to do
+
+
+def test_more_threads_than_a_launch_has_are_refused(qp):
+    i = _info(qp, N=65536, K=129)
+    _refused(qp, _dense(qp, i, M=1 << 30, ldy=65536), qp.QP_EUNSUPPORTED, "2^32 threads")
+    j = _info(qp, N=32, K=1 << 16)
+    _refused(qp, qp.lib().qgemm_w4_blockwise_dx(P, qp.QP_BF16, 1 << 28, 32, C.byref(j), P, P,
+                                                1 << 16, None, 0, None), qp.QP_EUNSUPPORTED,
+             "2^32 threads")
 
 
 @pytest.mark.parametrize("fmt", [2, 3, 4])
