@@ -13,6 +13,12 @@
 // (f16 as two pieces, f32 as three).  Of the pieces' products those are formed
 // whose order adds up to less than the number of weight pieces: what is left
 // out is below 2^-16 of a term (2^-23 for f32 rows).  Sums are f32.
+//
+// Groups of 128 on without offsets: a block has one scale a channel, so the rows
+// can carry it: dy*s, rounded to f32, goes in as two bf16 pieces (three for f32
+// rows), missing at most 2^-16 (2^-23), and q/16 exactly as one.  The weights then
+// cost an unpacking only, and f16 rows take two MFMAs instead of three, f32 rows
+// three instead of six.
 #include <atomic>
 #include <type_traits>
 
@@ -79,35 +85,49 @@ template <typename T>
 struct YFrag;
 template <>
 struct YFrag<bf16_t> {
-  static constexpr int kPieces = 1, kWPieces = 2;
+  static constexpr int kPieces = 1, kWPieces = 2, kScaledPieces = 2;
   XFrag<bf16_t> x;
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = x.v[i];
+      f[2 * i] = low_f32(u);
+      f[2 * i + 1] = high_f32(u);
+    }
+  }
   __device__ __forceinline__ void split(bf16x8 (&o)[1]) const {
     o[0] = __builtin_bit_cast(bf16x8, x.v);
   }
 };
 template <>
 struct YFrag<f16_t> {
-  static constexpr int kPieces = 2, kWPieces = 2;  // 11 bits: two pieces hold them
+  static constexpr int kPieces = 2, kWPieces = 2, kScaledPieces = 2;  // 11 bits: two pieces hold them
   XFrag<f16_t> x;
-  __device__ __forceinline__ void split(bf16x8 (&o)[2]) const {
+  __device__ __forceinline__ void values(float (&f)[8]) const {
     const f16x8 h = __builtin_bit_cast(f16x8, x.v);
-    float f[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = (float)h[i];
+  }
+  __device__ __forceinline__ void split(bf16x8 (&o)[2]) const {
+    float f[8];
+    values(f);
     split_bf16<2, true>(f, o);
   }
 };
 template <>
 struct YFrag<float> {
-  static constexpr int kPieces = 3, kWPieces = 3;
+  static constexpr int kPieces = 3, kWPieces = 3, kScaledPieces = 3;
   XFrag<float> x;
-  __device__ __forceinline__ void split(bf16x8 (&o)[3]) const {
-    float f[8];
+  __device__ __forceinline__ void values(float (&f)[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t u = x.v[i / 4][i & 3];
       f[i] = __builtin_bit_cast(float, u);
     }
+  }
+  __device__ __forceinline__ void split(bf16x8 (&o)[3]) const {
+    float f[8];
+    values(f);
     split_bf16<3, true>(f, o);
   }
 };
@@ -119,10 +139,11 @@ struct DxWeights {
   uint32_t d[8];
   uint32_t s[8];
   float o[kKind == 2 ? 8 : 1];
-  // a channel's scale, times the 16 that its q/16 lacks
-  __device__ __forceinline__ float s16(int r) const {
-    return __builtin_bit_cast(float, kKind == 1 ? s[r] << 16 : s[r]) * 16.0f;
+  __device__ __forceinline__ float scale(int r) const {
+    return __builtin_bit_cast(float, kKind == 1 ? s[r] << 16 : s[r]);
   }
+  // times the 16 that q/16 lacks
+  __device__ __forceinline__ float s16(int r) const { return scale(r) * 16.0f; }
 };
 
 // Where a lane finds them: lane (c, h) takes word c of the block -- 32-K number
@@ -190,6 +211,22 @@ __device__ __forceinline__ void dx_prepare(const DxWeights<kKind>& w, uint32_t (
   }
 }
 
+// Column j as it is, q/16 in bf16: for rows that carry the scales.
+template <int kKind>
+__device__ __forceinline__ bf16x8 dx_plain_column(const DxWeights<kKind>& w,
+                                                  const uint32_t (&hi)[8], int j) {
+  uint32_t f[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const uint32_t x = j < 4 ? w.d[r] : hi[r];
+    f[r] = __builtin_bit_cast(uint32_t, nib_f32((x >> (8 * (j & 3))) & 0xffu));
+  }
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = hi_halves(f[2 * i], f[2 * i + 1]);
+  return __builtin_bit_cast(bf16x8, o);
+}
+
 // The products of the pieces that count, small ones first.
 template <int NY, int NW>
 __device__ __forceinline__ f32x4 dx_mfma(const bf16x8 (&y)[NY], const bf16x8 (&w)[NW], f32x4 acc) {
@@ -210,8 +247,11 @@ __device__ __forceinline__ f32x4 dx_mfma(const bf16x8 (&y)[NY], const bf16x8 (&w
 // w4_dx_join_kernel adds up in order.  Bound by the vector instructions that make
 // the weights' pieces (some 330 a step and wave, for 16 MFMAs a row fragment):
 // 16 x 4096 x 4096 13 us (29 without splits), 16 x 11008 x 4096 18 us,
-// 37 x 1037 x 1100 f16 10 us, 512 x 4096 x 4096 51 us (338 TFLOP/s).
-template <typename T, int kKind, int kMT, int kWaves>
+// 37 x 1037 x 1100 f16 10 us, 512 x 4096 x 4096 51 us (338 TFLOP/s).  kOne: the
+// rows carry the scales (groups of 128 on); 1024 x 4096 x 4096 bf16 86 us (94
+// without), f16 88 (121), f32 122 (201); 1 x 4096 x 4096 9.3, 8.9, 9.3 us (10.7,
+// 10.6, 12.2).
+template <typename T, int kKind, bool kOne, int kMT, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) void w4_dx_rows_kernel(W4DxArgs a, uint32_t splits,
                                                                  float* part) {
   constexpr int NY = YFrag<T>::kPieces, NW = YFrag<T>::kWPieces;
@@ -245,6 +285,27 @@ __global__ __launch_bounds__(kWaves * 64) void w4_dx_rows_kernel(W4DxArgs a, uin
       uint32_t hi[8];
       float s16[8];
       dx_prepare<kKind>(w, hi, s16);
+      if constexpr (kOne) {  // the lane's eight channels are those of its rows' elements
+        constexpr int NS = YFrag<T>::kScaledPieces;
+        bf16x8 y[kMT][NS];
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) {
+          float f[8];
+          yf[m].values(f);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) f[r] = f[r] * w.scale(r);
+          split_bf16<NS, true>(f, y[m]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bf16x8 wv = dx_plain_column<kKind>(w, hi, j);
+#pragma unroll
+          for (int n = NS - 1; n >= 0; --n)
+#pragma unroll
+            for (int m = 0; m < kMT; ++m) acc[m][j] = mfma32(y[m][n], wv, acc[m][j]);
+        }
+        return;
+      }
       bf16x8 y[kMT][NY];
 #pragma unroll
       for (int m = 0; m < kMT; ++m) yf[m].split(y[m]);
@@ -325,6 +386,7 @@ __global__ __launch_bounds__(kWaves * 64) void w4_dx_rows_kernel(W4DxArgs a, uin
   for (int m = 0; m < kMT; ++m)
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
+      if constexpr (kOne) sum[m][e] *= 16.0f;
       const int id = threadIdx.x + e * kWaves * 64;
       const int64_t r = tile.r0 + m * 16 + (id >> 5);
       const int64_t k = (int64_t)blk * 128 + (id & 31) * 4;
@@ -591,14 +653,14 @@ qp_status launch_dx_tile(const W4DxArgs& a, hipStream_t stream) {
   return check_launch("qgemm_w4 gradient (many rows)");
 }
 
-template <typename T, int kKind, int kMT>
+template <typename T, int kKind, bool kOne, int kMT>
 qp_status launch_dx_rows(const W4DxArgs& a, int64_t splits, float* part, hipStream_t stream) {
   constexpr int kWaves = 8;
   const int64_t slots = w4_tile_slots(a.rows, 16 * kMT);
   const int64_t blocks = slots * splits * ceil_div(a.w.K, 128);
   QP_REQUIRE(blocks * kWaves * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
              "qgemm_w4 gradient: rows and K for more than 2^32 threads");
-  hipLaunchKernelGGL((w4_dx_rows_kernel<T, kKind, kMT, kWaves>), dim3((unsigned)blocks),
+  hipLaunchKernelGGL((w4_dx_rows_kernel<T, kKind, kOne, kMT, kWaves>), dim3((unsigned)blocks),
                      dim3(kWaves * 64), 0, stream, a, (uint32_t)splits, part);
   qp_status st = check_launch("qgemm_w4 gradient (few rows)");
   if (st || splits == 1) return st;
@@ -664,6 +726,13 @@ int64_t dx_ws_bytes(int64_t M, int64_t experts, int64_t N, int64_t K) {
   return p.splits == 1 ? 0 : round_up(p.splits * M * round_up(K, 128) * 4, 256);
 }
 
+template <typename T, int kKind, bool kOne>
+qp_status launch_dx_frags(const W4DxArgs& a, const DxPlan& p, float* part, hipStream_t stream) {
+  if (p.frags == 1) return launch_dx_rows<T, kKind, kOne, 1>(a, p.splits, part, stream);
+  if (p.frags == 2) return launch_dx_rows<T, kKind, kOne, 2>(a, p.splits, part, stream);
+  return launch_dx_rows<T, kKind, kOne, 4>(a, p.splits, part, stream);
+}
+
 template <typename T, int kKind>
 qp_status launch_dx(const W4DxArgs& a, void* ws, hipStream_t stream) {
   const int64_t M = a.rows.M, experts = a.rows.offsets ? a.rows.experts : 1;
@@ -677,9 +746,10 @@ qp_status launch_dx(const W4DxArgs& a, void* ws, hipStream_t stream) {
       return launch_dx_tile<T, kKind, 4>(a, stream);
   }
   float* part = static_cast<float*>(ws);
-  if (p.frags == 1) return launch_dx_rows<T, kKind, 1>(a, p.splits, part, stream);
-  if (p.frags == 2) return launch_dx_rows<T, kKind, 2>(a, p.splits, part, stream);
-  return launch_dx_rows<T, kKind, 4>(a, p.splits, part, stream);
+  if constexpr (kKind != 2)
+    if (a.w.group >= 128)
+      return launch_dx_frags<T, kKind, true>(a, p, part, stream);
+  return launch_dx_frags<T, kKind, false>(a, p, part, stream);
 }
 
 template <typename T>

@@ -612,8 +612,8 @@ qp_status qgemm_w4_experts(const void* X, int32_t dtype, int64_t x_rows, int64_t
  *   offsets  as qgemm_w4_experts; rows of no expert get zeros.
  *   ws       device workspace of qgemm_w4_dx_ws_size bytes (0: may be NULL),
  *            256-byte aligned.  experts = 1 for the dense product.
- * Each term dY * W is formed to within 2^-15 of itself (2^-22 for f32 rows),
- * sums are f32.  A row of dY with an infinity or a NaN gives infinities or
+ * Each term dY * W is formed to within 2^-15 of itself (2^-22 for f32 rows;
+ * terms below 2^-100 have fewer bits), sums are f32.  A row of dY with an infinity or a NaN gives infinities or
  * NaNs in that row of dX, not always which of the two the sum would give.
  */
 qp_status qgemm_w4_dx_ws_size(int64_t M, const qp_packed_info* w, int64_t experts, size_t* bytes);

@@ -274,6 +274,35 @@ def test_non_finite_rows_stay_apart(qp, dtype):
     assert not torch.isfinite(dX[3]).any() and torch.isnan(dX[20]).all()
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_gradient_with_one_scale_a_block(qp, dtype, kind):
+    """Groups of 128 and 384: by expert, with non-finite rows that stay apart,
+    and f32 rows over the exponent range."""
+    import torch
+    M, N = 75, 330
+    for group, K in [(128, 300), (384, 1000)]:
+        c = Case(qp, 3, N, K, group, kind, seed=group)
+        offsets = torch.tensor([0, 40, 40, 70], dtype=torch.int32, device="cuda")
+        dY, dy = c.rows(M, N, dtype)
+        if dtype == "f32":
+            dY *= torch.logspace(-25, 25, M, device="cuda")[:, None]
+            dy = dY.double().cpu().numpy()
+        print("one scale a block", dtype, kind, group, flush=True)
+        clean = qp.qgemm_w4_experts_dx(dY, c.blobs, c.info, offsets)
+        want, A = np.zeros((M, K)), np.zeros((M, K))
+        for e, r0, r1 in [(0, 0, 40), (2, 40, 70)]:
+            want[r0:r1] = dy[r0:r1] @ c.W[e]
+            A[r0:r1] = np.abs(dy[r0:r1]) @ np.abs(c.W[e])
+        _close(clean, want, A, N, dtype, "dx", 2.0 ** -22 if dtype == "f32" else 2.0 ** -15)
+        dY[3, 17] = float("inf")
+        dY[50, N - 1] = float("nan")
+        dX = qp.qgemm_w4_experts_dx(dY, c.blobs, c.info, offsets)
+        keep = [r for r in range(M) if r not in (3, 50)]
+        assert torch.equal(dX[keep], clean[keep])
+        assert not torch.isfinite(dX[3]).any() and torch.isnan(dX[50]).all()
+
+
 def test_large_f32_values_keep_their_accuracy(qp):
     """f32 rows over the whole exponent range, up to the largest finite value."""
     import torch
