@@ -657,6 +657,15 @@ def _ints(t, what, dtype=torch.int32):
         "%s must be a contiguous %s tensor" % (what, dtype)
 
 
+def _one_gpu(what, first, *others):
+    """What a launch reads and writes must be where it runs: a host address, or
+    another card's, would be a fault on the GPU."""
+    gpu = first.get_device()
+    assert gpu >= 0, "%s: its tensors must be on the GPU" % what
+    for t in others:
+        assert t is None or t.get_device() == gpu, "%s: its tensors must be on one GPU" % what
+
+
 def _f32(t, what):
     assert t is None or (t.dtype == torch.float32 and t.is_contiguous()), \
         "%s must be a contiguous float32 tensor" % what
@@ -689,6 +698,7 @@ def qgemm_w4_blockwise(X: torch.Tensor, blob: torch.Tensor, info: PackedInfo, bi
     if bias is not None:
         _f32(bias, "bias")
         assert bias.numel() == info.N, "bias must hold N values"
+    _one_gpu("qgemm_w4_blockwise", X, blob, bias, out)
     _check(_lib.qgemm_w4_blockwise(_ptr(X), dt, M, K, ldx, C.byref(info), _ptr(blob), _ptr(bias),
                                    clamp_lo, clamp_hi, _ptr(out), odt, ldy, _stream_of(X)),
            "qgemm_w4_blockwise")
@@ -720,6 +730,7 @@ def qgemm_w4_experts(X: torch.Tensor, blobs: torch.Tensor, info: PackedInfo, off
     if bias is not None:
         _f32(bias, "bias")
         assert bias.numel() == E * info.N, "bias must hold experts x N values"
+    _one_gpu("qgemm_w4_experts", X, blobs, offsets, bias, rows, out)
     _check(_lib.qgemm_w4_experts(_ptr(X), dt, x_rows, K, ldx, _ptr(rows), row_div, M,
                                  C.byref(info), _ptr(blobs), blobs.stride(0), E, _ptr(offsets),
                                  _ptr(bias), clamp_lo, clamp_hi, _ptr(out), odt, ldy,
@@ -748,6 +759,7 @@ def qgemm_w4_blockwise_dx(dY: torch.Tensor, blob: torch.Tensor, info: PackedInfo
                           ws=None):
     """The gradient of qgemm_w4_blockwise to its rows: dX = dY @ W."""
     dt, M, lddy, out, lddx, ws, n = _dx_buffers(dY, info, 1, out, ws)
+    _one_gpu("qgemm_w4_blockwise_dx", dY, blob, out, ws)
     _check(_lib.qgemm_w4_blockwise_dx(_ptr(dY), dt, M, lddy, C.byref(info), _ptr(blob), _ptr(out),
                                       lddx, _ptr(ws), n, _stream_of(dY)), "qgemm_w4_blockwise_dx")
     return out
@@ -758,6 +770,7 @@ def qgemm_w4_experts_dx(dY: torch.Tensor, blobs: torch.Tensor, info: PackedInfo,
     """The gradient of qgemm_w4_experts to its (sorted) rows."""
     E = _experts(blobs, offsets)
     dt, M, lddy, out, lddx, ws, n = _dx_buffers(dY, info, E, out, ws)
+    _one_gpu("qgemm_w4_experts_dx", dY, blobs, offsets, out, ws)
     _check(_lib.qgemm_w4_experts_dx(_ptr(dY), dt, M, lddy, C.byref(info), _ptr(blobs),
                                     blobs.stride(0), E, _ptr(offsets), _ptr(out), lddx, _ptr(ws), n,
                                     _stream_of(dY)), "qgemm_w4_experts_dx")
@@ -798,6 +811,7 @@ def qmoe_sort(ids: torch.Tensor, experts: int, ws=None):
     slot_of_row [T*top_k]), int32; ids outside [0, experts) are dropped."""
     idt, T, k, ldi = _ids(ids)
     offsets, ros, sor, ws, n = _sort_buffers(ids, T, k, experts, ws)
+    _one_gpu("qmoe_sort", ids, ws)
     _check(_lib.qmoe_sort(_ptr(ids), idt, T, k, ldi, experts, _ptr(offsets), _ptr(ros), _ptr(sor),
                           _ptr(ws), n, _stream_of(ids)), "qmoe_sort")
     return offsets, ros, sor
@@ -812,6 +826,7 @@ def qmoe_dispatch(X: torch.Tensor, ids: torch.Tensor, experts: int, out=None, ws
     out, odt, ldo = _out(out, T * k, H, X.dtype, X, "out")
     assert odt == dt, "out must be of X's type"
     offsets, ros, sor, ws, n = _sort_buffers(ids, T, k, experts, ws)
+    _one_gpu("qmoe_dispatch", X, ids, out, ws)
     _check(_lib.qmoe_dispatch(_ptr(X), dt, H, ldx, _ptr(ids), idt, T, k, ldi, experts, _ptr(out),
                               ldo, _ptr(offsets), _ptr(ros), _ptr(sor), _ptr(ws), n,
                               _stream_of(X)), "qmoe_dispatch")
@@ -826,6 +841,7 @@ def qmoe_dispatch_grad(dXs: torch.Tensor, row_of_slot: torch.Tensor, out=None):
     assert S == T * k, "dXs must have a row per slot"
     out, odt, ldo = _out(out, T, H, dXs.dtype, dXs, "out")
     assert odt == dt, "out must be of dXs's type"
+    _one_gpu("qmoe_dispatch_grad", dXs, row_of_slot, out)
     _check(_lib.qmoe_dispatch_grad(_ptr(dXs), dt, T, k, H, ld, _ptr(row_of_slot), _ptr(out), ldo,
                                    _stream_of(dXs)), "qmoe_dispatch_grad")
     return out
@@ -846,6 +862,7 @@ def qmoe_combine(Z: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tens
     dt, T, k, H, ldz, ldw = _combine_args(Z, row_of_slot, weights)
     out, odt, ldo = _out(out, T, H, Z.dtype, Z, "out")
     assert odt == dt, "out must be of Z's type"
+    _one_gpu("qmoe_combine", Z, row_of_slot, weights, out)
     _check(_lib.qmoe_combine(_ptr(Z), dt, T, k, H, ldz, _ptr(row_of_slot), _ptr(weights), ldw,
                              _ptr(out), ldo, _stream_of(Z)), "qmoe_combine")
     return out
@@ -864,6 +881,7 @@ def qmoe_combine_grad(dY: torch.Tensor, Z: torch.Tensor, row_of_slot: torch.Tens
     assert odt == dt, "out must be of Z's type"
     out_weights, wdt, lddw = _out(out_weights, T, k, torch.float32, Z, "out_weights")
     assert wdt == QP_F32, "out_weights must be float32"
+    _one_gpu("qmoe_combine_grad", Z, dY, row_of_slot, slot_of_row, weights, out, out_weights)
     _check(_lib.qmoe_combine_grad(_ptr(dY), lddy, _ptr(Z), ldz, dt, T, k, H, _ptr(row_of_slot),
                                   _ptr(slot_of_row), _ptr(weights), ldw, _ptr(out), ldo,
                                   _ptr(out_weights), lddw, _stream_of(Z)), "qmoe_combine_grad")

@@ -1,0 +1,112 @@
+"""What the binding of the float operators over int4 blobs and experts looks at
+before anything reaches the library: where its tensors are.
+No GPU needed: a tensor that says it is on card 0 stands for one that
+is, and every call here is refused before its address is used."""
+import pytest
+import torch
+
+
+class OnCard(torch.Tensor):
+    """A host tensor that gives card 0 as its place."""
+
+    def get_device(self):
+        return 0
+
+
+def _card(t):
+    return t.as_subclass(OnCard)
+
+
+@pytest.fixture(scope="module")
+def qp():
+    import conv_qpack_weights_amd as qp
+    return qp
+
+
+@pytest.fixture
+def no_launch(qp, monkeypatch):
+    """The library's entry points replaced: a call that gets as far is a failure."""
+    reached = []
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_ws_size"):
+                return getattr(real, name)
+            return lambda *a: reached.append(name) or qp.QP_OK
+
+    real = qp._lib
+    monkeypatch.setattr(qp, "_lib", Lib())
+    monkeypatch.setattr(qp, "_stream_of", lambda t: None)
+    return reached
+
+
+def _info(qp, N=48, K=64):
+    """The description of f32-scaled int4 weights in groups of 32."""
+    i = qp.PackedInfo()
+    up = lambda a, b: -(-a // b) * b
+    i.format, i.scheme, i.N, i.K, i.group = 2, qp.QP_BLOCKWISE, N, K, 32
+    i.Npad, i.Kpad = up(N, 64), up(K, 128)
+    i.data_off, i.data_bytes = 256, i.Npad * i.Kpad // 2
+    i.scale_off = 256 + up(i.data_bytes, 256)
+    i.sum_off = i.scale_off + up(16 * i.Npad * (-(-(i.Kpad // 32) // 4)), 256)
+    i.total_bytes = i.sum_off + up(4 * i.Npad, 256)
+    return i
+
+
+def _calls(qp, i):
+    """Every operator with arguments that fit: {name: (function, tensors by name)}."""
+    ints = lambda *shape: torch.zeros(*shape, dtype=torch.int32)
+    bytes_ = lambda *shape: torch.zeros(*shape, dtype=torch.uint8)
+    n = i.total_bytes
+    f = lambda *shape: torch.zeros(*shape)
+    return {
+        "qgemm_w4_blockwise": (
+            lambda X, blob, bias, out: qp.qgemm_w4_blockwise(X, blob, i, bias, out=out),
+            dict(X=f(4, 64), blob=bytes_(n), bias=f(48), out=f(4, 48))),
+        "qgemm_w4_experts": (
+            lambda X, blobs, offsets, bias, rows, out: qp.qgemm_w4_experts(
+                X, blobs, i, offsets, bias, rows=rows, out=out),
+            dict(X=f(4, 64), blobs=bytes_(2, n), offsets=ints(3), bias=f(2, 48), rows=ints(4),
+                 out=f(4, 48))),
+        "qgemm_w4_blockwise_dx": (
+            lambda dY, blob, out, ws: qp.qgemm_w4_blockwise_dx(dY, blob, i, out=out, ws=ws),
+            dict(dY=f(4, 48), blob=bytes_(n), out=f(4, 64), ws=bytes_(4096))),
+        "qgemm_w4_experts_dx": (
+            lambda dY, blobs, offsets, out, ws: qp.qgemm_w4_experts_dx(
+                dY, blobs, i, offsets, out=out, ws=ws),
+            dict(dY=f(4, 48), blobs=bytes_(2, n), offsets=ints(3), out=f(4, 64),
+                 ws=bytes_(4096))),
+        "qmoe_sort": (lambda ids, ws: qp.qmoe_sort(ids, 3, ws=ws),
+                      dict(ids=ints(4, 2), ws=bytes_(256))),
+        "qmoe_dispatch": (lambda X, ids, out, ws: qp.qmoe_dispatch(X, ids, 3, out=out, ws=ws),
+                          dict(X=f(4, 64), ids=ints(4, 2), out=f(8, 64), ws=bytes_(256))),
+        "qmoe_dispatch_grad": (
+            lambda dXs, ros, out: qp.qmoe_dispatch_grad(dXs, ros, out=out),
+            dict(dXs=f(8, 64), ros=ints(4, 2), out=f(4, 64))),
+        "qmoe_combine": (
+            lambda Z, ros, weights, out: qp.qmoe_combine(Z, ros, weights, out=out),
+            dict(Z=f(8, 64), ros=ints(4, 2), weights=f(4, 2), out=f(4, 64))),
+        "qmoe_combine_grad": (
+            lambda dY, Z, ros, sor, weights, out, out_weights: qp.qmoe_combine_grad(
+                dY, Z, ros, sor, weights, out=out, out_weights=out_weights),
+            dict(dY=f(4, 64), Z=f(8, 64), ros=ints(4, 2), sor=ints(8), weights=f(4, 2),
+                 out=f(8, 64), out_weights=f(4, 2))),
+    }
+
+
+NAMES = ["qgemm_w4_blockwise", "qgemm_w4_experts", "qgemm_w4_blockwise_dx", "qgemm_w4_experts_dx",
+         "qmoe_sort", "qmoe_dispatch", "qmoe_dispatch_grad", "qmoe_combine", "qmoe_combine_grad"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_tensor_elsewhere_is_refused(qp, no_launch, name):
+    call, tensors = _calls(qp, _info(qp))[name]
+    on_card = {k: _card(t) for k, t in tensors.items()}
+    call(**on_card)
+    assert no_launch == [name]               # the arguments fit as they are
+    for k in tensors:
+        with pytest.raises(AssertionError, match="GPU"):
+            call(**dict(on_card, **{k: tensors[k]}))
+    with pytest.raises(AssertionError, match="on the GPU"):
+        call(**tensors)                      # all of them on the host
+    assert no_launch == [name]
