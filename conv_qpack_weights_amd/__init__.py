@@ -666,6 +666,20 @@ def _one_gpu(what, first, *others):
         assert t is None or t.get_device() == gpu, "%s: its tensors must be on one GPU" % what
 
 
+def _blob(blob, info):
+    assert blob.dtype == torch.uint8 and blob.is_contiguous(), \
+        "the weights must be a contiguous uint8 blob (pack_s4)"
+    assert blob.numel() >= info.total_bytes, "the blob holds %d bytes, its description says %d" % (
+        blob.numel(), info.total_bytes)
+
+
+def _ws_bytes(ws):
+    if ws is None:
+        return 0
+    assert ws.is_contiguous(), "ws must be contiguous"
+    return ws.numel() * ws.element_size()
+
+
 def _f32(t, what):
     assert t is None or (t.dtype == torch.float32 and t.is_contiguous()), \
         "%s must be a contiguous float32 tensor" % what
@@ -698,6 +712,7 @@ def qgemm_w4_blockwise(X: torch.Tensor, blob: torch.Tensor, info: PackedInfo, bi
     if bias is not None:
         _f32(bias, "bias")
         assert bias.numel() == info.N, "bias must hold N values"
+    _blob(blob, info)
     _one_gpu("qgemm_w4_blockwise", X, blob, bias, out)
     _check(_lib.qgemm_w4_blockwise(_ptr(X), dt, M, K, ldx, C.byref(info), _ptr(blob), _ptr(bias),
                                    clamp_lo, clamp_hi, _ptr(out), odt, ldy, _stream_of(X)),
@@ -705,9 +720,11 @@ def qgemm_w4_blockwise(X: torch.Tensor, blob: torch.Tensor, info: PackedInfo, bi
     return out
 
 
-def _experts(blobs, offsets):
+def _experts(blobs, info, offsets):
     assert blobs.dim() == 2 and blobs.dtype == torch.uint8 and blobs.stride(1) == 1, \
         "blobs must be uint8 [experts, bytes] (pack_s4_experts)"
+    assert blobs.shape[1] >= info.total_bytes, "a blob holds %d bytes, its description says %d" % (
+        blobs.shape[1], info.total_bytes)
     _ints(offsets, "offsets")
     E = blobs.shape[0]
     assert offsets.numel() == E + 1, "offsets must hold experts + 1 values"
@@ -721,7 +738,7 @@ def qgemm_w4_experts(X: torch.Tensor, blobs: torch.Tensor, info: PackedInfo, off
     and bias [E, N].  ``rows`` [M] int32 with ``row_div``: row r reads
     X[rows[r] // row_div] (slot_of_row and top_k: no sorted copy needed)."""
     dt, x_rows, K, ldx = _rows(X, "X")
-    E = _experts(blobs, offsets)
+    E = _experts(blobs, info, offsets)
     M = x_rows
     if rows is not None:
         _ints(rows, "rows")
@@ -752,12 +769,13 @@ def _dx_buffers(dY, info, experts, out, ws):
     if ws is None:
         n = qgemm_w4_dx_ws_size(M, info, experts)
         ws = _alloc_bytes(n, dY.device) if n else None
-    return dt, M, lddy, out, lddx, ws, 0 if ws is None else ws.numel()
+    return dt, M, lddy, out, lddx, ws, _ws_bytes(ws)
 
 
 def qgemm_w4_blockwise_dx(dY: torch.Tensor, blob: torch.Tensor, info: PackedInfo, out=None,
                           ws=None):
     """The gradient of qgemm_w4_blockwise to its rows: dX = dY @ W."""
+    _blob(blob, info)
     dt, M, lddy, out, lddx, ws, n = _dx_buffers(dY, info, 1, out, ws)
     _one_gpu("qgemm_w4_blockwise_dx", dY, blob, out, ws)
     _check(_lib.qgemm_w4_blockwise_dx(_ptr(dY), dt, M, lddy, C.byref(info), _ptr(blob), _ptr(out),
@@ -768,7 +786,7 @@ def qgemm_w4_blockwise_dx(dY: torch.Tensor, blob: torch.Tensor, info: PackedInfo
 def qgemm_w4_experts_dx(dY: torch.Tensor, blobs: torch.Tensor, info: PackedInfo,
                         offsets: torch.Tensor, out=None, ws=None):
     """The gradient of qgemm_w4_experts to its (sorted) rows."""
-    E = _experts(blobs, offsets)
+    E = _experts(blobs, info, offsets)
     dt, M, lddy, out, lddx, ws, n = _dx_buffers(dY, info, E, out, ws)
     _one_gpu("qgemm_w4_experts_dx", dY, blobs, offsets, out, ws)
     _check(_lib.qgemm_w4_experts_dx(_ptr(dY), dt, M, lddy, C.byref(info), _ptr(blobs),
@@ -803,7 +821,7 @@ def _sort_buffers(ids, T, k, experts, ws):
         ws = _alloc_bytes(n, ids.device) if n else None
     offsets, ros, sor = ids.new_empty(experts + 1 + 2 * S, dtype=torch.int32).split_with_sizes(
         (experts + 1, S, S))
-    return offsets, ros.view(T, k), sor, ws, 0 if ws is None else ws.numel()
+    return offsets, ros.view(T, k), sor, ws, _ws_bytes(ws)
 
 
 def qmoe_sort(ids: torch.Tensor, experts: int, ws=None):

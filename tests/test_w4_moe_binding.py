@@ -1,6 +1,6 @@
 """What the binding of the float operators over int4 blobs and experts looks at
-before anything reaches the library: where its tensors are.
-No GPU needed: a tensor that says it is on card 0 stands for one that
+before anything reaches the library: where its tensors are and how large their
+buffers.  No GPU needed: a tensor that says it is on card 0 stands for one that
 is, and every call here is refused before its address is used."""
 import pytest
 import torch
@@ -110,3 +110,36 @@ def test_a_tensor_elsewhere_is_refused(qp, no_launch, name):
     with pytest.raises(AssertionError, match="on the GPU"):
         call(**tensors)                      # all of them on the host
     assert no_launch == [name]
+
+
+@pytest.mark.parametrize("name", [n for n in NAMES if n.startswith("qgemm")])
+def test_a_blob_shorter_than_its_description_is_refused(qp, no_launch, name):
+    call, tensors = _calls(qp, _info(qp))[name]
+    on_card = {k: _card(t) for k, t in tensors.items()}
+    key = "blobs" if "experts" in name else "blob"
+    blob = tensors[key]
+    short = blob[..., :-1].contiguous()
+    with pytest.raises(AssertionError, match="holds"):
+        call(**dict(on_card, **{key: _card(short)}))
+    if key == "blobs":                       # one expert's, too
+        with pytest.raises(AssertionError, match="holds"):
+            call(**dict(on_card, blobs=_card(short[:1]), offsets=on_card["offsets"][:2],
+                        **({"bias": on_card["bias"][:1]} if "bias" in tensors else {})))
+    else:
+        apart = torch.zeros(2 * blob.numel(), dtype=torch.uint8)[::2]
+        with pytest.raises(AssertionError, match="contiguous"):
+            call(**dict(on_card, blob=_card(apart)))
+        with pytest.raises(AssertionError, match="uint8"):
+            call(**dict(on_card, blob=_card(torch.zeros(blob.numel()))))
+    assert no_launch == []
+
+
+@pytest.mark.parametrize("name", ["qgemm_w4_blockwise_dx", "qgemm_w4_experts_dx", "qmoe_sort",
+                                  "qmoe_dispatch"])
+def test_a_workspace_with_gaps_is_refused(qp, no_launch, name):
+    call, tensors = _calls(qp, _info(qp))[name]
+    on_card = {k: _card(t) for k, t in tensors.items()}
+    gaps = torch.zeros(2 * tensors["ws"].numel(), dtype=torch.uint8)[::2]
+    with pytest.raises(AssertionError, match="contiguous"):
+        call(**dict(on_card, ws=_card(gaps)))
+    assert no_launch == []
