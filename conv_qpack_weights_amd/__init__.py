@@ -258,18 +258,34 @@ def pack_s8_blockwise(w: torch.Tensor, scales: torch.Tensor, block=128, into=Non
     return qpack_weights(w, desc, k_axis, n_axis, into)
 
 
+def _group_values(t, w, group_size, what):
+    """The groups' scales or offsets as the packer reads them: contiguous f32,
+    one per channel and group."""
+    assert t.is_floating_point(), "%s must be floating point" % what
+    if group_size > 0 and w.dim() in (2, 4):   # (else the library says what is wrong)
+        N, K = w.shape[0], w.shape[1:].numel()
+        want = N * -(-K // group_size)
+        assert t.numel() == want, "%s must hold %d values (one per channel and group), not %d" % (
+            what, want, t.numel())
+    return t.float().contiguous()
+
+
 def pack_s4(w: torch.Tensor, scales: torch.Tensor, group_size=32, scale_dtype="f32",
             offsets=None, into=None):
     """Pack int4 values (one per int8 byte, in [-8,7]) given as [N, K] with
-    f32 group scales [N, ceil(K/group)]; scale_dtype "bf16" stores the
-    scales rounded to bf16; `offsets` [N, ceil(K/group)] makes the weights
+    group scales [N, ceil(K/group)] (f32, or of another float type and
+    converted); scale_dtype "bf16" stores the scales rounded to bf16; `offsets` [N, ceil(K/group)] makes the weights
     asymmetric (real weight = scale*q + offset).  ``into=(blob, info)``
     refills an existing blob of the same shape and format."""
     scheme = {"f32": QP_BLOCKWISE, "bf16": QP_BLOCKWISE_BF16}[scale_dtype]
+    assert w.element_size() == 1, "int4 values must come one per byte"
+    _one_gpu("pack_s4", w, scales, offsets)
+    scales = _group_values(scales, w, group_size, "scales")
     if offsets is not None:
         assert scale_dtype == "f32", "asymmetric int4 keeps f32 scales"
         scheme = QP_BLOCKWISE_ASYM
-        scales = torch.stack((offsets.float(), scales.float()), dim=-1).contiguous()
+        offsets = _group_values(offsets, w, group_size, "offsets")
+        scales = torch.stack((offsets, scales), dim=-1).contiguous()
     desc = qtensor(QP_S4, list(w.shape), list(w.stride()), scheme=scheme, scales=scales,
                    group_size=group_size, axis=0)
     return qpack_weights(w, desc, 1, 0, into)
@@ -690,7 +706,10 @@ def pack_s4_experts(w: torch.Tensor, scales: torch.Tensor, group_size=32, scale_
     """Pack the int4 weights of a set of experts, [E, N, K] with scales (and
     offsets) [E, N, ceil(K/group)]: returns (blobs uint8 [E, bytes], info),
     expert e's blob at blobs[e]."""
-    assert w.dim() == 3 and w.shape[0] >= 1
+    assert w.dim() == 3 and w.shape[0] >= 1, "w must be [experts, N, K]"
+    for t in (scales,) if offsets is None else (scales, offsets):
+        assert t.dim() == 3 and t.shape[:2] == w.shape[:2], \
+            "scales and offsets must be [experts, N, groups]"
     blobs = info = None
     for e in range(w.shape[0]):
         off = None if offsets is None else offsets[e]

@@ -143,3 +143,81 @@ def test_a_workspace_with_gaps_is_refused(qp, no_launch, name):
     with pytest.raises(AssertionError, match="contiguous"):
         call(**dict(on_card, ws=_card(gaps)))
     assert no_launch == []
+
+
+# ---------------------------------------------------------------- packing int4 weights
+@pytest.fixture
+def packed(qp, monkeypatch):
+    """What pack_s4 hands to the packer: the values at the scales' address."""
+    import ctypes as C
+    import numpy as np
+    seen = []
+
+    def pack(w, desc, k_axis, n_axis, into=None):
+        groups = -(-w.shape[1] // desc.group_size) * (2 if desc.scheme == qp.QP_BLOCKWISE_ASYM else 1)
+        at = (C.c_float * (w.shape[0] * groups)).from_address(desc.scales)
+        seen.append(np.array(at).reshape(w.shape[0], groups))
+        return (torch.zeros(256, dtype=torch.uint8), None) if into is None else into
+
+    monkeypatch.setattr(qp, "qpack_weights", pack)
+    monkeypatch.setattr(qp, "_alloc_bytes", lambda n, device: torch.empty(n, dtype=torch.uint8))
+    return seen
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16, torch.float64])
+@pytest.mark.parametrize("layout", ["plain", "transposed", "every other"])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "asym"])
+def test_scales_of_any_float_type_and_layout(qp, packed, dtype, layout, kind):
+    """The packer reads f32 values one behind the other: bf16 scales, or a view
+    with strides, have to be laid out that way first."""
+    E, N, K, group = 3, 5, 100, 32
+    G = 4
+    g = torch.Generator().manual_seed(1)
+
+    def make():
+        v = (0.5 + torch.rand(E, N, G, generator=g)).to(torch.bfloat16).to(dtype)
+        if layout == "transposed":
+            t = v.transpose(1, 2).contiguous().transpose(1, 2)
+        elif layout == "every other":
+            t = torch.zeros(E, N, 2 * G, dtype=v.dtype)[:, :, ::2]
+            t.copy_(v)
+        else:
+            t = v
+        return t, v.double()
+
+    scales, s = make()
+    offsets, o = make() if kind == "asym" else (None, None)
+    w = torch.zeros(E, N, K, dtype=torch.int8)
+    card = lambda t: None if t is None else _card(t)
+    qp.pack_s4(card(w[0]), card(scales[0]), group, "bf16" if kind == "bf16" else "f32",
+               card(None if offsets is None else offsets[0]))
+    qp.pack_s4_experts(card(w), card(scales), group, "bf16" if kind == "bf16" else "f32",
+                       card(offsets))
+    want = s if o is None else torch.stack((o, s), dim=-1).flatten(2)
+    assert len(packed) == 1 + E
+    for got, e in zip(packed, [0, *range(E)]):
+        assert (torch.from_numpy(got).double() == want[e]).all()
+
+
+def test_scales_that_do_not_fit_are_refused(qp, packed):
+    w, s = _card(torch.zeros(2, 5, 100, dtype=torch.int8)), _card(torch.ones(2, 5, 4))
+    for bad in (s[0, :, :3], s[0, :4], s[0].to(torch.int32)):
+        with pytest.raises(AssertionError, match="scales"):
+            qp.pack_s4(w[0], bad)
+        with pytest.raises(AssertionError, match="offsets"):
+            qp.pack_s4(w[0], s[0], offsets=bad)
+    for bad in (s[:1], s[0], s[:, :, :3], s[:, :4]):
+        with pytest.raises(AssertionError):
+            qp.pack_s4_experts(w, bad)
+        with pytest.raises(AssertionError):
+            qp.pack_s4_experts(w, s, offsets=bad)
+    with pytest.raises(AssertionError, match="byte"):
+        qp.pack_s4(_card(torch.zeros(5, 100, dtype=torch.int32)), s[0])
+    host = torch.ones(5, 4)
+    with pytest.raises(AssertionError, match="GPU"):
+        qp.pack_s4(w[0], host)
+    with pytest.raises(AssertionError, match="GPU"):
+        qp.pack_s4(w[0], s[0], offsets=host)
+    with pytest.raises(AssertionError, match="GPU"):
+        qp.pack_s4(torch.zeros(5, 100, dtype=torch.int8), s[0])
+    assert packed == []
