@@ -116,6 +116,7 @@ SIGNATURES = {
                                         _P]),
     "qgemm_w4_experts_dx": (C.c_int, [_P, _I32, _I64, _I64, _PI, _P, _I64, _I64, _P, _P, _I64, _P,
                                       C.c_size_t, _P]),
+    "qgemm_w4_kernel_name": (C.c_int, [_I64, _PI, _I32, _I64, _I32, C.c_char_p, C.c_size_t]),
     "qmoe_sort_ws_size": (C.c_int, [_I64, _I64, _I64, _SZ]),
     "qmoe_sort": (C.c_int, [_P, _I32, _I64, _I64, _I64, _I64, _P, _P, _P, _P, C.c_size_t, _P]),
     "qmoe_dispatch": (C.c_int, [_P, _I32, _I64, _I64, _P, _I32, _I64, _I64, _I64, _I64, _P, _I64,
@@ -812,6 +813,15 @@ def qgemm_w4_experts_dx(dY: torch.Tensor, blobs: torch.Tensor, info: PackedInfo,
                                     blobs.stride(0), E, _ptr(offsets), _ptr(out), lddx, _ptr(ws), n,
                                     _stream_of(dY)), "qgemm_w4_experts_dx")
     return out
+
+
+def qgemm_w4_kernel_name(M: int, info: PackedInfo, dtype: torch.dtype, experts=1,
+                         gradient=False) -> str:
+    """Which kernel qgemm_w4_* (or with `gradient` its _dx) takes for M rows."""
+    name = C.create_string_buffer(32)
+    _check(_lib.qgemm_w4_kernel_name(M, C.byref(info), _FLOAT[dtype], experts, int(gradient), name,
+                                     len(name)), "qgemm_w4_kernel_name")
+    return name.value.decode()
 
 
 # ---------------------------------------------------------------- rows by expert

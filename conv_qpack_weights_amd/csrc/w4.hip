@@ -6,6 +6,8 @@
 // goes into the MFMA exactly, so the only roundings are those of the f32
 // sums; the scales multiply the f32 group sums.  q enters as q/16 (what the
 // 4-bit conversion gives); the factor 16 leaves exactly at the end.
+#include <cstdio>
+
 #include "w4.hpp"
 
 namespace qp {
@@ -31,33 +33,32 @@ constexpr ShapeCost kShapes[] = {
     {kTile4x8, 4, 8, 42.0, 21.7}, {kTile8x8, 8, 8, 59.0, 42.0},
 };
 
-W4Shape w4_choose(const W4Args& a) {
-  const double experts = a.rows.offsets ? (double)(a.rows.experts < a.rows.M ? a.rows.experts
-                                                                             : a.rows.M)
-                                        : 1.0;
-  const double each = (double)a.rows.M / experts;  // rows of an expert, if all were alike
-  W4Shape best = kRows1x1;
+const ShapeCost& w4_choose(int64_t M, int64_t parts, int64_t Npad) {
+  const double experts = (double)(parts < M ? parts : M);
+  const double each = (double)M / experts;  // rows of an expert, if all were alike
+  const ShapeCost* best = kShapes;
   double least = 1e300;
   for (const ShapeCost& s : kShapes) {
     // row tiles of an expert: its last one is half empty on average
-    double tiles = (double)ceil_div(a.rows.M, 16 * s.rows);
+    double tiles = (double)ceil_div(M, 16 * s.rows);
     if (experts > 1.0) {
       tiles = each / (16 * s.rows) + 0.5;
       tiles = experts * (tiles > 1.0 ? tiles : 1.0);
     }
-    const double groups = tiles * (double)ceil_div(a.w.Npad / 16, s.tiles);
+    const double groups = tiles * (double)ceil_div(Npad / 16, s.tiles);
     const double rounds = groups <= 256.0 ? 0.0 : (double)(int64_t)((groups + 255.0) / 256.0) - 1.0;
     const double cost = s.first + s.more * rounds;
     if (cost < least) {
       least = cost;
-      best = s.shape;
+      best = &s;
     }
   }
-  return best;
+  return *best;
 }
 
 qp_status run_w4(const W4Args& a, int32_t dtype, int32_t format, hipStream_t stream) {
-  const W4Shape shape = w4_choose(a);
+  const W4Shape shape =
+      w4_choose(a.rows.M, a.rows.offsets ? a.rows.experts : 1, a.w.Npad).shape;
   if (dtype == QP_F32) return run_w4_f32(a, format, shape, stream);
   if (dtype == QP_BF16) return run_w4_bf16(a, format, shape, stream);
   return run_w4_f16(a, format, shape, stream);
@@ -182,4 +183,29 @@ extern "C" qp_status qgemm_w4_experts(const void* X, int32_t dtype, int64_t x_ro
            W4Rows{offsets, (int32_t)experts, M, rows, rows ? row_div : 1, x_rows},
            X, ldx, bias, clamp_lo, clamp_hi, Y, y_dtype, ldy};
   return run_w4(a, dtype, w->format, stream);
+}
+
+extern "C" qp_status qgemm_w4_kernel_name(int64_t M, const qp_packed_info* w, int32_t dtype,
+                                          int64_t experts, int32_t gradient, char* name,
+                                          size_t bytes) {
+  using namespace qp;
+  clear_error();
+  const char* what = "qgemm_w4_kernel_name";
+  QP_REQUIRE(w && w->format >= 2 && w->format <= 4, QP_EINVAL, "%s: weights must be an int4 blob",
+             what);
+  QP_REQUIRE(M >= 1 && M <= kW4MaxRows && experts >= 1 && w->N > 0 && w->K > 0, QP_EINVAL,
+             "%s: needs a row and an expert", what);
+  QP_REQUIRE(dtype == QP_F32 || dtype == QP_BF16 || dtype == QP_F16, QP_EINVAL,
+             "%s: rows must be QP_F32, QP_BF16 or QP_F16 (got %d)", what, dtype);
+  QP_REQUIRE(name && bytes >= 16, QP_EINVAL, "%s: needs room for 16 characters", what);
+  if (gradient) {
+    w4_dx_kernel_name(M, w, dtype, experts, name, bytes);
+    return QP_OK;
+  }
+  const ShapeCost& s = w4_choose(M, experts, w->Npad);
+  const bool tile = s.shape == kTile4x8 || s.shape == kTile8x8;
+  // (f32 rows take the 64-row tile for either)
+  std::snprintf(name, bytes, "%s%dx%d", tile ? "tile" : "rows",
+                tile && dtype == QP_F32 ? 4 : s.rows, s.tiles);
+  return QP_OK;
 }

@@ -287,6 +287,10 @@ qp_status run_w4_f32(const W4Args& a, int32_t format, W4Shape shape, hipStream_t
 qp_status run_w4_bf16(const W4Args& a, int32_t format, W4Shape shape, hipStream_t stream);
 qp_status run_w4_f16(const W4Args& a, int32_t format, W4Shape shape, hipStream_t stream);
 
+// the gradient's kernel for M rows, see qgemm_w4_kernel_name
+void w4_dx_kernel_name(int64_t M, const qp_packed_info* w, int32_t dtype, int64_t experts,
+                       char* name, size_t bytes);
+
 W4View w4_view(const qp_packed_info* w, const void* packed, int64_t expert_stride);
 qp_status w4_check_weights(const char* what, const qp_packed_info* w, const void* packed,
                            int64_t experts, int64_t expert_stride);

@@ -20,6 +20,7 @@
 // cost an unpacking only, and f16 rows take two MFMAs instead of three, f32 rows
 // three instead of six.
 #include <atomic>
+#include <cstdio>
 #include <type_traits>
 
 #include "w4.hpp"
@@ -726,6 +727,15 @@ int64_t dx_ws_bytes(int64_t M, int64_t experts, int64_t N, int64_t K) {
   return p.splits == 1 ? 0 : round_up(p.splits * M * round_up(K, 128) * 4, 256);
 }
 
+// The tile kernel is for bf16: the pieces of f16 and f32 rows leave it no more
+// rows a workgroup than the other has (f16: 242 us against 231 at 2048 rows).
+// It addresses its rows by 32-bit offsets from the tile's first.
+bool dx_takes_tile(int64_t M, int64_t experts, int64_t N, int64_t K, int32_t dtype, int64_t lddy,
+                   const DxPlan& p) {
+  return dtype == QP_BF16 && 128 * lddy * 2 < (INT64_C(1) << 32) &&
+         dx_tile_cost(M, experts, N, K) < p.cost;
+}
+
 template <typename T, int kKind, bool kOne>
 qp_status launch_dx_frags(const W4DxArgs& a, const DxPlan& p, float* part, hipStream_t stream) {
   if (p.frags == 1) return launch_dx_rows<T, kKind, kOne, 1>(a, p.splits, part, stream);
@@ -737,12 +747,8 @@ template <typename T, int kKind>
 qp_status launch_dx(const W4DxArgs& a, void* ws, hipStream_t stream) {
   const int64_t M = a.rows.M, experts = a.rows.offsets ? a.rows.experts : 1;
   const DxPlan p = dx_plan(M, experts, a.w.N, a.w.K);
-  // The tile kernel is for bf16: the pieces of f16 and f32 rows leave it no more
-  // rows a workgroup than the other has (f16: 242 us against 231 at 2048 rows).
-  // It addresses its rows by 32-bit offsets from the tile's first.
   if constexpr (__is_same(T, bf16_t)) {
-    if (128 * a.lddy * (int64_t)sizeof(T) < (INT64_C(1) << 32) &&
-        dx_tile_cost(M, experts, a.w.N, a.w.K) < p.cost)
+    if (dx_takes_tile(M, experts, a.w.N, a.w.K, a.dtype, a.lddy, p))
       return launch_dx_tile<T, kKind, 4>(a, stream);
   }
   float* part = static_cast<float*>(ws);
@@ -782,6 +788,16 @@ qp_status dx_entry(const char* what, const void* dY, int32_t dtype, int64_t M, i
 }
 
 }  // namespace
+
+void w4_dx_kernel_name(int64_t M, const qp_packed_info* w, int32_t dtype, int64_t experts,
+                       char* name, size_t bytes) {
+  const DxPlan p = dx_plan(M, experts, w->N, w->K);
+  if (dx_takes_tile(M, experts, w->N, w->K, dtype, w->N, p))
+    std::snprintf(name, bytes, "tile");
+  else
+    std::snprintf(name, bytes, "rows%d/%d", p.frags, (int)p.splits);
+}
+
 }  // namespace qp
 
 extern "C" qp_status qgemm_w4_dx_ws_size(int64_t M, const qp_packed_info* w, int64_t experts,

@@ -627,6 +627,16 @@ qp_status qgemm_w4_experts_dx(const void* dY, int32_t dtype, int64_t M, int64_t 
                               hipStream_t stream);
 
 /*
+ * qgemm_w4_kernel_name -- which kernel the products (gradient = 0) or their
+ *   gradients (1) take for M rows of `dtype`, dense or (experts > 1) by expert:
+ *   for profiles and tests, on the host alone.  name: "rows1x3" is 16 rows by
+ *   48 channels a workgroup, "tile8x8" 128 by 128 over LDS; gradients "rows2/4"
+ *   (32 rows, the channels in 4 splits) or "tile".
+ */
+qp_status qgemm_w4_kernel_name(int64_t M, const qp_packed_info* w, int32_t dtype, int64_t experts,
+                               int32_t gradient, char* name, size_t bytes);
+
+/*
  * Rows of tokens sorted by expert and back.  T tokens choose top_k experts
  * each; slot s = t*top_k + j is one choice.  A slot whose id is negative or
  * >= experts is dropped.
