@@ -572,6 +572,11 @@ qp_status qconv2d_s8_blockwise_f32(const qp_qtensor* x, const int8_t* X, const q
  * A row with an infinity or a NaN gives what the sum gives; other rows are
  * not touched by it.  Run to run the same bits.  Outputs of this and the
  * following operators must not overlap their inputs.
+ * Range: x q/16 is summed over a group, up to 128 K at a time, before the scale
+ * multiplies it.  f32 and bf16 rows of values up to 2^121 are always safe; above,
+ * a sum that passes 2^128 gives an infinity or a NaN, also where the scale would
+ * bring it back.  f32 values are held to 2^-133, so those below 2^-109 have fewer
+ * than 24 bits; results below 2^-122 step by 2^-145.
  * Errors: QP_EINVAL on shapes, types, NaN or reversed bounds; QP_EALIGN;
  * QP_EUNSUPPORTED above 2^30 rows or where a launch would pass 2^32 threads
  * (16 rows by 64 channels take 512 at most).
