@@ -53,9 +53,12 @@ __device__ __forceinline__ float high_f32(uint32_t p) {
 
 // Eight values as kPieces bf16 each, largest first: every piece is what the
 // ones before it leave, rounded to nearest, so n pieces miss at most 2^-8n of
-// the value.  kAny: where the first piece is an infinity or a NaN (the value is
-// one, or rounds up to one) the others are zero; without it they are NaN.
-template <int kPieces, bool kAny>
+// the value.  What may be among them: kFinite only values that round to finite
+// ones (of others the later pieces are NaN); kSpecial infinities and NaNs too,
+// whose later pieces are zero; kAnySize also finite values above the largest bf16,
+// whose first piece is that largest one and not the infinity they round to.
+enum SplitRange { kFinite, kSpecial, kAnySize };
+template <int kPieces, SplitRange kRange>
 __device__ __forceinline__ void split_bf16(const float (&f)[8], bf16x8 (&o)[kPieces]) {
   u32x4 p[kPieces];
 #pragma unroll
@@ -63,16 +66,27 @@ __device__ __forceinline__ void split_bf16(const float (&f)[8], bf16x8 (&o)[kPie
     float a = f[2 * i], b = f[2 * i + 1];
 #pragma unroll
     for (int n = 0; n < kPieces; ++n) {
-      uint32_t h = bf16_pair(a, b);
+      bool fa = true, fb = true;
+      float ca = a, cb = b;
+      if (kRange != kFinite && n == 0) {
+        fa = __builtin_fabsf(a) < __builtin_inff();  // (not a NaN either)
+        fb = __builtin_fabsf(b) < __builtin_inff();
+      }
+      if (kRange == kAnySize && n == 0) {
+        constexpr float kLargest = 0x1.fep127f;
+        ca = fa ? __builtin_amdgcn_fmed3f(a, -kLargest, kLargest) : a;
+        cb = fb ? __builtin_amdgcn_fmed3f(b, -kLargest, kLargest) : b;
+      }
+      uint32_t h = bf16_pair(ca, cb);
       // (opaque: the compiler would round `a` once more to find the low half)
       asm("" : "+v"(h));
       p[n][i] = h;
       if (n + 1 < kPieces) {
         a = a - low_f32(h);
         b = b - high_f32(h);
-        if (kAny && n == 0) {
-          a = a == a && __builtin_fabsf(a) != __builtin_inff() ? a : 0.0f;
-          b = b == b && __builtin_fabsf(b) != __builtin_inff() ? b : 0.0f;
+        if (kRange != kFinite && n == 0) {
+          a = fa ? a : 0.0f;
+          b = fb ? b : 0.0f;
         }
       }
     }
@@ -112,7 +126,7 @@ struct YFrag<f16_t> {
   __device__ __forceinline__ void split(bf16x8 (&o)[2]) const {
     float f[8];
     values(f);
-    split_bf16<2, true>(f, o);
+    split_bf16<2, kSpecial>(f, o);
   }
 };
 template <>
@@ -129,7 +143,7 @@ struct YFrag<float> {
   __device__ __forceinline__ void split(bf16x8 (&o)[3]) const {
     float f[8];
     values(f);
-    split_bf16<3, true>(f, o);
+    split_bf16<3, kAnySize>(f, o);
   }
 };
 
@@ -198,7 +212,7 @@ __device__ __forceinline__ void dx_column(const DxWeights<kKind>& w, const uint3
     f[r] = nib_f32((x >> (8 * (j & 3))) & 0xffu) * s16[r];
     if constexpr (kKind == 2) f[r] = f[r] + w.o[r];
   }
-  split_bf16<NW, false>(f, o);
+  split_bf16<NW, kFinite>(f, o);
 }
 
 template <int kKind>
@@ -295,7 +309,7 @@ __global__ __launch_bounds__(kWaves * 64) void w4_dx_rows_kernel(W4DxArgs a, uin
           yf[m].values(f);
 #pragma unroll
           for (int r = 0; r < 8; ++r) f[r] = f[r] * w.scale(r);
-          split_bf16<NS, true>(f, y[m]);
+          split_bf16<NS, kAnySize>(f, y[m]);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

@@ -618,8 +618,12 @@ qp_status qgemm_w4_experts(const void* X, int32_t dtype, int64_t x_rows, int64_t
  *   ws       device workspace of qgemm_w4_dx_ws_size bytes (0: may be NULL),
  *            256-byte aligned.  experts = 1 for the dense product.
  * Each term dY * W is formed to within 2^-15 of itself (2^-22 for f32 rows;
- * terms below 2^-100 have fewer bits), sums are f32.  A row of dY with an infinity or a NaN gives infinities or
- * NaNs in that row of dX, not always which of the two the sum would give.
+ * terms below 2^-100 have fewer bits), sums are f32.  A row of dY with an
+ * infinity or a NaN gives infinities or NaNs in that row of dX, not always which
+ * of the two the sum would give.  Finite rows of dY may hold any values, if the
+ * scales are below 2^123 and the weights s q (+ o) below 2^127, and for groups of
+ * 128 on without offsets if dY s stays below 2^128 (else infinities or NaNs, also
+ * where q is 0).
  */
 qp_status qgemm_w4_dx_ws_size(int64_t M, const qp_packed_info* w, int64_t experts, size_t* bytes);
 qp_status qgemm_w4_blockwise_dx(const void* dY, int32_t dtype, int64_t M, int64_t lddy,
