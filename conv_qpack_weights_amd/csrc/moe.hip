@@ -466,7 +466,8 @@ __global__ __launch_bounds__(256) void moe_combine_grad_kernel(
         const int64_t r = row_of_slot[s];
         row[j] = r < S ? r : -1;
         w[j] = weights[t * ldw + j0 + j];
-        bare[j] = slot_of_row[s] < 0;
+        const int64_t slot = slot_of_row[s];
+        bare[j] = slot < 0 || slot >= S;
       }
     }
     for (int64_t h0 = (int64_t)threadIdx.x * kPer; h0 < H; h0 += 256 * kPer) {
