@@ -7,7 +7,7 @@ weights are int4 blobs (packed once), the rows stay in bf16:
               -> silu(gate) * up -> qgemm_w4_experts -> qmoe_combine
     training  qmoe_dispatch, the same products, qmoe_combine, and their gradients
               to the tokens and to the router's weights; the 4-bit weights are
-              frozen (adapters or the router learn)
+              frozen (adapters or the router learn); first derivatives only
 
 Run it on an MI355X:  python examples/moe_w4_layer.py
 """
@@ -33,6 +33,19 @@ def quantize_int4(w, group=32):
     return q.view(E, N, G * group)[:, :, :K].contiguous(), scale
 
 
+class _Once(torch.autograd.Function):
+    """A first derivative: still tied to what it depends on, so that to
+    differentiate it again is an error and not a result without its terms."""
+
+    @staticmethod
+    def forward(ctx, compute, *tensors):
+        return compute(*tensors)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("cannot differentiate twice through the expert layer")
+
+
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, ids, experts):
@@ -43,7 +56,9 @@ class _Dispatch(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dxs, *_):
-        return qp.qmoe_dispatch_grad(dxs.contiguous(), ctx.saved_tensors[0]), None, None
+        row_of_slot, = ctx.saved_tensors
+        dx = _Once.apply(lambda d: qp.qmoe_dispatch_grad(d.contiguous(), row_of_slot), dxs)
+        return dx, None, None
 
 
 class _Experts(torch.autograd.Function):
@@ -56,7 +71,9 @@ class _Experts(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         blobs, offsets = ctx.saved_tensors
-        return qp.qgemm_w4_experts_dx(dy.contiguous(), blobs, ctx.info, offsets), None, None, None
+        dx = _Once.apply(
+            lambda d: qp.qgemm_w4_experts_dx(d.contiguous(), blobs, ctx.info, offsets), dy)
+        return dx, None, None, None
 
 
 class _Combine(torch.autograd.Function):
@@ -68,7 +85,9 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         z, weights, row_of_slot, slot_of_row = ctx.saved_tensors
-        dz, dw = qp.qmoe_combine_grad(dy.contiguous(), z, row_of_slot, slot_of_row, weights)
+        dz, dw = _Once.apply(
+            lambda d, z, w: qp.qmoe_combine_grad(d.contiguous(), z, row_of_slot, slot_of_row, w),
+            dy, z, weights)
         return dz, dw, None, None
 
 
