@@ -81,11 +81,17 @@ struct RowPiece {
 // ---- the sort and the copy in one launch, few slots ------------------------
 // A wave per slot finds the slot's row by counting: ids below its own, and
 // equal ids before it, 64 ids a step and a ballot each; up to kSmallSlots
-// slots that is at most 64 steps on ids that sit in LDS.  The token's row is
+// slots that is at most 8 steps on ids that sit in LDS.  The token's row is
 // on its way to registers meanwhile.  Blocks past the slots' own
-// write the offsets.  16 tokens x 2 of 8 experts, rows of 4096 bf16: 3.3 us, of
-// which an empty launch is about 2 (three launches took 12).
-constexpr int kSmallSlots = 4096;
+// write the offsets, a thread per expert walking over all the slots: that is what
+// ends the range of this kernel.  16 tokens x 2 of 8 experts, rows of 4096 bf16:
+// 3.3 us, of which an empty launch is about 2 (three launches took 12).
+// Replayed in a graph, against the kernels for many slots: the sort alone, 128
+// slots of 64 experts 3.4 us (3.8), 256 slots 5.0 (3.7), 1024 15.4 (4.4), 4096
+// 59 (5.8); with rows of 4096 bf16, 256 slots 5.2 (8.7), 512 8.9 (9.2; of 8
+// experts 9.1 and 7.5, of 512 experts 10.5 both), 1024 16.1 (10.3).
+constexpr int kSmallSort = 128;
+constexpr int kSmallSlots = 512;
 constexpr int kSmallVecs = 4;  // 16-byte pieces of a row a lane holds
 
 template <int ES, bool kCopy, int kSmallThreads>
@@ -205,8 +211,7 @@ __device__ __forceinline__ uint64_t same_key(bool live, int32_t key, int bits) {
   return same;
 }
 
-// row_all[s]: the row of every slot, rows past offsets[experts] for dropped
-// ones (null: not wanted).  kSelf: every block counts all the slots itself (a
+// kSelf: every block counts all the slots itself (a
 // launch less, but the count grows with the slots).  Alone, called in a row /
 // replayed in a graph: 5000 slots of 256 experts 10.1 / 6.9 us, with the
 // counting launch 13.5 / 7.9; 12000 of 64 experts 10.8 / 9.3 against 13.0 / 7.0.
@@ -216,7 +221,7 @@ template <bool kSelf>
 __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(
     Ids ids, uint32_t S, uint32_t chunk, const int32_t* __restrict__ counts,
     int32_t* __restrict__ offsets, int32_t* __restrict__ row_of_slot,
-    int32_t* __restrict__ slot_of_row, int32_t* __restrict__ row_all) {
+    int32_t* __restrict__ slot_of_row) {
   __shared__ int32_t at[kSortWaves][kMaxExperts + 1];
   __shared__ int32_t before[2 * kSortThreads];  // partial sums, then the scan
   __shared__ int32_t wave_sum[kSortWaves];
@@ -336,18 +341,18 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(
       const bool kept = key < ids.experts;
       row_of_slot[s] = kept ? row : -1;
       slot_of_row[row] = kept ? (int32_t)s : -1;
-      if (row_all) row_all[s] = row;
     }
   }
 }
 
 // Row copies of many slots: a wave per token and piece of the row; the piece
-// is read once and stored to the token's top_k rows (604 MB in 117 us).
+// is read once and stored to the token's top_k rows (604 MB in 117 us).  Rows
+// without a slot are zeroed by the token whose slots have their numbers.
 constexpr int kCopyVecs = 4;
 template <int ES>
 __global__ __launch_bounds__(256) void moe_copy_kernel(
     const uint8_t* __restrict__ X, int64_t ldx_bytes, int64_t row_elems, int64_t T, int32_t top_k,
-    const int32_t* __restrict__ row_all, const int32_t* __restrict__ total_rows,
+    const int32_t* __restrict__ row_of_slot, const int32_t* __restrict__ slot_of_row,
     uint8_t* __restrict__ Xs, int64_t ldxs_bytes, int64_t first) {
   using RP = RowPiece<ES>;
   constexpr int kPer = RP::kPer;
@@ -362,14 +367,11 @@ __global__ __launch_bounds__(256) void moe_copy_kernel(
     const int64_t e = RP::start(e0 + (int64_t)i * 64 * kPer, row_elems);
     if (e >= 0 && e < row_elems) v[i] = *reinterpret_cast<const typename RP::vec*>(src + e * ES);
   }
-  const int32_t total = *total_rows;
-  for (int j = 0; j < top_k; ++j) {
-    const int32_t row = row_all[t * top_k + j];
-    const bool kept = row < total;
-    uint8_t* dst = Xs + (int64_t)row * ldxs_bytes;
+  auto store = [&](int64_t row, bool kept) {
+    uint8_t* dst = Xs + row * ldxs_bytes;
     if (row_elems < kPer) {
       if (lane == 0) RP::short_row(src, dst, kept, row_elems);
-      continue;
+      return;
     }
 #pragma unroll
     for (int i = 0; i < kCopyVecs; ++i) {
@@ -379,6 +381,12 @@ __global__ __launch_bounds__(256) void moe_copy_kernel(
         *reinterpret_cast<typename RP::vec*>(dst + e * ES) = kept ? v[i] : zero;
       }
     }
+  };
+  for (int j = 0; j < top_k; ++j) {
+    const int64_t s = t * top_k + j;
+    const int32_t row = row_of_slot[s];
+    if (row >= 0) store(row, true);
+    if (slot_of_row[s] < 0) store(s, false);
   }
 }
 
@@ -560,9 +568,9 @@ qp_status check_rows(const char* what, const char* name, const void* p, int64_t 
 }
 
 size_t sort_ws_bytes(int64_t S, int64_t experts) {
-  if (S <= kSmallSlots) return 0;
+  if (S <= kSelfSlots) return 0;
   const int64_t nb = ceil_div(S, sort_chunk(S));
-  return (size_t)(round_up(nb * (experts + 1) * 4, 256) + round_up(S * 4, 256));
+  return (size_t)round_up(nb * (experts + 1) * 4, 256);
 }
 
 template <int ES, bool kCopy, int kSmallThreads>
@@ -598,7 +606,7 @@ qp_status run_sort(const Ids& ids, int64_t T, const void* X, int32_t dtype, int6
                    int32_t* slot_of_row, void* ws, hipStream_t stream) {
   const int64_t S = T * ids.top_k;
   const int es = X ? elem_bytes(dtype) : 4;
-  if (S <= kSmallSlots) {
+  if (S <= (X ? kSmallSlots : kSmallSort)) {
     if (!X)
       return launch_small<4, false>(ids, S, X, 0, 0, Xs, 0, offsets, row_of_slot, slot_of_row,
                                     stream);
@@ -609,21 +617,18 @@ qp_status run_sort(const Ids& ids, int64_t T, const void* X, int32_t dtype, int6
   }
   const int64_t chunk = sort_chunk(S), nb = ceil_div(S, chunk);
   int32_t* counts = static_cast<int32_t*>(ws);
-  int32_t* row_all = X ? reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) +
-                                                    round_up(nb * (ids.experts + 1) * 4, 256))
-                       : nullptr;
   qp_status st;
   if (S <= kSelfSlots) {
     hipLaunchKernelGGL((moe_place_kernel<true>), dim3((unsigned)nb), dim3(kSortThreads), 0, stream,
                        ids, (uint32_t)S, (uint32_t)chunk, (const int32_t*)nullptr, offsets,
-                       row_of_slot, slot_of_row, row_all);
+                       row_of_slot, slot_of_row);
   } else {
     hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)nb), dim3(kSortThreads), 0, stream, ids,
                        (uint32_t)S, (uint32_t)chunk, counts);
     if ((st = check_launch("qmoe sort (counts)"))) return st;
     hipLaunchKernelGGL((moe_place_kernel<false>), dim3((unsigned)nb), dim3(kSortThreads), 0, stream,
                        ids, (uint32_t)S, (uint32_t)chunk, (const int32_t*)counts, offsets,
-                       row_of_slot, slot_of_row, row_all);
+                       row_of_slot, slot_of_row);
   }
   st = check_launch("qmoe sort (rows)");
   if (st || !X) return st;
@@ -634,12 +639,12 @@ qp_status run_sort(const Ids& ids, int64_t T, const void* X, int32_t dtype, int6
     if (es == 2)
       hipLaunchKernelGGL((moe_copy_kernel<2>), grid, dim3(256), 0, stream,
                          static_cast<const uint8_t*>(X), ldx * 2, H, T, ids.top_k,
-                         (const int32_t*)row_all, (const int32_t*)(offsets + ids.experts),
+                         (const int32_t*)row_of_slot, (const int32_t*)slot_of_row,
                          static_cast<uint8_t*>(Xs), ldxs * 2, t);
     else
       hipLaunchKernelGGL((moe_copy_kernel<4>), grid, dim3(256), 0, stream,
                          static_cast<const uint8_t*>(X), ldx * 4, H, T, ids.top_k,
-                         (const int32_t*)row_all, (const int32_t*)(offsets + ids.experts),
+                         (const int32_t*)row_of_slot, (const int32_t*)slot_of_row,
                          static_cast<uint8_t*>(Xs), ldxs * 4, t);
   }
   return check_launch("qmoe dispatch (copy)");

@@ -656,7 +656,7 @@ qp_status qgemm_w4_kernel_name(int64_t M, const qp_packed_info* w, int32_t dtype
  *                the number of kept slots.
  *   row_of_slot  device int32 [T*top_k], -1 for dropped slots.
  *   slot_of_row  device int32 [T*top_k], -1 for the rows past the kept ones.
- *   ws           device workspace of qmoe_sort_ws_size bytes (0 up to 4096
+ *   ws           device workspace of qmoe_sort_ws_size bytes (0 up to 8192
  *                slots; then ws may be NULL).
  *   At most 512 experts and 2^30 slots, else QP_EUNSUPPORTED.  T = 0 writes
  *   offsets only.  Integer work: the same result in any run.

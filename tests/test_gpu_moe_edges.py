@@ -40,3 +40,37 @@ def test_rows_whose_slot_is_out_of_range_get_zeros(qp, dtype, T, k, H):
         assert torch.equal(got, dZ) and torch.equal(gw, dw), value
         assert torch.equal(qp.qmoe_combine(Z, maps, w), qp.qmoe_combine(Z, ros, w)), value
         assert torch.equal(qp.qmoe_dispatch_grad(Z, maps), qp.qmoe_dispatch_grad(Z, ros)), value
+
+
+@pytest.mark.parametrize("S", [63, 64, 65, 127, 128, 129, 255, 511, 512, 513, 1023, 1024, 1025, 4095,
+                               4096, 4097, 8191, 8192, 8193])
+@pytest.mark.parametrize("E", [1, 3, 64, 512])
+def test_every_switch_of_the_sort(qp, S, E):
+    """The sort alone and with rows, around the slot counts where its kernels
+    change: offsets, maps and rows from a stable sort."""
+    import torch
+    rng = np.random.default_rng(S + E)
+    print("sort around a switch", S, E, flush=True)
+    for k in (1, 3) if S % 3 == 0 else (1,):
+        T = S // k
+        ids = rng.integers(0, E, (T, k))
+        ids[rng.random((T, k)) < 0.2] = -1
+        flat = ids.reshape(-1)
+        order = np.argsort(np.where(flat < 0, E, flat), kind="stable")
+        n = int((flat >= 0).sum())
+        offsets = np.searchsorted(flat[order][:n], np.arange(E + 1))
+        ros, sor = np.full(S, -1), np.full(S, -1)
+        sor[:n] = order[:n]
+        ros[order[:n]] = np.arange(n)
+        d = torch.from_numpy(ids).cuda()
+        for H, dtype in ((5, torch.float32), (130, torch.bfloat16)):
+            X = torch.from_numpy(rng.standard_normal((T, H))).to(dtype).cuda()
+            out = torch.full((S, H), float("nan"), dtype=dtype, device="cuda")
+            Xs, *maps = qp.qmoe_dispatch(X, d, E, out=out)
+            for got in (maps, qp.qmoe_sort(d, E)):
+                assert np.array_equal(got[0].cpu().numpy(), offsets)
+                assert np.array_equal(got[1].cpu().numpy().reshape(-1), ros)
+                assert np.array_equal(got[2].cpu().numpy(), sor)
+            want = torch.zeros_like(Xs)
+            want[:n] = X[torch.from_numpy(sor[:n] // k).cuda()]
+            assert torch.equal(Xs, want)

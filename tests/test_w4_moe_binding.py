@@ -221,3 +221,9 @@ def test_scales_that_do_not_fit_are_refused(qp, packed):
     with pytest.raises(AssertionError, match="GPU"):
         qp.pack_s4(torch.zeros(5, 100, dtype=torch.int8), s[0])
     assert packed == []
+
+
+def test_sorts_of_up_to_8192_slots_need_no_workspace(qp):
+    for T, k, E in ((1, 1, 1), (2048, 2, 8), (4096, 2, 512), (8192, 1, 512)):
+        assert qp.qmoe_sort_ws_size(T, k, E) == 0
+    assert qp.qmoe_sort_ws_size(4097, 2, 8) > 0
