@@ -12,7 +12,10 @@
 // for f32 rows), which miss at most 2^-16 (2^-24) of it; dy enters exactly
 // (f16 as two pieces, f32 as three).  Of the pieces' products those are formed
 // whose order adds up to less than the number of weight pieces: what is left
-// out is below 2^-16 of a term (2^-23 for f32 rows).  Sums are f32.
+// out is below 2^-16 of a term (2^-23 for f32 rows).  Sums are f32.  Two pieces are
+// fewer bits than an f32 weight has; a third would be half as many MFMAs again.  Over
+// sums of 4096 terms they miss 2.5e-6 (bf16 rows) and 3.8e-6 (f16) of the result in
+// the norm, and the rounding of the outputs 1.7e-3 and 2.1e-4.
 //
 // Groups of 128 on without offsets: a block has one scale a channel, so the rows
 // can carry it: dy*s, rounded to f32, goes in as two bf16 pieces (three for f32
@@ -461,7 +464,7 @@ struct DxLds {
 };
 
 template <typename T, int kKind, int kMT>
-__global__ __launch_bounds__(256, 2) void w4_dx_tile_kernel(W4DxArgs a, uint32_t row_slots,
+__global__ __launch_bounds__(256, 2) void w4_dx_tile_kernel(W4DxArgs a,
                                                             uint32_t blk_pairs) {
   constexpr int NY = YFrag<T>::kPieces, NW = YFrag<T>::kWPieces;
   constexpr int kFrags = 2 * kMT;  // 16-row fragments of the workgroup
@@ -664,7 +667,7 @@ qp_status launch_dx_tile(const W4DxArgs& a, hipStream_t stream) {
     lds_attr_devices.fetch_or(bit, std::memory_order_release);
   }
   hipLaunchKernelGGL(kern, dim3((unsigned)(slots * pairs)), dim3(256), kLds, stream, a,
-                     (uint32_t)slots, (uint32_t)pairs);
+                     (uint32_t)pairs);
   return check_launch("qgemm_w4 gradient (many rows)");
 }
 
@@ -695,7 +698,11 @@ qp_status launch_dx_rows(const W4DxArgs& a, int64_t splits, float* part, hipStre
 // second launch and the partial sums' way through memory.  The tile kernel takes
 // 155 us for up to a workgroup a CU and 255 us for two, 4096 channels (4096 rows:
 // 255 us against 359; 4096 rows of 8 experts 400 against 404; 1024 rows 162
-// against 96).  The few-rows plan must not depend on the rows' type: the workspace
+// against 96).  Groups of 128 on, whose rows carry the scales in the few-rows
+// kernel, change little there (4096 rows 241 against 349, 2048 rows 161 and 177,
+// 3000 of 8 experts 240 and 284).  Where 8 experts' tiles make just a workgroup a
+// CU (1536 rows), the empty workgroups of the grid spread them unevenly and the
+// tile kernel, taken there, is the slower one (220 against 143).  The few-rows plan must not depend on the rows' type: the workspace
 // is asked for without it.
 struct DxPlan {
   int frags;       // 16-row fragments of the few-rows kernel

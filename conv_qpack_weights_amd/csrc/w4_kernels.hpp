@@ -131,7 +131,7 @@ __device__ __forceinline__ void w4_step(const W4Stage<T, kKind, kOne, kFM, kTile
 // scales and the rows' pieces, all straight from memory: a wave's rows are
 // nobody else's, so LDS would only add a hop), and the waves' sums meet in LDS
 // in a fixed order.  Bound by the weights' way from memory and, above some eight
-// rows, by the vector instructions (17 a word to unpack, 4 a group and tile to
+// rows, by the vector instructions (13 a word to unpack, 4 a group and tile to
 // rescale): 1 x 4096 x 4096 5.0 us (10.5 MB; a read of the same bytes takes 3.4),
 // 16 x 11008 x 4096 f16 9.5 us (24.5 MB), 64 tokens x 2 of 16 experts of
 // 11008 x 4096 98 us (454 MB, 4.6 TB/s).  kAhead = 1: two and four blocks in
@@ -287,7 +287,10 @@ qp_status launch_rows(const W4Args& a, hipStream_t stream) {
 // measured 1540, 1100 and 1130 us where this took 1050.  Every register counts
 // (168 a lane at three waves): the weights' and scales' addresses are a scalar
 // base and one lane offset, made anew each block so that they are not kept as
-// 64-bit pointers (11 reloads of spilled registers a block without).  Groups of
+// 64-bit pointers (11 reloads of spilled registers a block without).  The loop over
+// whole blocks then spills none; the prologue and the cut or half block at the end
+// of K do (40 to 119 registers in all for bf16 and f16 rows without offsets), which
+// a K off 128 pays once.  Groups of
 // 128 on take one rescale per 64 K: 1024 x 11008 x 4096 f16 107 us (119 with
 // those reloads); the MFMAs of a tile spread out between the other tile's changed
 // nothing.
@@ -667,7 +670,7 @@ qp_status launch_shape(const W4Args& a, W4Shape shape, hipStream_t stream) {
     case kTile4x8:
       // (three pieces a row and the asymmetric sums need the registers)
       return launch_tile<T, kKind, kOne, 4, 2, sizeof(T) == 4 || kKind == 2 ? 2 : 4>(a, stream);
-    case kTile8x8: break;
+    case kTile8x8: break;  // (for f32 rows 64 rows a workgroup here too, at about the same cost a row)
   }
   if constexpr (sizeof(T) == 4)
     return launch_tile<T, kKind, kOne, 4, 2, 2>(a, stream);  // (LDS holds three pieces of 64 rows)
