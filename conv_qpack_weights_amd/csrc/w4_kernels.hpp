@@ -133,8 +133,8 @@ __device__ __forceinline__ void w4_step(const W4Stage<T, kKind, kOne, kFM, kTile
 // in a fixed order.  Bound by the weights' way from memory and, above some eight
 // rows, by the vector instructions (13 a word to unpack, 4 a group and tile to
 // rescale): 1 x 4096 x 4096 5.0 us (10.5 MB; a read of the same bytes takes 3.4),
-// 16 x 11008 x 4096 f16 9.5 us (24.5 MB), 64 tokens x 2 of 16 experts of
-// 11008 x 4096 98 us (454 MB, 4.6 TB/s).  kAhead = 1: two and four blocks in
+// 16 x 11008 x 4096 f16 10 us (24.5 MB), 64 tokens x 2 of 16 experts of
+// 11008 x 4096 96-100 us (454 MB, 4.6 TB/s).  kAhead = 1: two and four blocks in
 // flight cost waves a SIMD and measured 1-15% slower at every shape.
 template <typename T, int kKind, bool kOne, int kFM, int kTiles, int kWaves, int kAhead>
 __global__ __launch_bounds__(kWaves * 64) void w4_rows_kernel(W4Args a, uint32_t row_slots) {
@@ -280,8 +280,8 @@ qp_status launch_rows(const W4Args& a, hipStream_t stream) {
 // What bounds it with groups of 32: per 16x16x32 MFMA (16 cycles of the matrix
 // unit) the group's rescale is 4 fused multiply-adds and a weight word costs 13
 // vector instructions to unpack, used kFM times; the two units hardly overlap
-// on this part.  8192 rows x 11008 x 4096 over 8 experts: 903 us, 817 TFLOP/s;
-// of the cycles the matrix unit is busy 38%, vector instructions issue 65%
+// on this part.  8192 rows x 11008 x 4096 over 8 experts: 920 us, 800 TFLOP/s;
+// of the cycles the matrix unit is busy 38%, vector instructions issue 63%
 // (a library product of bf16 matrices of 8192: 1275 TFLOP/s).  128 x 128 tiles
 // at three waves a SIMD; 128 x 256 (spills), 64 x 256 and two waves a SIMD
 // measured 1540, 1100 and 1130 us where this took 1050.  Every register counts
