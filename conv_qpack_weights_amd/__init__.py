@@ -23,6 +23,7 @@ QP_BF16, QP_F16, QP_S64 = 5, 6, 7
 QP_PER_TENSOR, QP_PER_CHANNEL, QP_BLOCKWISE, QP_DYNAMIC_PER_ROW = 0, 1, 2, 3
 QP_BLOCKWISE_BF16, QP_BLOCKWISE_ASYM = 4, 5
 QP_ROUND_HALF_EVEN = 0
+QP_MX_FLOOR, QP_MX_CEIL = 0, 1
 
 _STATUS = {0: "QP_OK", -1: "QP_EINVAL", -2: "QP_EUNSUPPORTED", -3: "QP_EOVERFLOW",
            -4: "QP_ESIZE", -5: "QP_EALIGN", -6: "QP_EHIP"}
@@ -53,12 +54,21 @@ class QPackError(RuntimeError):
         self.status = status
 
 
+class Mx4Desc(C.Structure):
+    """qp_mx4: where an MXFP4 matrix (or one an expert) lies."""
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int64),
+                ("K", C.c_int64), ("ld_codes", C.c_int64), ("ld_scales", C.c_int64),
+                ("matrices", C.c_int64), ("codes_stride", C.c_int64),
+                ("scales_stride", C.c_int64)]
+
+
 _P = C.c_void_p
 _I64 = C.c_int64
 _I32 = C.c_int32
 _F = C.c_float
 _QT = C.POINTER(QTensor)
 _PI = C.POINTER(PackedInfo)
+_MX = C.POINTER(Mx4Desc)
 _SZ = C.POINTER(C.c_size_t)
 
 SIGNATURES = {
@@ -125,6 +135,18 @@ SIGNATURES = {
     "qmoe_combine": (C.c_int, [_P, _I32, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _P]),
     "qmoe_combine_grad": (C.c_int, [_P, _I64, _P, _I64, _I32, _I64, _I64, _I64, _P, _P, _P, _I64,
                                     _P, _I64, _P, _I64, _P]),
+    "qquantize_rows_mx4": (C.c_int, [_P, _I32, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64, _P]),
+    "qdequantize_rows_mx4": (C.c_int, [_MX, _P, _I32, _I64, _P]),
+    "qgemm_a4w4_mx": (C.c_int, [_MX, _MX, _P, _F, _F, _P, _I32, _I64, _P]),
+    "qgemm_a4w4_mx_experts": (C.c_int, [_MX, _P, _I64, _I64, _MX, _P, _P, _F, _F, _P, _I32, _I64,
+                                        _P]),
+    "qgemm_w4_mx": (C.c_int, [_P, _I32, _I64, _I64, _I64, _MX, _P, _F, _F, _P, _I32, _I64, _P]),
+    "qgemm_w4_mx_experts": (C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _I64, _I64, _MX, _P, _P, _F,
+                                      _F, _P, _I32, _I64, _P]),
+    "qgemm_w4_mx_dx_ws_size": (C.c_int, [_I64, _MX, _SZ]),
+    "qgemm_w4_mx_dx": (C.c_int, [_P, _I32, _I64, _I64, _MX, _P, _I64, _P, C.c_size_t, _P]),
+    "qgemm_w4_mx_experts_dx": (C.c_int, [_P, _I32, _I64, _I64, _MX, _P, _P, _I64, _P, C.c_size_t,
+                                         _P]),
 }
 
 
@@ -933,3 +955,257 @@ def qmoe_combine_grad(dY: torch.Tensor, Z: torch.Tensor, row_of_slot: torch.Tens
                                   _ptr(slot_of_row), _ptr(weights), ldw, _ptr(out), ldo,
                                   _ptr(out_weights), lddw, _stream_of(Z)), "qmoe_combine_grad")
     return out, out_weights
+
+
+# ---------------------------------------------------------------- MXFP4
+class MX4:
+    """An MXFP4 matrix [rows, K], or one an expert [experts, rows, K]: ``codes``
+    uint8 [.., rows, 16*ceil(K/32)] (two values a byte, the first in the low bits)
+    and ``scales`` uint8 [.., rows, ceil(K/32)].  Made by :func:`mx4_tensor` and
+    :func:`qquantize_rows_mx4`; an expert's matrix is ``m[e]``."""
+    __slots__ = ("codes", "scales", "K", "desc")
+
+    def __init__(self, codes, scales, K):
+        self.codes, self.scales, self.K = codes, scales, K
+        d = self.desc = Mx4Desc()
+        d.codes, d.scales = codes.data_ptr(), scales.data_ptr()
+        d.rows, d.K = codes.shape[-2], K
+        # (the stride of a single row means nothing to torch: the library gets the
+        # row's length)
+        G = scales.shape[-1]
+        one = codes.shape[-2] < 2
+        d.ld_codes = 16 * G if one else codes.stride(-2)
+        d.ld_scales = -(-G // 4) * 4 if one else scales.stride(-2)
+        d.matrices = codes.shape[0] if codes.dim() == 3 else 1
+        if codes.dim() == 3:
+            d.codes_stride, d.scales_stride = codes.stride(0), scales.stride(0)
+
+    @property
+    def shape(self):
+        return (*self.codes.shape[:-1], self.K)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def __getitem__(self, e):
+        assert self.codes.dim() == 3, "one matrix only"
+        return MX4(self.codes[e], self.scales[e], self.K)
+
+
+def _mx4_codes(t, rows_shape, G):
+    """`t` as the kernels read codes: itself, or laid out anew."""
+    ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(
+        s % 16 == 0 for s, n in zip(t.stride()[:-1], rows_shape) if n > 1) and \
+        (rows_shape[-1] < 2 or t.stride(-2) >= 16 * G)
+    return t if ok else t.contiguous().clone()
+
+
+def _mx4_scales(rows_shape, G, like):
+    """New scales: rows of whole words, the view of their G bytes."""
+    return like.new_empty((*rows_shape, -(-G // 4) * 4), dtype=torch.uint8)[..., :G]
+
+
+def mx4_tensor(codes: torch.Tensor, scales: torch.Tensor, K=None) -> MX4:
+    """An MXFP4 matrix (or one an expert) from codes uint8 [.., rows, 16*ceil(K/32)]
+    and scales uint8 [.., rows, ceil(K/32)], as checkpoints hold them: taken as they
+    are where the kernels can read them, else laid out anew (once, at load time)."""
+    assert codes.dtype == torch.uint8 and scales.dtype == torch.uint8, \
+        "codes and scales must be uint8"
+    assert codes.dim() in (2, 3) and codes.shape[:-1] == scales.shape[:-1], \
+        "codes and scales must be [rows, bytes] or [experts, rows, bytes] alike"
+    G = scales.shape[-1]
+    assert G > 0 and codes.shape[-1] == 16 * G, "codes must hold 16 bytes a block, scales one"
+    K = 32 * G if K is None else int(K)
+    assert 32 * (G - 1) < K <= 32 * G, "K=%d does not fit %d blocks of 32" % (K, G)
+    assert codes.device == scales.device, "codes and scales must be on one device"
+    lead = codes.shape[:-1]
+    codes = _mx4_codes(codes, lead, G)
+    # (a row of scales is read in words: the last one's padding must be there)
+    if G % 4 or scales.stride(-1) != 1 or scales.data_ptr() % 4 or any(
+            s % 4 for s, n in zip(scales.stride()[:-1], lead) if n > 1) or \
+            (lead[-1] > 1 and scales.stride(-2) < G):
+        scales = _mx4_scales(lead, G, scales).copy_(scales)
+    return MX4(codes, scales, K)
+
+
+@functools.lru_cache(maxsize=None)
+def _several_gpus():
+    return torch.cuda.device_count() > 1
+
+
+def _mx_call(name, t, *args):
+    """The library's `name` on t's GPU and its current stream there."""
+    f = getattr(_lib, name)
+    if _several_gpus():
+        with torch.cuda.device(t.get_device()):
+            status = f(*args, _stream_of(t))
+    else:
+        status = f(*args, _stream_of(t))
+    _check(status, name)
+
+
+_MX_RULES = {"floor": QP_MX_FLOOR, "ceil": QP_MX_CEIL}
+
+
+def _is_mx4(m, what, dims=2):
+    assert isinstance(m, MX4), "%s must be an MX4 (mx4_tensor, qquantize_rows_mx4)" % what
+    assert m.codes.dim() == dims, "%s must be %s" % (
+        what, "one matrix" if dims == 2 else "a matrix an expert")
+
+
+def qquantize_rows_mx4(X: torch.Tensor, rule="floor", out=None) -> MX4:
+    """Rows [M, K] (f32, bf16, f16) to MXFP4; a contiguous [E, N, K] gives a matrix
+    an expert.  ``rule``: "floor" (a block's scale from its largest value's
+    exponent; values above 6 scales become 6) or "ceil" (no value is cut)."""
+    assert rule in _MX_RULES, "rule must be 'floor' or 'ceil'"
+    lead = X.shape[:-1]
+    if X.dim() == 3:
+        assert X.is_contiguous(), "the matrices must be contiguous"
+        X = X.view(-1, X.shape[-1])
+    dt, M, K, ldx = _rows(X, "X")
+    G = -(-K // 32)
+    if out is None:
+        out = MX4(X.new_empty((*lead, 16 * G), dtype=torch.uint8), _mx4_scales(lead, G, X), K)
+    else:
+        assert isinstance(out, MX4) and out.shape == (*lead, K), "out must be of X's shape"
+        assert out.codes.dim() == 2 or (out.codes.is_contiguous() and
+                                        out.desc.scales_stride == out.desc.rows * out.desc.ld_scales), \
+            "out's matrices must follow each other"
+    d = out.desc
+    _one_gpu("qquantize_rows_mx4", X, out.codes, out.scales)
+    _mx_call("qquantize_rows_mx4", X, _ptr(X), dt, M, K, ldx, _MX_RULES[rule], d.codes,
+             d.ld_codes, d.scales, d.ld_scales)
+    return out
+
+
+def qdequantize_rows_mx4(a: MX4, dtype=torch.float32, out=None):
+    """The values of an MXFP4 matrix, [rows, K] in `dtype`."""
+    _is_mx4(a, "a")
+    assert dtype in _FLOAT, "dtype must be float32, bfloat16 or float16"
+    M, K = a.shape
+    out, odt, ldy = _out(out, M, K, dtype, a.codes, "out")
+    _one_gpu("qdequantize_rows_mx4", a.codes, a.scales, out)
+    _mx_call("qdequantize_rows_mx4", a.codes, C.byref(a.desc), _ptr(out), odt, ldy)
+    return out
+
+
+def _mx_bias(bias, n, what):
+    if bias is not None:
+        _f32(bias, "bias")
+        assert bias.numel() == n, "bias must hold %s values" % what
+
+
+def qgemm_a4w4_mx(A: MX4, W: MX4, bias=None, clamp_lo=-float("inf"), clamp_hi=float("inf"),
+                  out=None, out_dtype=torch.float32):
+    """Y = clamp(A @ W^T + bias), both MXFP4: A [M, K], W [N, K]; outputs f32, bf16
+    or f16."""
+    _is_mx4(A, "A")
+    _is_mx4(W, "W")
+    M, N = A.desc.rows, W.desc.rows
+    assert out_dtype in _FLOAT, "out_dtype must be float32, bfloat16 or float16"
+    out, odt, ldy = _out(out, M, N, out_dtype, A.codes, "out")
+    _mx_bias(bias, N, "N")
+    _one_gpu("qgemm_a4w4_mx", A.codes, A.scales, W.codes, W.scales, bias, out)
+    _mx_call("qgemm_a4w4_mx", A.codes, C.byref(A.desc), C.byref(W.desc), _ptr(bias), clamp_lo,
+             clamp_hi, _ptr(out), odt, ldy)
+    return out
+
+
+def _mx_experts(W, offsets, bias, rows, x_rows):
+    _is_mx4(W, "W", 3)
+    _ints(offsets, "offsets")
+    E, N = W.desc.matrices, W.desc.rows
+    assert offsets.numel() == E + 1, "offsets must hold experts + 1 values"
+    _mx_bias(bias, E * N, "experts x N")
+    if rows is None:
+        return x_rows, N
+    _ints(rows, "rows")
+    return rows.numel(), N
+
+
+def qgemm_a4w4_mx_experts(A: MX4, W: MX4, offsets: torch.Tensor, bias=None, rows=None, row_div=1,
+                          clamp_lo=-float("inf"), clamp_hi=float("inf"), out=None,
+                          out_dtype=torch.float32):
+    """The product with rows [offsets[e], offsets[e+1]) on W[e] [E, N, K] and bias
+    [E, N]; ``rows`` and ``row_div`` as in :func:`qgemm_w4_experts` (tokens
+    quantized once, read through slot_of_row)."""
+    _is_mx4(A, "A")
+    M, N = _mx_experts(W, offsets, bias, rows, A.desc.rows)
+    assert out_dtype in _FLOAT, "out_dtype must be float32, bfloat16 or float16"
+    out, odt, ldy = _out(out, M, N, out_dtype, A.codes, "out")
+    _one_gpu("qgemm_a4w4_mx_experts", A.codes, A.scales, W.codes, W.scales, offsets, bias, rows, out)
+    _mx_call("qgemm_a4w4_mx_experts", A.codes, C.byref(A.desc), _ptr(rows), row_div, M,
+             C.byref(W.desc), _ptr(offsets), _ptr(bias), clamp_lo, clamp_hi, _ptr(out), odt, ldy)
+    return out
+
+
+def qgemm_w4_mx(X: torch.Tensor, W: MX4, bias=None, clamp_lo=-float("inf"),
+                clamp_hi=float("inf"), out=None, out_dtype=None):
+    """Y = clamp(X @ W^T + bias): float rows (f32, bf16 or f16, not quantized) times
+    MXFP4 weights; outputs in X's type or `out_dtype` float32."""
+    dt, M, K, ldx = _rows(X, "X")
+    _is_mx4(W, "W")
+    N = W.desc.rows
+    assert out_dtype is None or out_dtype in _FLOAT, "out_dtype must be X's type or float32"
+    out, odt, ldy = _out(out, M, N, out_dtype or X.dtype, X, "out")
+    _mx_bias(bias, N, "N")
+    _one_gpu("qgemm_w4_mx", X, W.codes, W.scales, bias, out)
+    _mx_call("qgemm_w4_mx", X, _ptr(X), dt, M, K, ldx, C.byref(W.desc), _ptr(bias), clamp_lo,
+             clamp_hi, _ptr(out), odt, ldy)
+    return out
+
+
+def qgemm_w4_mx_experts(X: torch.Tensor, W: MX4, offsets: torch.Tensor, bias=None, rows=None,
+                        row_div=1, clamp_lo=-float("inf"), clamp_hi=float("inf"), out=None,
+                        out_dtype=None):
+    """The product with rows [offsets[e], offsets[e+1]) on W[e] [E, N, K] and bias
+    [E, N]; ``rows`` and ``row_div`` as in :func:`qgemm_w4_experts`."""
+    dt, x_rows, K, ldx = _rows(X, "X")
+    M, N = _mx_experts(W, offsets, bias, rows, x_rows)
+    assert out_dtype is None or out_dtype in _FLOAT, "out_dtype must be X's type or float32"
+    out, odt, ldy = _out(out, M, N, out_dtype or X.dtype, X, "out")
+    _one_gpu("qgemm_w4_mx_experts", X, W.codes, W.scales, offsets, bias, rows, out)
+    _mx_call("qgemm_w4_mx_experts", X, _ptr(X), dt, x_rows, K, ldx, _ptr(rows), row_div, M,
+             C.byref(W.desc), _ptr(offsets), _ptr(bias), clamp_lo, clamp_hi, _ptr(out), odt, ldy)
+    return out
+
+
+def qgemm_w4_mx_dx_ws_size(M: int, W: MX4) -> int:
+    n = C.c_size_t()
+    _check(_lib.qgemm_w4_mx_dx_ws_size(M, C.byref(W.desc), C.byref(n)), "qgemm_w4_mx_dx_ws_size")
+    return n.value
+
+
+def _mx_dx_buffers(dY, W, out, ws):
+    dt, M, N, lddy = _rows(dY, "dY")
+    assert N == W.desc.rows, "dY must have N columns"
+    out, odt, lddx = _out(out, M, W.K, dY.dtype, dY, "out")
+    assert odt == dt, "out must be of dY's type"
+    if ws is None:
+        n = qgemm_w4_mx_dx_ws_size(M, W)
+        ws = _alloc_bytes(n, dY.device) if n else None
+    return dt, M, lddy, out, lddx, ws, _ws_bytes(ws)
+
+
+def qgemm_w4_mx_dx(dY: torch.Tensor, W: MX4, out=None, ws=None):
+    """The gradient of qgemm_w4_mx (and of qgemm_a4w4_mx, past the quantization) to
+    the rows: dX = dY @ W."""
+    _is_mx4(W, "W")
+    dt, M, lddy, out, lddx, ws, n = _mx_dx_buffers(dY, W, out, ws)
+    _one_gpu("qgemm_w4_mx_dx", dY, W.codes, W.scales, out, ws)
+    _mx_call("qgemm_w4_mx_dx", dY, _ptr(dY), dt, M, lddy, C.byref(W.desc), _ptr(out), lddx,
+             _ptr(ws), n)
+    return out
+
+
+def qgemm_w4_mx_experts_dx(dY: torch.Tensor, W: MX4, offsets: torch.Tensor, out=None, ws=None):
+    """The gradient of qgemm_w4_mx_experts to its (sorted) rows."""
+    _is_mx4(W, "W", 3)
+    _ints(offsets, "offsets")
+    assert offsets.numel() == W.desc.matrices + 1, "offsets must hold experts + 1 values"
+    dt, M, lddy, out, lddx, ws, n = _mx_dx_buffers(dY, W, out, ws)
+    _one_gpu("qgemm_w4_mx_experts_dx", dY, W.codes, W.scales, offsets, out, ws)
+    _mx_call("qgemm_w4_mx_experts_dx", dY, _ptr(dY), dt, M, lddy, C.byref(W.desc), _ptr(offsets),
+             _ptr(out), lddx, _ptr(ws), n)
+    return out

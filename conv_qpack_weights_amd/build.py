@@ -23,7 +23,8 @@ FLOORS_SRC = "floors.hip"
 FLOORS_LIB = os.path.join(HERE, "libqpfloors.so")
 SOURCES = ["status.cpp", "pack.hip", "quant.hip", "im2col.hip", "gemm_s8.hip", "conv.hip",
            "conv_implicit.hip", "a8w4.hip", "a8w8b.hip", "unpack.hip", "moe.hip", "w4.hip",
-           "w4_f32.hip", "w4_bf16.hip", "w4_f16.hip", "w4_dx.hip"]
+           "w4_f32.hip", "w4_bf16.hip", "w4_f16.hip", "w4_dx.hip", "mx4.hip", "mx4_quant.hip",
+           "mx4_a4w4.hip", "mx4_w4_f32.hip", "mx4_w4_bf16.hip", "mx4_w4_f16.hip", "mx4_dx.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

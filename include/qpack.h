@@ -701,6 +701,120 @@ qp_status qmoe_combine_grad(const void* dY, int64_t lddy, const void* Z, int64_t
                             const float* weights, int64_t ldw, void* dZ, int64_t lddz,
                             float* dweights, int64_t lddw, hipStream_t stream);
 
+/*
+ * Microscaled 4-bit floating point (MXFP4): a row is K values of four bits,
+ * e2m1 -- sign, two exponent bits, one of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6 --
+ * and every 32 of them share a scale byte s: value * 2^(s - 127); s = 255 makes
+ * the whole block NaN.
+ *   codes   two values a byte, the first in the low bits; a row's blocks one
+ *           after another, 16 bytes each.  The values that fill up the last
+ *           block of a K not a multiple of 32 must be zeros.  Rows, matrices and
+ *           the first byte at multiples of 16 bytes.
+ *   scales  a byte a block; rows, matrices and the first byte at multiples of 4
+ *           bytes.  The bytes up to the next multiple of 4 after a row's last
+ *           scale must be readable; what they hold does not matter.
+ *   rows, K logical shape; K at most 2^22, rows at most 2^30.
+ *   ld_codes, ld_scales  bytes between rows (at most 2^23).
+ *   matrices             1, or the number of experts; codes_stride and
+ *                        scales_stride are the bytes between them.
+ */
+typedef struct {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t rows;
+  int64_t K;
+  int64_t ld_codes;
+  int64_t ld_scales;
+  int64_t matrices;
+  int64_t codes_stride;
+  int64_t scales_stride;
+} qp_mx4;
+
+typedef enum {
+  QP_MX_FLOOR = 0, /* s from the largest magnitude's exponent: values above 6 2^(s-127) become that */
+  QP_MX_CEIL = 1   /* the least s that lets no value pass 6 2^(s-127) */
+} qp_mx_rule;
+
+/*
+ * qquantize_rows_mx4 -- float rows to MXFP4.  For a block whose largest
+ *   magnitude is in [2^p, 2^(p+1)): s = p - 2 + 127 (QP_MX_FLOOR), one more if
+ *   that magnitude is above 1.5 2^p (QP_MX_CEIL), 0 at least; an all-zero block
+ *   gets 0.  Codes: x / 2^(s-127) to the nearest value, ties to the even code,
+ *   6 at most, the sign kept.  A block with an infinity or a NaN gets s = 255
+ *   and zero codes.  Columns from K on count as zeros.
+ *   X        device rows of `dtype` (QP_F32, QP_BF16 or QP_F16), [M][ldx],
+ *            aligned to their elements only.
+ *   codes, scales, ld_*  as in qp_mx4; only whole blocks' codes and one byte a
+ *            block are written.
+ *
+ * qdequantize_rows_mx4 -- the values back, in y_dtype: exact in f32 and bf16 (above
+ *   their range infinities), rounded once in f16.  One matrix (matrices = 1).
+ */
+qp_status qquantize_rows_mx4(const void* X, int32_t dtype, int64_t M, int64_t K, int64_t ldx,
+                             int32_t rule, uint8_t* codes, int64_t ld_codes, uint8_t* scales,
+                             int64_t ld_scales, hipStream_t stream);
+qp_status qdequantize_rows_mx4(const qp_mx4* a, void* Y, int32_t y_dtype, int64_t ldy,
+                               hipStream_t stream);
+
+/*
+ * qgemm_a4w4_mx -- Y = clamp(A x W^T + bias, lo, hi), rows and weights MXFP4:
+ *   every product of two values and their scales is exact, the sums are f32, one
+ *   rounding to y_dtype (QP_F32, QP_BF16 or QP_F16) at the end.
+ *   a        the rows: one matrix [M][K], M = a->rows >= 0.
+ *   w        the weights: one matrix [N][K], N = w->rows.
+ *   bias     device f32 [N] or NULL, added before the clamp.
+ *   Y        device [M][ldy], ldy >= N, aligned to its elements.
+ * qgemm_a4w4_mx_experts -- the same with rows [offsets[e], offsets[e+1]) on matrix
+ *   e of w; offsets, rows, row_div, M and bias [experts][N] as in
+ *   qgemm_w4_experts (with `rows`, the tokens are quantized once).
+ * No workspace; run to run the same bits.  Outputs must not overlap inputs.
+ * Errors: QP_EINVAL on shapes, types, NaN or reversed bounds; QP_EALIGN;
+ * QP_EUNSUPPORTED above 2^30 rows, or where a launch would pass 2^32 threads.
+ */
+qp_status qgemm_a4w4_mx(const qp_mx4* a, const qp_mx4* w, const float* bias, float clamp_lo,
+                        float clamp_hi, void* Y, int32_t y_dtype, int64_t ldy,
+                        hipStream_t stream);
+qp_status qgemm_a4w4_mx_experts(const qp_mx4* a, const int32_t* rows, int64_t row_div, int64_t M,
+                                const qp_mx4* w, const int32_t* offsets, const float* bias,
+                                float clamp_lo, float clamp_hi, void* Y, int32_t y_dtype,
+                                int64_t ldy, hipStream_t stream);
+
+/*
+ * qgemm_w4_mx, qgemm_w4_mx_experts -- float rows, not quantized, times MXFP4
+ *   weights; arguments as qgemm_w4_blockwise and qgemm_w4_experts with w (one
+ *   matrix, or one an expert) in place of the blob.  The weights are exact, the
+ *   rows keep their own type's accuracy, the sums are f32.
+ * Range: a weight above the f32 range (s of 253 and more) is an infinity; f32 rows
+ * are held to 2^-133.
+ */
+qp_status qgemm_w4_mx(const void* X, int32_t dtype, int64_t M, int64_t K, int64_t ldx,
+                      const qp_mx4* w, const float* bias, float clamp_lo, float clamp_hi, void* Y,
+                      int32_t y_dtype, int64_t ldy, hipStream_t stream);
+qp_status qgemm_w4_mx_experts(const void* X, int32_t dtype, int64_t x_rows, int64_t K, int64_t ldx,
+                              const int32_t* rows, int64_t row_div, int64_t M, const qp_mx4* w,
+                              const int32_t* offsets, const float* bias, float clamp_lo,
+                              float clamp_hi, void* Y, int32_t y_dtype, int64_t ldy,
+                              hipStream_t stream);
+
+/*
+ * qgemm_w4_mx_dx, qgemm_w4_mx_experts_dx -- the gradients of the products (of
+ *   qgemm_a4w4_mx* too, past the rows' quantization) to their rows, without bias
+ *   and clamp:  dX[m,k] = sum_n dY[m,n] * w[n,k].
+ *   (With dY transposed for the rows and quantized rows [M][K] for w it is also the
+ *   dense product's gradient to its weights.)
+ *   dY       device [M][lddy], lddy >= N;  dX  device [M][lddx], lddx >= K,
+ *            both of `dtype`.
+ *   offsets  as qgemm_w4_experts; rows of no expert get zeros.
+ *   ws       device workspace of qgemm_w4_mx_dx_ws_size bytes (0: may be NULL),
+ *            256-byte aligned.
+ */
+qp_status qgemm_w4_mx_dx_ws_size(int64_t M, const qp_mx4* w, size_t* bytes);
+qp_status qgemm_w4_mx_dx(const void* dY, int32_t dtype, int64_t M, int64_t lddy, const qp_mx4* w,
+                         void* dX, int64_t lddx, void* ws, size_t ws_bytes, hipStream_t stream);
+qp_status qgemm_w4_mx_experts_dx(const void* dY, int32_t dtype, int64_t M, int64_t lddy,
+                                 const qp_mx4* w, const int32_t* offsets, void* dX, int64_t lddx,
+                                 void* ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
