@@ -1,9 +1,436 @@
 // mx4_a4w4.hip -- MXFP4 rows times MXFP4 weights: both go into the scaled 4-bit
-// MFMA as they are.
+// MFMA as they are,
+//   y[r,n] = clamp(sum_b 2^(sa[r,b] + sw[n,b] - 254) sum_{k in b} a[r,k] w[n,k] + bias[n], lo, hi)
+// with every product and scaling exact and the sums in f32.  Few rows: the kernel
+// of mx4_rows.hpp; many rows: tiles over LDS, below.
+#include <type_traits>
+
 #include "mx4_rows.hpp"
 
+#pragma clang fp contract(off)
+
 namespace qp {
-qp_status run_mx_a4w4(const MxArgs& a, hipStream_t stream) {
-  return mx_launch_rows<mx4_t, 1, 2, 8, 1>(a, stream);
+namespace {
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+// d + a b^T over 64 K: lane l holds 32 values of row l%32 from 32 (l/32) on; their
+// scale is byte kByte of sa / sb.
+template <int kByte>
+__device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x16 d) {
+  const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, d, 4, 4, kByte, (int)sa, kByte,
+                                                         (int)sb);
 }
+
+// kBytes per lane from base + voff + soff straight into LDS, lane after lane from dst
+// on; offsets of `range` bytes and more ask for nothing.  (The caller waits.)
+template <int kBytes>
+__device__ __forceinline__ void dma_to_lds(const void* base, int range, lds_u8* dst, uint32_t voff,
+                                           uint32_t soff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __amdgpu_buffer_rsrc_t r =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, range, 0x00020000);
+  if constexpr (kBytes == 16)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)dst, 16, voff, soff, 0, 0);
+  else
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)dst, 4, voff, soff, 0, 0);
+#endif
+}
+
+// ---- many rows -----------------------------------------------------------------
+// A workgroup owns BM rows x BN channels, its WM x WN waves 32 FM rows x 32 FN
+// channels each, in registers.  256 K of rows and channels at a time, a stage, come
+// into one of D LDS buffers by direct loads, 128 bytes of a row side by side; the
+// 16-byte piece c of row r lies at place c ^ turn(r) of the row's eight, so that the
+// rows an operand takes piece c of meet every bank alike.  The weights are the
+// MFMA's first operand: a lane ends with one row and runs of four channels.
+enum A4Shape { kA4Rows, kA4Tile64, kA4Tile128, kA4Tile256 };
+
+template <int BM, int BN, int WM, int WN, int D>
+struct A4Tile {
+  static constexpr int NW = WM * WN, FM = BM / (32 * WM), FN = BN / (32 * WN);
+  static constexpr int kStage = (BM + BN) * 128, kScales = (BM + BN) * 16;
+  static constexpr int kSpans = D == 2 ? 2 : 4;  // of 512 K: D / 2 + 1 are live
+  static constexpr int kOutLd = 32 * FN + 4;
+  static constexpr int kOut = NW * 32 * kOutLd * 4;
+  static constexpr int kRing = D * kStage + kSpans * kScales;
+  static constexpr int kLds = kRing > kOut ? kRing : kOut;
+};
+
+template <int BM, int BN, int WM, int WN, int D>
+__global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, uint32_t row_slots,
+                                                                   uint32_t col_groups) {
+  using L = A4Tile<BM, BN, WM, WN, D>;
+  constexpr int NW = L::NW, FM = L::FM, FN = L::FN;
+  constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW, kSI = (BM + BN) / 16,
+                kS = (kSI + NW - 1) / NW;
+  static_assert(kA * 8 * NW == BM && kB * 8 * NW == BN && BM % 16 == 0, "shares");
+  // piece c of row r lies at place c ^ turn(r) of the row's eight: the 16 rows whose
+  // pieces are read at a time are at 16 different places of the banks' 256 bytes
+  auto turn = [](int r) { return (r >> 1) & 7; };
+  extern __shared__ __attribute__((aligned(16))) uint8_t mx_lds[];
+  lds_u8* const ring = (lds_u8*)mx_lds;
+  lds_u8* const scales = ring + D * L::kStage;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  // eight row tiles by neighbouring channel groups, in runs per XCD
+  const uint32_t id = xcd_run(blockIdx.x, gridDim.x);
+  const uint32_t band = id / (8 * col_groups), in_band = id - band * 8 * col_groups;
+  const uint32_t band_rows = row_slots - band * 8 < 8 ? row_slots - band * 8 : 8;
+  const uint32_t slot = band * 8 + in_band % band_rows;
+  const int64_t n0 = (int64_t)(in_band / band_rows) * BN;
+  const int64_t N = a.w.rows;
+  const W4Tile tile = w4_find_tile<BM>(a.rows, slot);
+  if (tile.expert < 0) return;
+  if (a.rows.offsets && tile.expert == a.rows.experts) {  // rows of no expert
+    for (int64_t r = tile.r0 + wave; r < tile.r1; r += NW)
+      for (int64_t n = n0 + lane; n < n0 + BN && n < N; n += 64)
+        w4_store(a.Y, a.y_dtype, r * a.ldy + n, 0.0f);
+    return;
+  }
+
+  // what a lane loads: a piece of row lane / 8 of eight; rows past the tile's end
+  // repeat its last row
+  const int lrow = lane >> 3;
+  auto piece = [&](int j) { return (lane & 7) ^ turn(j * 8 + lrow); };
+  static_assert(kA % 2 == 0 && kB % 2 == 0, "turn of a wave's first row");
+  const uint8_t *abase = a.a.codes, *sabase = a.a.scales;
+  int64_t first = 0;
+  if (!a.rows.map) {
+    first = tile.r0;
+    abase += first * a.a.ldc;
+    sabase += first * a.a.lds;
+  }
+  auto source = [&](int row) {
+    int64_t r = tile.r0 + row;
+    r = r < tile.r1 ? r : tile.r1 - 1;
+    const int64_t x = w4_source_row(a.rows, r);
+    return x < 0 ? INT64_C(0) : x - first;
+  };
+  const uint8_t* const wbase = a.w.codes + tile.expert * a.w.cstride + n0 * a.w.ldc;
+  const uint8_t* const swbase = a.w.scales + tile.expert * a.w.sstride + n0 * a.w.lds;
+  const int64_t last_n = N - 1 - n0;
+  uint32_t va[kA], vb[kB], vs[kS];
+#pragma unroll
+  for (int j = 0; j < kA; ++j)
+    va[j] = (uint32_t)(source((wave * kA + j) * 8 + lrow) * a.a.ldc) + piece(j) * 16;
+#pragma unroll
+  for (int j = 0; j < kB; ++j) {
+    const int64_t n = (wave * kB + j) * 8 + lrow;
+    vb[j] = (uint32_t)((n < last_n ? n : last_n) * a.w.ldc) + piece(j) * 16;
+  }
+  // which 16 rows' scales a wave loads (the last ones twice where they do not go round)
+  const int sdw = lane & 3;
+  auto scale_part = [&](int j) {
+    const int i = wave * kS + j;
+    return i < kSI ? i : kSI - 1;
+  };
+#pragma unroll
+  for (int j = 0; j < kS; ++j) {
+    const int i = scale_part(j), row = i * 16 + (lane >> 2);
+    if (i * 16 < BM) {
+      vs[j] = (uint32_t)(source(row) * a.a.lds) + sdw * 4;
+    } else {
+      const int64_t n = row - BM;
+      vs[j] = (uint32_t)((n < last_n ? n : last_n) * a.w.lds) + sdw * 4;
+    }
+  }
+
+  // Stage s into buffer s % D, and with an even one the scales of it and the next.
+  // Pieces past the row's last block and words past its last scale are read from the
+  // stage's first (the cut stage puts them to zero).  A stage past the last one asks
+  // for nothing: its buffers' range is empty, so that every round of the loop has the
+  // same loads to wait for.
+  const int G = (int)a.w.G, full = G / 8, stages = (G + 7) / 8, words = (G + 3) / 4;
+  auto issue = [&](int s, auto with_scales) {
+    lds_u8* const to = ring + (s % D) * L::kStage;
+    const int range = s < stages ? 0x7fffffff : 0;
+    auto back = [&](int j) { return s * 8 + piece(j) < G ? 0u : piece(j) * 16u; };
+#pragma unroll
+    for (int j = 0; j < kA; ++j)
+      dma_to_lds<16>(abase, range, to + (wave * kA + j) * 1024, va[j] - back(j),
+                     s * 128);
+#pragma unroll
+    for (int j = 0; j < kB; ++j)
+      dma_to_lds<16>(wbase, range, to + BM * 128 + (wave * kB + j) * 1024, vb[j] - back(j),
+                     s * 128);
+    if constexpr (decltype(with_scales)::value) {
+      lds_u8* const st = scales + ((s >> 1) % L::kSpans) * L::kScales;
+      const uint32_t sback = s * 2 + sdw < words ? 0u : sdw * 4u;
+#pragma unroll
+      for (int j = 0; j < kS; ++j) {
+        const int i = scale_part(j);
+        dma_to_lds<4>(i * 16 < BM ? sabase : swbase, range, st + i * 256, vs[j] - sback,
+                      s * 8);
+      }
+    }
+  };
+
+  f32x16 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  const int l32 = lane & 31, half = lane >> 5;
+  const uint32_t sel = half ? 0x07050301u : 0x06040200u;  // the half's scale of each 64 K
+  auto mine = [&](const lds_u8* at) {
+    const u32x2 v = *(const __attribute__((address_space(3))) u32x2*)at;
+    return __builtin_amdgcn_perm(v.y, v.x, sel);
+  };
+  const int arow = wm * 32 * FM + l32, brow = wn * 32 * FN + l32;
+  struct Operands {
+    u32x4 x[FM], w[FN];
+  };
+  struct Scales {
+    uint32_t a[FM], w[FN];
+  };
+  auto read = [&](Operands& o, int s, int step) {
+    const lds_u8* const from = ring + (s % D) * L::kStage;
+    const int at = ((2 * step + half) ^ turn(l32)) * 16;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+      o.w[i] = *(const __attribute__((address_space(3))) u32x4*)(
+          from + (BM + brow + i * 32) * 128 + at);
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+      o.x[j] = *(const __attribute__((address_space(3))) u32x4*)(
+          from + (arow + j * 32) * 128 + at);
+  };
+  auto read_scales = [&](Scales& o, int s) {
+    const lds_u8* const st =
+        scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) o.a[j] = mine(st + (arow + j * 32) * 16);
+#pragma unroll
+    for (int i = 0; i < FN; ++i) o.w[i] = mine(st + (BM + brow + i * 32) * 16);
+  };
+  auto multiply = [&](auto which, const Operands& o, const Scales& c) {
+    constexpr int S = decltype(which)::value;
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+        acc[i][j] = mx_mfma32<S>(o.w[i], c.w[i], o.x[j], c.a[j], acc[i][j]);
+  };
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
+  using S2 = std::integral_constant<int, 2>;
+  using S3 = std::integral_constant<int, 3>;
+  using std::false_type;
+  using std::true_type;
+
+  // The next stage is in LDS for everyone (all loads but those of the D - 2 stages
+  // after it are done; of two stages running one brings scales), and everyone has
+  // read all of this one, whose buffer is filled next.
+  constexpr int kAllowed = (D - 2) * (kA + kB) + (D - 2) / 2 * kS;
+  static_assert((D == 2 || D == 4) && kAllowed < 64, "vmcnt range");
+  auto arrive = [&]() {
+    wait_vmcnt<kAllowed>();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  };
+  issue(0, true_type{});
+#pragma unroll
+  for (int s = 1; s < D - 1; ++s) {
+    if (s & 1)
+      issue(s, false_type{});
+    else
+      issue(s, true_type{});
+  }
+  arrive();
+  issue(D - 1, false_type{});
+  Operands even, odd;
+  Scales now, next;
+  read(even, 0, 0);
+  read_scales(now, 0);
+  // (no branch in the loop: the compiler would move the MFMAs past it, behind the
+  // barrier)
+  auto stage = [&](int s, auto with_scales) {
+    read(odd, s, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(S0{}, even, now);
+    __builtin_amdgcn_sched_barrier(0);
+    read(even, s, 2);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(S1{}, odd, now);
+    __builtin_amdgcn_sched_barrier(0);
+    read(odd, s, 3);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(S2{}, even, now);
+    __builtin_amdgcn_sched_barrier(0);
+    arrive();
+    issue(s + D, with_scales);
+    read(even, s + 1, 0);
+    read_scales(next, s + 1);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(S3{}, odd, now);
+    __builtin_amdgcn_sched_barrier(0);
+    now = next;
+  };
+  const int pairs = full / 2;
+  for (int t = 0; t < pairs; ++t) {
+    stage(2 * t, true_type{});
+    stage(2 * t + 1, false_type{});
+  }
+  wait_vmcnt<0>();
+  __syncthreads();
+  // a last odd stage, and the one that K cuts: zero codes and scales past the last
+  // block (all their loads are done: at most two stages are left, and D were under
+  // way)
+#pragma unroll 1
+  for (int s = 2 * pairs; s < stages; ++s) {
+    const int left = G - s * 8;
+    if (left < 8) {
+      lds_u8* const to = ring + (s % D) * L::kStage;
+      lds_u8* const st = scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8;
+      for (int i = threadIdx.x; i < (BM + BN) * 8; i += NW * 64) {
+        if (((i & 7) ^ turn(i >> 3)) >= left)
+          *(__attribute__((address_space(3))) u32x4*)(to + i * 16) = u32x4{0, 0, 0, 0};
+        if ((i & 7) >= left) st[(i >> 3) * 16 + (i & 7)] = 0;
+      }
+      __syncthreads();
+    }
+    read_scales(now, s);
+    read(even, s, 0);
+    multiply(S0{}, even, now);
+    read(even, s, 1);
+    multiply(S1{}, even, now);
+    read(even, s, 2);
+    multiply(S2{}, even, now);
+    read(even, s, 3);
+    multiply(S3{}, even, now);
+  }
+  __syncthreads();
+
+  // out: 32 rows at a time through the wave's own LDS, so that a lane stores eight
+  // neighbouring channels
+  float* const out = reinterpret_cast<float*>(mx_lds) + wave * 32 * L::kOutLd;
+  constexpr int kPieces8 = 4 * FN, kRowsPass = 64 / kPieces8;
+  const int p8 = lane % kPieces8, row_in = lane / kPieces8;
+  const int64_t col = n0 + wn * 32 * FN + p8 * 8;
+  float bias[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    bias[j] = a.bias && col + j < N ? a.bias[tile.expert * N + col + j] : 0.0f;
+  // (the loops are kept rolled: unrolled with all the types' stores they are tens of
+  // kilobytes, and fetching those took longer than a short product)
+#pragma unroll 1
+  for (int f = 0; f < FM; ++f) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+      if (j == f) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(out + l32 * L::kOutLd + i * 32 + q * 8 + half * 4) =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                      acc[i][j][4 * q + 3]};
+      }
+    wave_sync();
+#pragma unroll 1
+    for (int h = 0; h < 32; h += kRowsPass) {
+      const int64_t r = tile.r0 + (wm * FM + f) * 32 + h + row_in;
+      if (r < tile.r1 && col < N) {
+        const float* src = out + (h + row_in) * L::kOutLd + p8 * 8;
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
+        const bool none = w4_source_row(a.rows, r) < 0;
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float v = (none ? 0.0f : j < 4 ? lo[j % 4] : hi[j % 4]) + bias[j];
+          v = v < a.lo ? a.lo : v;
+          y[j] = v > a.hi ? a.hi : v;
+        }
+        w4_store8(a.Y, a.y_dtype, r * a.ldy + col, y, N - col < 8 ? (int)(N - col) : 8);
+      }
+    }
+    wave_sync();
+  }
+}
+
+template <int BM, int BN, int WM, int WN, int D>
+qp_status launch_tile(const MxArgs& a, hipStream_t stream) {
+  using L = A4Tile<BM, BN, WM, WN, D>;
+  const int64_t slots = w4_tile_slots(a.rows, BM), groups = ceil_div(a.w.rows, BN);
+  QP_REQUIRE(slots * groups * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
+             "qgemm_a4w4_mx: rows and channels for more than 2^32 threads");
+  auto kern = mx_a4w4_tile_kernel<BM, BN, WM, WN, D>;
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds) != hipSuccess)
+    QP_FAIL(QP_EHIP, "qgemm_a4w4_mx: %d bytes of LDS are not to be had", L::kLds);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * groups)), dim3(L::NW * 64), L::kLds, stream, a,
+                     (uint32_t)slots, (uint32_t)groups);
+  return check_launch("qgemm_a4w4_mx (many rows)");
+}
+
+// Which kernel: the one whose time the following estimate puts lowest.  A shape
+// takes `first` microseconds for up to one workgroup a CU (256) and `more` for every
+// further round of them, at K = 4096 (both grow with K, which changes no order).
+// Measured, cold weights: e.g. 1 x 4096 rows 5.2, 64 x 64 tiles 8.1 us; 32 x 4096
+// 10.1 and 8.4; 256 x 4096 59, 9.1, 128 x 128 tiles 16; 512 x 11008 tiles of 64 / 128 /
+// 256 31.9, 25.2, 36.9; 4096 x 4096 82, 53, 45.
+struct A4Cost {
+  A4Shape shape;
+  int rows, channels;
+  double first, more;
+};
+constexpr A4Cost kA4Shapes[] = {
+    {kA4Rows, 16, 16, 5.2, 3.0},
+    {kA4Tile64, 64, 64, 8.1, 4.4},
+    {kA4Tile128, 128, 128, 16.0, 11.5},
+    {kA4Tile256, 256, 256, 35.0, 37.0},
+};
+
+A4Shape a4_choose(int64_t M, int64_t parts, int64_t N) {
+  const double experts = (double)(parts < M ? parts : M);
+  const double each = (double)M / experts;  // rows of an expert, if all were alike
+  A4Shape best = kA4Rows;
+  double least = 1e300;
+  for (const A4Cost& s : kA4Shapes) {
+    // row tiles of an expert: its last one is half empty on average
+    double tiles = (double)ceil_div(M, s.rows);
+    if (experts > 1.0) {
+      tiles = each / s.rows + 0.5;
+      tiles = experts * (tiles > 1.0 ? tiles : 1.0);
+    }
+    const double rounds = tiles * (double)ceil_div(N, s.channels) / 256.0;
+    const double cost = s.first + s.more * (rounds > 1.0 ? rounds - 1.0 : 0.0);
+    if (cost < least) {
+      least = cost;
+      best = s.shape;
+    }
+  }
+  return best;
+}
+
+// The tiles' direct loads take 32-bit offsets from a tile's first row (from row 0
+// through a map).
+bool tiles_reach(const MxArgs& a) {
+  const int64_t most = (INT64_C(1) << 31) - 1;
+  if (a.w.ldc * 256 > most || a.a.ldc * 256 > most) return false;
+  return !a.rows.map || (a.a.rows * a.a.ldc <= most && a.a.rows * a.a.lds <= most);
+}
+
+}  // namespace
+
+qp_status run_mx_a4w4(const MxArgs& a, hipStream_t stream) {
+  if (tiles_reach(a)) {
+    switch (a4_choose(a.rows.M, a.rows.offsets ? a.rows.experts : 1, a.w.rows)) {
+      case kA4Tile256: return launch_tile<256, 256, 2, 4, 2>(a, stream);
+      case kA4Tile128: return launch_tile<128, 128, 2, 2, 2>(a, stream);
+      case kA4Tile64: return launch_tile<64, 64, 2, 2, 4>(a, stream);
+      case kA4Rows: break;
+    }
+  }
+  return mx_launch_rows<mx4_t, 1, 1, 8, 1>(a, stream);
+}
+
 }  // namespace qp
