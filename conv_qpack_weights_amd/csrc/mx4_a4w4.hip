@@ -6,13 +6,12 @@
 #include <type_traits>
 
 #include "mx4_rows.hpp"
+#include "mx4_tile.hpp"
 
 #pragma clang fp contract(off)
 
 namespace qp {
 namespace {
-
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 // d + a b^T over 64 K: lane l holds 32 values of row l%32 from 32 (l/32) on; their
 // scale is byte kByte of sa / sb.
@@ -24,26 +23,11 @@ __device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, uint32_t sa, u32x4 b, uint3
                                                          (int)sb);
 }
 
-// kBytes per lane from base + voff + soff straight into LDS, lane after lane from dst
-// on; offsets of `range` bytes and more ask for nothing.  (The caller waits.)
-template <int kBytes>
-__device__ __forceinline__ void dma_to_lds(const void* base, int range, lds_u8* dst, uint32_t voff,
-                                           uint32_t soff) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __amdgpu_buffer_rsrc_t r =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, range, 0x00020000);
-  if constexpr (kBytes == 16)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)dst, 16, voff, soff, 0, 0);
-  else
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)dst, 4, voff, soff, 0, 0);
-#endif
-}
-
 // ---- many rows -----------------------------------------------------------------
 // A workgroup owns BM rows x BN channels, its WM x WN waves 32 FM rows x 32 FN
 // channels each, in registers.  256 K of rows and channels at a time, a stage, come
 // into one of D LDS buffers by direct loads, 128 bytes of a row side by side; the
-// 16-byte piece c of row r lies at place c ^ turn(r) of the row's eight, so that the
+// 16-byte piece c of row r lies at place c ^ mx_turn(r) of the row's eight, so that the
 // rows an operand takes piece c of meet every bank alike.  The weights are the
 // MFMA's first operand: a lane ends with one row and runs of four channels.
 enum A4Shape { kA4Rows, kA4Tile64, kA4Tile128, kA4Tile256 };
@@ -53,7 +37,7 @@ struct A4Tile {
   static constexpr int NW = WM * WN, FM = BM / (32 * WM), FN = BN / (32 * WN);
   static constexpr int kStage = (BM + BN) * 128, kScales = (BM + BN) * 16;
   static constexpr int kSpans = D == 2 ? 2 : 4;  // of 512 K: D / 2 + 1 are live
-  static constexpr int kOutLd = 32 * FN + 4;
+  static constexpr int kOutLd = mx_out_ld(FN);
   static constexpr int kOut = NW * 32 * kOutLd * 4;
   static constexpr int kRing = D * kStage + kSpans * kScales;
   static constexpr int kLds = kRing > kOut ? kRing : kOut;
@@ -67,9 +51,6 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW, kSI = (BM + BN) / 16,
                 kS = (kSI + NW - 1) / NW;
   static_assert(kA * 8 * NW == BM && kB * 8 * NW == BN && BM % 16 == 0, "shares");
-  // piece c of row r lies at place c ^ turn(r) of the row's eight: the 16 rows whose
-  // pieces are read at a time are at 16 different places of the banks' 256 bytes
-  auto turn = [](int r) { return (r >> 1) & 7; };
   extern __shared__ __attribute__((aligned(16))) uint8_t mx_lds[];
   lds_u8* const ring = (lds_u8*)mx_lds;
   lds_u8* const scales = ring + D * L::kStage;
@@ -77,12 +58,9 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
 
-  // eight row tiles by neighbouring channel groups, in runs per XCD
-  const uint32_t id = xcd_run(blockIdx.x, gridDim.x);
-  const uint32_t band = id / (8 * col_groups), in_band = id - band * 8 * col_groups;
-  const uint32_t band_rows = row_slots - band * 8 < 8 ? row_slots - band * 8 : 8;
-  const uint32_t slot = band * 8 + in_band % band_rows;
-  const int64_t n0 = (int64_t)(in_band / band_rows) * BN;
+  uint32_t slot, group;
+  mx_place(row_slots, col_groups, slot, group);
+  const int64_t n0 = (int64_t)group * BN;
   const int64_t N = a.w.rows;
   const W4Tile tile = w4_find_tile<BM>(a.rows, slot);
   if (tile.expert < 0) return;
@@ -96,7 +74,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   // what a lane loads: a piece of row lane / 8 of eight; rows past the tile's end
   // repeat its last row
   const int lrow = lane >> 3;
-  auto piece = [&](int j) { return (lane & 7) ^ turn(j * 8 + lrow); };
+  auto piece = [&](int j) { return (lane & 7) ^ mx_turn(j * 8 + lrow); };
   static_assert(kA % 2 == 0 && kB % 2 == 0, "turn of a wave's first row");
   const uint8_t *abase = a.a.codes, *sabase = a.a.scales;
   int64_t first = 0;
@@ -193,7 +171,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   };
   auto read = [&](Operands& o, int s, int step) {
     const lds_u8* const from = ring + (s % D) * L::kStage;
-    const int at = ((2 * step + half) ^ turn(l32)) * 16;
+    const int at = ((2 * step + half) ^ mx_turn(l32)) * 16;
 #pragma unroll
     for (int i = 0; i < FN; ++i)
       o.w[i] = *(const __attribute__((address_space(3))) u32x4*)(
@@ -290,7 +268,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
       lds_u8* const to = ring + (s % D) * L::kStage;
       lds_u8* const st = scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8;
       for (int i = threadIdx.x; i < (BM + BN) * 8; i += NW * 64) {
-        if (((i & 7) ^ turn(i >> 3)) >= left)
+        if (((i & 7) ^ mx_turn(i >> 3)) >= left)
           *(__attribute__((address_space(3))) u32x4*)(to + i * 16) = u32x4{0, 0, 0, 0};
         if ((i & 7) >= left) st[(i >> 3) * 16 + (i & 7)] = 0;
       }
@@ -308,52 +286,8 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   }
   __syncthreads();
 
-  // out: 32 rows at a time through the wave's own LDS, so that a lane stores eight
-  // neighbouring channels
-  float* const out = reinterpret_cast<float*>(mx_lds) + wave * 32 * L::kOutLd;
-  constexpr int kPieces8 = 4 * FN, kRowsPass = 64 / kPieces8;
-  const int p8 = lane % kPieces8, row_in = lane / kPieces8;
-  const int64_t col = n0 + wn * 32 * FN + p8 * 8;
-  float bias[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    bias[j] = a.bias && col + j < N ? a.bias[tile.expert * N + col + j] : 0.0f;
-  // (the loops are kept rolled: unrolled with all the types' stores they are tens of
-  // kilobytes, and fetching those took longer than a short product)
-#pragma unroll 1
-  for (int f = 0; f < FM; ++f) {
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-      if (j == f) {
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<f32x4*>(out + l32 * L::kOutLd + i * 32 + q * 8 + half * 4) =
-                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                      acc[i][j][4 * q + 3]};
-      }
-    wave_sync();
-#pragma unroll 1
-    for (int h = 0; h < 32; h += kRowsPass) {
-      const int64_t r = tile.r0 + (wm * FM + f) * 32 + h + row_in;
-      if (r < tile.r1 && col < N) {
-        const float* src = out + (h + row_in) * L::kOutLd + p8 * 8;
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
-        const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
-        const bool none = w4_source_row(a.rows, r) < 0;
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float v = (none ? 0.0f : j < 4 ? lo[j % 4] : hi[j % 4]) + bias[j];
-          v = v < a.lo ? a.lo : v;
-          y[j] = v > a.hi ? a.hi : v;
-        }
-        w4_store8(a.Y, a.y_dtype, r * a.ldy + col, y, N - col < 8 ? (int)(N - col) : 8);
-      }
-    }
-    wave_sync();
-  }
+  mx_store_tile<FM, FN>(acc, a, tile, wm * FM * 32, n0 + wn * FN * 32,
+                        reinterpret_cast<float*>(mx_lds) + wave * 32 * L::kOutLd);
 }
 
 template <int BM, int BN, int WM, int WN, int D>

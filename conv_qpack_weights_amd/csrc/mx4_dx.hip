@@ -6,7 +6,11 @@
 // channels' scales, exactly, and pairs the channels' halves up (32 conversions
 // and 32 v_perm for eight operands, no LDS): operand j then holds column 8 i + j
 // in lane i of 16, and a lane ends with eight neighbouring columns of a row.
+#include <cstdlib>
+#include <type_traits>
+
 #include "mx4.hpp"
+#include "mx4_tile.hpp"
 
 #pragma clang fp contract(off)
 
@@ -173,6 +177,359 @@ __global__ __launch_bounds__(256) void mx_dx_sum_kernel(const float* __restrict_
   w4_store8(dX, dtype, r * lddx + k, y, n);
 }
 
+// ---- many rows -----------------------------------------------------------------
+// A workgroup owns BM rows x BC columns, its WM x WN waves 32 FM x 64 each, in
+// registers.  The channels go by in stages of 64: dY's stage (of f32 rows a plane for
+// each of the three bf16 pieces) comes into one of two LDS buffers by direct loads or
+// through registers, as the rows of mx4_w4_tile.hpp; the weights' through registers:
+// a thread takes four columns (two bytes) of eight channels, a stage ahead, converts
+// and pairs them up, and writes for each of its columns the eight channels' values,
+// 16 bytes, to the other buffer, so that every weight is converted once in a
+// workgroup.  In that buffer column 4u + j of a wave's 64 is row 16 j + u: 16 threads
+// then write 16 rows, whose places meet every bank alike (mx_turn).
+// f16 rows: as there, with f16 weights where a look over the scales allows it.
+template <typename T, int BM, int BC, int WM, int WN>
+struct MxDxTile {
+  static constexpr int NW = WM * WN, FM = BM / (32 * WM);
+  static constexpr int NP = sizeof(T) == 4 ? 3 : 1;
+  static constexpr int kX = BM * 128 * NP, kW = BC * 128;
+  static constexpr int kRing = 2 * (kX + kW);
+  static constexpr int kOutLd = 64 + 4;
+  static constexpr int kOut = NW * 32 * kOutLd * 4;
+  static constexpr int kLds = kRing > kOut ? kRing : kOut;
+};
+
+template <typename T, bool kDirect, int BM, int BC, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, uint32_t row_slots,
+                                                                 uint32_t col_groups) {
+  using L = MxDxTile<T, BM, BC, WM, WN>;
+  constexpr int NW = L::NW, FM = L::FM, FN = 2, NP = L::NP;
+  constexpr bool kF16 = __is_same(T, f16_t);
+  constexpr int kA = BM / 8 / NW;  // pieces of eight elements of dY a thread and stage
+  static_assert(kA * 8 * NW == BM && kA % 2 == 0 && BC == 64 * WN && BC == 32 * NW, "shares");
+  extern __shared__ __attribute__((aligned(16))) uint8_t mx_lds[];
+  lds_u8* const xbuf = (lds_u8*)mx_lds;
+  lds_u8* const wbuf = xbuf + 2 * L::kX;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  uint32_t slot, group;
+  mx_place(row_slots, col_groups, slot, group);
+  const int64_t k0 = (int64_t)group * BC;
+  const int64_t N = a.w.rows, K = a.w.K;
+  const W4Tile tile = w4_find_tile<BM>(a.rows, slot);
+  if (tile.expert < 0) return;
+  if (a.rows.offsets && tile.expert == a.rows.experts) {  // rows of no expert
+    for (int64_t r = tile.r0 + wave; r < tile.r1; r += NW)
+      for (int64_t k = k0 + lane; k < k0 + BC && k < K; k += 64)
+        w4_store(a.dX, a.dtype, r * a.lddx + k, 0.0f);
+    return;
+  }
+
+  // dY: a lane loads a piece of row lane / 8 of eight; rows past the tile's end repeat
+  // its last row
+  const int lrow = lane >> 3;
+  auto piece = [&](int j) { return (lane & 7) ^ mx_turn(j * 8 + lrow); };
+  const T* const xbase = static_cast<const T*>(a.dY) + tile.r0 * a.lddy;
+  auto row_of = [&](int j) {
+    const int64_t r = (wave * kA + j) * 8 + lrow, last = tile.r1 - 1 - tile.r0;
+    return (r < last ? r : last) * a.lddy;
+  };
+  uint32_t vx[kDirect ? kA : 1];
+  const T* px[kDirect ? 1 : kA];
+#pragma unroll
+  for (int j = 0; j < kA; ++j) {
+    if constexpr (kDirect)
+      vx[j] = (uint32_t)(row_of(j) * (int64_t)sizeof(T)) + piece(j) * 16;
+    else
+      px[j] = xbase + row_of(j);
+  }
+  const int full = (int)(N / 64);
+  auto issue_x = [&](int s) {
+    const int range = s < full ? 0x7fffffff : 0;
+    lds_u8* const to = xbuf + (s & 1) * L::kX;
+#pragma unroll
+    for (int j = 0; j < kA; ++j)
+      dma_to_lds<16>(xbase, range, to + (wave * kA + j) * 1024, vx[j], s * 128);
+  };
+  // through registers: stage s, the part before N
+  auto put = [&](const MxFrag<T>& f, int s, int j) {
+    lds_u8* const at =
+        xbuf + (s & 1) * L::kX + ((wave * kA + j) * 8 + lrow) * 128 + (lane & 7) * 16;
+    if constexpr (NP == 1) {
+      *(__attribute__((address_space(3))) u32x4*)at = f.v;
+    } else {
+      bf16x8 v[NP];
+      f.split(v);
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        *(__attribute__((address_space(3))) bf16x8*)(at + i * BM * 128) = v[i];
+    }
+  };
+  auto fetch_full = [&](MxFrag<T> (&f)[kA], int s) {
+#pragma unroll
+    for (int j = 0; j < kA; ++j)
+      f[j].load(px[kDirect ? 0 : j] + (int64_t)s * 64 + piece(j) * 8);
+  };
+
+  // the weights: columns 4u .. 4u + 3 of channels 8g .. 8g + 7 of a stage
+  const int u = threadIdx.x % (BC / 4), g = threadIdx.x / (BC / 4);
+  const bool col_in = k0 / 32 + u / 8 < a.w.G;  // (else the row's first: not stored)
+  const uint8_t* const codes =
+      a.w.codes + tile.expert * a.w.cstride + (col_in ? k0 / 2 + 2 * u : 0);
+  const uint8_t* const scales =
+      a.w.scales + tile.expert * a.w.sstride + (col_in ? k0 / 32 + u / 8 : 0);
+  struct Raw {
+    uint32_t q[8], s[8];
+  };
+  auto load_w = [&](Raw& w, int s) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      int64_t n = (int64_t)s * 64 + g * 8 + i;
+      n = n < N ? n : N - 1;
+      w.q[i] = *reinterpret_cast<const uint16_t*>(codes + n * a.w.ldc);
+      w.s[i] = scales[n * a.w.lds];
+    }
+  };
+  auto convert = [&](const Raw& w, int s, auto kind) {
+    uint32_t c[8][2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // (a channel past the last: its scale could be a NaN)
+      const float by = mx_scale((int64_t)s * 64 + g * 8 + i < N ? w.s[i] : 0u);
+      if constexpr (decltype(kind)::value) {
+        c[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 0));
+        c[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 1));
+      } else {
+        c[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.q[i], by, 0));
+        c[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.q[i], by, 1));
+      }
+    }
+    lds_u8* const to = wbuf + (s & 1) * L::kW;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u32x4 v;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        v[r] = j & 1 ? hi_halves(c[2 * r][j / 2], c[2 * r + 1][j / 2])
+                     : lo_halves(c[2 * r][j / 2], c[2 * r + 1][j / 2]);
+      const int row = u / 16 * 64 + j * 16 + u % 16;
+      *(__attribute__((address_space(3))) u32x4*)(to + row * 128 + (g ^ mx_turn(row)) * 16) = v;
+    }
+  };
+
+  f32x16 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  const int l32 = lane & 31, half = lane >> 5;
+  const int arow = wm * 32 * FM + l32, brow = wn * 64 + l32;
+  struct Operands {
+    u32x4 x[FM][NP], w[FN];
+  };
+  // 16 channels a step: lane l holds eight of row l%32 from 8 (l/32) on
+  auto read = [&](Operands& o, int s, int step) {
+    const lds_u8* const fx = xbuf + (s & 1) * L::kX;
+    const lds_u8* const fw = wbuf + (s & 1) * L::kW;
+    const int at = ((2 * step + half) ^ mx_turn(l32)) * 16;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+      o.w[i] = *(const __attribute__((address_space(3))) u32x4*)(fw + (brow + i * 32) * 128 + at);
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int n = 0; n < NP; ++n)
+        o.x[j][n] = *(const __attribute__((address_space(3))) u32x4*)(
+            fx + (n * BM + arow + j * 32) * 128 + at);
+  };
+  auto multiply = [&](const Operands& o, auto kind) {
+    constexpr bool kAsF16 = decltype(kind)::value;
+    constexpr int kPieces = kF16 && !kAsF16 ? 2 : NP;
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      if constexpr (kAsF16) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+          acc[i][j] = mx_mfma_f16(__builtin_bit_cast(f16x8, o.w[i]),
+                                  __builtin_bit_cast(f16x8, o.x[j][0]), acc[i][j]);
+      } else {
+        bf16x8 xv[kPieces];
+        if constexpr (kF16)
+          MxFrag<f16_t>{o.x[j][0]}.split(xv);
+        else
+#pragma unroll
+          for (int n = 0; n < NP; ++n) xv[n] = __builtin_bit_cast(bf16x8, o.x[j][n]);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int n = 0; n < kPieces; ++n)
+            acc[i][j] = mx_mfma_bf16(__builtin_bit_cast(bf16x8, o.w[i]), xv[n], acc[i][j]);
+      }
+    }
+  };
+
+  using std::false_type;
+  using std::true_type;
+  // everyone's share of the next stage is there, and everyone has read all of this one
+  auto arrive = [&]() {
+    wait_vmcnt<0>();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  };
+  auto run = [&](auto kind) {
+    Raw raw;
+    MxFrag<T> f[kA];
+    load_w(raw, 0);
+    if constexpr (kDirect) {
+      issue_x(0);
+    } else if (full > 0) {
+      fetch_full(f, 0);
+#pragma unroll
+      for (int j = 0; j < kA; ++j) put(f[j], 0, j);
+    }
+    convert(raw, 0, kind);
+    arrive();
+    load_w(raw, 1);
+    if constexpr (kDirect) issue_x(1);
+    Operands even, odd;
+    if constexpr (kDirect) {
+      read(even, 0, 0);
+      // (no branch between MFMAs, as in the products)
+      for (int s = 0; s < full; ++s) {
+        read(odd, s, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(even, kind);
+        __builtin_amdgcn_sched_barrier(0);
+        read(even, s, 2);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(odd, kind);
+        __builtin_amdgcn_sched_barrier(0);
+        read(odd, s, 3);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(even, kind);
+        __builtin_amdgcn_sched_barrier(0);
+        convert(raw, s + 1, kind);
+        __builtin_amdgcn_sched_barrier(0);
+        arrive();
+        load_w(raw, s + 2);
+        issue_x(s + 2);
+        read(even, s + 1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(odd, kind);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      for (int s = 0; s < full; ++s) {
+        fetch_full(f, s + 1 < full ? s + 1 : s);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          read(even, s, t);
+          multiply(even, kind);
+        }
+        convert(raw, s + 1, kind);
+#pragma unroll
+        for (int j = 0; j < kA; ++j) put(f[j], s + 1, j);
+        arrive();
+        load_w(raw, s + 2);
+      }
+    }
+    wait_vmcnt<0>();
+    __syncthreads();
+    if ((int64_t)full * 64 < N) {
+      // the stage that N cuts: its rows through registers, zeros from N on (its weights
+      // are there)
+#pragma unroll 1
+      for (int j = 0; j < kA; ++j) {
+        const int64_t n = (int64_t)full * 64 + piece(j) * 8, left = N - n;
+        const T* p = xbase + row_of(j);
+        MxFrag<T> one;
+        one.load_n(p + (left > 0 ? n : 0), left > 8 ? 8 : left < 0 ? 0 : (int)left);
+        put(one, full, j);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        read(even, full, t);
+        multiply(even, kind);
+      }
+      __syncthreads();
+    }
+  };
+  if constexpr (kF16) {
+    bool fit = true;
+    const int blocks = a.w.G - k0 / 32 < BC / 32 ? (int)(a.w.G - k0 / 32) : BC / 32;
+    const uint8_t* const sc = a.w.scales + tile.expert * a.w.sstride + k0 / 32;
+#pragma unroll 4
+    for (int64_t n = threadIdx.x; n < N; n += NW * 64) {
+#pragma unroll
+      for (int w = 0; w < BC / 128; ++w) {  // (rows are whole words)
+        const uint32_t v = w * 4 < blocks
+                               ? *reinterpret_cast<const uint32_t*>(sc + n * a.w.lds + w * 4) : 0u;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          fit = fit && (w * 4 + b >= blocks || ((v >> (8 * b)) & 0xffu) - 104u <= 36u);
+      }
+    }
+    if (__syncthreads_and(fit))
+      run(true_type{});
+    else
+      run(false_type{});
+  } else {
+    run(false_type{});
+  }
+
+  // out: 32 rows at a time through the wave's own LDS
+  float* const out = reinterpret_cast<float*>(mx_lds) + wave * 32 * L::kOutLd;
+  const int p8 = lane & 7, row_in = lane >> 3;
+  const int64_t col = k0 + wn * 64 + p8 * 8;
+#pragma unroll 1
+  for (int f = 0; f < FM; ++f) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+      if (j == f) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int at = i * 32 + 8 * (r / 4) + r % 4;  // + 4 half: the weights' row
+            out[l32 * L::kOutLd + 4 * (at % 16 + 4 * half) + at / 16] = acc[i][j][r];
+          }
+      }
+    wave_sync();
+#pragma unroll 1
+    for (int h = 0; h < 32; h += 8) {
+      const int64_t r = tile.r0 + (wm * FM + f) * 32 + h + row_in;
+      if (r < tile.r1 && col < K) {
+        const float* src = out + (h + row_in) * L::kOutLd + p8 * 8;
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
+        const float y[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        w4_store8(a.dX, a.dtype, r * a.lddx + col, y, K - col < 8 ? (int)(K - col) : 8);
+      }
+    }
+    wave_sync();
+  }
+}
+
+template <typename T, bool kDirect, int BM, int BC, int WM, int WN>
+qp_status launch_dx_tile(const char* what, const MxDxArgs& a, hipStream_t stream) {
+  using L = MxDxTile<T, BM, BC, WM, WN>;
+  const int64_t slots = w4_tile_slots(a.rows, BM), groups = ceil_div(a.w.K, BC);
+  QP_REQUIRE(slots * groups * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
+             "%s: rows and columns for more than 2^32 threads", what);
+  auto kern = mx_dx_tile_kernel<T, kDirect, BM, BC, WM, WN>;
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds) != hipSuccess)
+    QP_FAIL(QP_EHIP, "%s: %d bytes of LDS are not to be had", what, L::kLds);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * groups)), dim3(L::NW * 64), L::kLds, stream, a,
+                     (uint32_t)slots, (uint32_t)groups);
+  return check_launch(what);
+}
+
 // In how many splits the channels go: enough workgroups for the card, no split
 // without a step of 32 channels for each of its waves.
 constexpr int kDxWaves = 8;
@@ -220,6 +577,18 @@ qp_status run_dx(const char* what, const void* dY, int32_t dtype, int64_t M, int
              "%s: the workspace must be 256-byte aligned", what);
   MxDxArgs a{mx_view(w), W4Rows{offsets, (int32_t)w->matrices, M, nullptr, 1, M}, dY, lddy, dX,
              dtype, lddx, static_cast<float*>(ws)};
+  {
+    const char* e = getenv("MXD");
+    const int t = e ? atoi(e) : 0;
+    const bool al = (uintptr_t)dY % 4 == 0 && lddy % 2 == 0;
+    if (t == 1 && al && dtype == QP_BF16) return launch_dx_tile<bf16_t, true, 256, 256, 2, 4>(what, a, stream);
+    if (t == 1 && al && dtype == QP_F16) return launch_dx_tile<f16_t, true, 256, 256, 2, 4>(what, a, stream);
+    if (t == 2 && al && dtype == QP_BF16) return launch_dx_tile<bf16_t, true, 128, 128, 2, 2>(what, a, stream);
+    if (t == 2 && al && dtype == QP_F16) return launch_dx_tile<f16_t, true, 128, 128, 2, 2>(what, a, stream);
+    if (t && dtype == QP_BF16) return launch_dx_tile<bf16_t, false, 128, 128, 2, 2>(what, a, stream);
+    if (t && dtype == QP_F16) return launch_dx_tile<f16_t, false, 128, 128, 2, 2>(what, a, stream);
+    if (t) return launch_dx_tile<float, false, 128, 128, 2, 2>(what, a, stream);
+  }
   const int64_t slots = w4_tile_slots(a.rows, 16), cols = ceil_div(w->K, 128);
   QP_REQUIRE(slots * cols * splits * kDxWaves * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
              "%s: rows and columns for more than 2^32 threads", what);

@@ -1,0 +1,110 @@
+// mx4_tile.hpp -- what the many-row kernels of the MXFP4 products share: direct
+// loads into LDS, the order of the tiles, the way out.
+#pragma once
+
+#include "mx4.hpp"
+
+#pragma clang fp contract(off)
+
+namespace qp {
+namespace {
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+// kBytes per lane from base + voff + soff straight into LDS, lane after lane from dst
+// on; offsets of `range` bytes and more ask for nothing.  (The caller waits.)
+template <int kBytes>
+__device__ __forceinline__ void dma_to_lds(const void* base, int range, lds_u8* dst, uint32_t voff,
+                                           uint32_t soff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __amdgpu_buffer_rsrc_t r =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, range, 0x00020000);
+  if constexpr (kBytes == 16)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)dst, 16, voff, soff, 0, 0);
+  else
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)dst, 4, voff, soff, 0, 0);
+#endif
+}
+
+// Rows of 128 bytes in LDS: the 16-byte piece c of row r lies at place c ^ mx_turn(r)
+// of the row's eight, so that the 16 rows whose pieces are read at a time are at 16
+// different places of the banks' 256 bytes.
+__device__ __forceinline__ int mx_turn(int r) { return (r >> 1) & 7; }
+
+__device__ __forceinline__ f32x16 mx_mfma_bf16(bf16x8 a, bf16x8 b, f32x16 d) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, d, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x16 mx_mfma_f16(f16x8 a, f16x8 b, f32x16 d) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, d, 0, 0, 0);
+}
+
+// Which tile a workgroup takes: eight row tiles by neighbouring channel groups, in
+// runs per XCD.
+__device__ __forceinline__ void mx_place(uint32_t row_slots, uint32_t col_groups, uint32_t& slot,
+                                         uint32_t& group) {
+  const uint32_t id = xcd_run(blockIdx.x, gridDim.x);
+  const uint32_t band = id / (8 * col_groups), in_band = id - band * 8 * col_groups;
+  const uint32_t band_rows = row_slots - band * 8 < 8 ? row_slots - band * 8 : 8;
+  slot = band * 8 + in_band % band_rows;
+  group = in_band / band_rows;
+}
+
+constexpr int mx_out_ld(int FN) { return 32 * FN + 4; }
+
+// A wave's sums (weights the first operand of its 32x32 MFMAs: a lane holds one row
+// and runs of four channels) to Y: 32 rows at a time through `out`, the wave's own
+// LDS of 32 mx_out_ld(FN) floats, so that a lane stores eight neighbouring channels.
+// (The loops are kept rolled: unrolled with all the types' stores they are tens of
+// kilobytes, and fetching those takes longer than a short product.)
+template <int FM, int FN>
+__device__ __forceinline__ void mx_store_tile(const f32x16 (&acc)[FN][FM], const MxArgs& a,
+                                              const W4Tile& tile, int row0, int64_t col0,
+                                              float* out) {
+  constexpr int kLd = mx_out_ld(FN);
+  constexpr int kPieces8 = 4 * FN, kRowsPass = 64 / kPieces8;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
+  const int p8 = lane % kPieces8, row_in = lane / kPieces8;
+  const int64_t N = a.w.rows, col = col0 + p8 * 8;
+  float bias[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    bias[j] = a.bias && col + j < N ? a.bias[tile.expert * N + col + j] : 0.0f;
+#pragma unroll 1
+  for (int f = 0; f < FM; ++f) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+      if (j == f) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<f32x4*>(out + l32 * kLd + i * 32 + q * 8 + half * 4) =
+                f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                      acc[i][j][4 * q + 3]};
+      }
+    wave_sync();
+#pragma unroll 1
+    for (int h = 0; h < 32; h += kRowsPass) {
+      const int64_t r = tile.r0 + row0 + f * 32 + h + row_in;
+      if (r < tile.r1 && col < N) {
+        const float* src = out + (h + row_in) * kLd + p8 * 8;
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
+        const bool none = w4_source_row(a.rows, r) < 0;
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float v = (none ? 0.0f : j < 4 ? lo[j % 4] : hi[j % 4]) + bias[j];
+          v = v < a.lo ? a.lo : v;
+          y[j] = v > a.hi ? a.hi : v;
+        }
+        w4_store8(a.Y, a.y_dtype, r * a.ldy + col, y, N - col < 8 ? (int)(N - col) : 8);
+      }
+    }
+    wave_sync();
+  }
+}
+
+}  // namespace
+}  // namespace qp

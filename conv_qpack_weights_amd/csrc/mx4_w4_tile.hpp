@@ -1,0 +1,432 @@
+// mx4_w4_tile.hpp -- many float rows times MXFP4 weights (the mathematics: mx4.hpp).
+//
+// A workgroup owns BM rows x BN channels, its WM x WN waves 32 FM x 32 FN each, in
+// registers.  K goes by in stages of 64: the rows' stage (of f32 rows a plane for
+// each of the three bf16 pieces of their values) is in one of D LDS buffers, 128
+// bytes of a row side by side; the weights' codes in one of kChunks buffers of 256 K
+// (128 bytes of a channel), a quarter of whose channels comes in with every stage.  A
+// wave reads its channels' 16 bytes (32 K, lane l: channel l%32, the stage's 32-block
+// l/32) and converts a word for each of the stage's four steps; the rows' operand of
+// step t is piece 4 (l/32) + t of the row.  Weights are the MFMA's first operand.
+//
+// f16 rows: a weight is an f16 exactly where its block's scale is one of 2^-23 ..
+// 2^13 (then 0.5 and 6 times it are), which weights of layers are.  Where a look over
+// the scales finds that all of a workgroup's are, its weights go in as f16 and the
+// rows as they are; else the weights as bf16 and the rows as two bf16 pieces, twice
+// the MFMAs and the cuts.  (Deciding stage by stage instead doubled the registers.)
+#pragma once
+
+#include <type_traits>
+
+#include "mx4_rows.hpp"
+#include "mx4_tile.hpp"
+
+#pragma clang fp contract(off)
+
+namespace qp {
+namespace {
+
+// The eight values of a word of codes as f16, their scale one of 2^-23 .. 2^13.
+__device__ __forceinline__ f16x8 mx_unpack_f16(uint32_t w, float scale) {
+  u32x4 o;
+  o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 0));
+  o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 1));
+  o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 2));
+  o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 3));
+  return __builtin_bit_cast(f16x8, o);
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int D>
+struct W4MxTile {
+  static constexpr int NW = WM * WN, FM = BM / (32 * WM), FN = BN / (32 * WN);
+  static constexpr int NP = sizeof(T) == 4 ? 3 : 1;  // planes
+  static constexpr int kX = BM * 128 * NP, kW = BN * 128, kScales = BN * 8;
+  static constexpr int kAhead = D == 2 ? 1 : 2;       // chunks of 256 K under way
+  static constexpr int kChunks = 2 * kAhead;
+  static constexpr int kRing = D * kX + kChunks * (kW + kScales);
+  static constexpr int kOut = NW * 32 * mx_out_ld(FN) * 4;
+  static constexpr int kLds = kRing > kOut ? kRing : kOut;
+};
+
+// kDirect (16-bit rows at multiples of 4 bytes): the rows come by direct loads, and
+// the first operands of a stage are read behind the barrier before the last MFMAs of
+// the stage before.  Else (D = 2) through registers, where f32 is cut into pieces.
+template <typename T, bool kDirect, int BM, int BN, int WM, int WN, int D>
+__global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint32_t row_slots,
+                                                                 uint32_t col_groups) {
+  using L = W4MxTile<T, BM, BN, WM, WN, D>;
+  constexpr int NW = L::NW, FM = L::FM, FN = L::FN, NP = L::NP;
+  constexpr int kA = BM / 8 / NW;  // direct loads of a stage's rows a wave
+  constexpr int kSlots = BM / (8 * NW);  // pieces of eight elements a thread and stage
+  constexpr bool kF16 = __is_same(T, f16_t);
+  static_assert(kA * 8 * NW == BM && kA % 2 == 0 && BN == 32 * NW, "shares");
+  static_assert(D == 2 || (D == 4 && kDirect), "buffers of the rows");
+  extern __shared__ __attribute__((aligned(16))) uint8_t mx_lds[];
+  lds_u8* const xbuf = (lds_u8*)mx_lds;
+  lds_u8* const wbuf = xbuf + D * L::kX;
+  lds_u8* const sbuf = wbuf + L::kChunks * L::kW;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  uint32_t slot, group;
+  mx_place(row_slots, col_groups, slot, group);
+  const int64_t n0 = (int64_t)group * BN;
+  const int64_t N = a.w.rows, K = a.w.K;
+  const W4Tile tile = w4_find_tile<BM>(a.rows, slot);
+  if (tile.expert < 0) return;
+  if (a.rows.offsets && tile.expert == a.rows.experts) {  // rows of no expert
+    for (int64_t r = tile.r0 + wave; r < tile.r1; r += NW)
+      for (int64_t n = n0 + lane; n < n0 + BN && n < N; n += 64)
+        w4_store(a.Y, a.y_dtype, r * a.ldy + n, 0.0f);
+    return;
+  }
+
+  // what a lane loads: a piece of row lane / 8 of eight; rows past the tile's end
+  // repeat its last row
+  const int lrow = lane >> 3;
+  auto piece = [&](int j) { return (lane & 7) ^ mx_turn(j * 8 + lrow); };
+  const T* xbase = static_cast<const T*>(a.X);
+  int64_t first = 0;
+  if (!a.rows.map) {
+    first = tile.r0;
+    xbase += first * a.ldx;
+  }
+  auto source = [&](int row) {
+    int64_t r = tile.r0 + row;
+    r = r < tile.r1 ? r : tile.r1 - 1;
+    const int64_t x = w4_source_row(a.rows, r);
+    return x < 0 ? INT64_C(0) : x - first;
+  };
+  uint32_t vx[kDirect ? kA : 1];
+  const T* px[kDirect ? 1 : kSlots];
+  if constexpr (kDirect) {
+#pragma unroll
+    for (int j = 0; j < kA; ++j)
+      vx[j] = (uint32_t)(source((wave * kA + j) * 8 + lrow) * a.ldx * (int64_t)sizeof(T)) +
+              piece(j) * 16;
+  } else {
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j)
+      px[j] = xbase + source((wave * kSlots + j) * 8 + lrow) * a.ldx;
+  }
+  const uint8_t* const wbase = a.w.codes + tile.expert * a.w.cstride + n0 * a.w.ldc;
+  const uint8_t* const swbase = a.w.scales + tile.expert * a.w.sstride + n0 * a.w.lds;
+  const int64_t last_n = N - 1 - n0;
+  // quarter q of the channels: rows q BN/4 + wave 8 + lane/8
+  uint32_t vw[4], vs;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t n = q * (BN / 4) + wave * 8 + lrow;
+    vw[q] = (uint32_t)((n < last_n ? n : last_n) * a.w.ldc) + ((lane & 7) ^ mx_turn(wave * 8 + lrow)) * 16;
+  }
+  static_assert(BN / 4 % 16 == 0, "turn of a quarter's rows");
+  {
+    const int64_t n = wave * 32 + (lane >> 1);
+    vs = (uint32_t)((n < last_n ? n : last_n) * a.w.lds) + (lane & 1) * 4;
+  }
+
+  const int G = (int)a.w.G, full = (int)(K / 64), words = (G + 3) / 4;
+  auto issue_x = [&](int s) {
+    const int range = s < full ? 0x7fffffff : 0;
+    lds_u8* const to = xbuf + (s % D) * L::kX;
+#pragma unroll
+    for (int j = 0; j < kA; ++j)
+      dma_to_lds<16>(xbase, range, to + (wave * kA + j) * 1024, vx[j], s * 128);
+  };
+  // codes past the row's last block and words past its last scale are read from the
+  // 256 K's first; past the last 256 K nothing is asked for
+  auto issue_w = [&](int c, int q) {
+    const int p = (lane & 7) ^ mx_turn(wave * 8 + lrow);
+    const uint32_t back = c * 8 + p < G ? 0u : p * 16u;
+    dma_to_lds<16>(wbase, c * 8 < G ? 0x7fffffff : 0,
+                   wbuf + (c % L::kChunks) * L::kW + (q * (BN / 4) + wave * 8) * 128, vw[q] - back, c * 128);
+  };
+  auto issue_s = [&](int c) {
+    const uint32_t back = c * 2 + (lane & 1) < words ? 0u : (lane & 1) * 4u;
+    dma_to_lds<4>(swbase, c * 8 < G ? 0x7fffffff : 0,
+                  sbuf + (c % L::kChunks) * L::kScales + wave * 256, vs - back, c * 8);
+  };
+  // what comes in behind stage s (of place `place` in its 256 K): the rows of stage
+  // s + D and the next quarter of the weights of the 256 K that are kAhead on
+  auto issue = [&](int s, auto place) {
+    constexpr int kNext = (decltype(place)::value + 1) % 4;
+    if constexpr (kDirect) issue_x(s + D);
+    issue_w((s + 1) / 4 + L::kAhead, kNext);
+    if constexpr (kNext == 0) issue_s((s + 1) / 4 + L::kAhead);
+  };
+
+  f32x16 acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  const int l32 = lane & 31, half = lane >> 5;
+  const uint32_t sel = half ? 0x07050301u : 0x06040200u;  // the half's scale of each 64 K
+  const int arow = wm * 32 * FM + l32, brow = wn * 32 * FN + l32;
+  struct Rows {
+    u32x4 x[FM][NP];
+  };
+  struct Weights {
+    u32x4 q[FN];
+    float s[FN];
+  };
+  auto read_x = [&](Rows& o, int s, int step) {
+    const lds_u8* const from = xbuf + (s % D) * L::kX;
+    const int at = ((4 * half + step) ^ mx_turn(l32)) * 16;
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        o.x[j][i] = *(const __attribute__((address_space(3))) u32x4*)(
+            from + (i * BM + arow + j * 32) * 128 + at);
+  };
+  auto read_w = [&](Weights& o, int s) {
+    const int c = s >> 2, p = s & 3;
+    const lds_u8* const from = wbuf + (c % L::kChunks) * L::kW;
+    const lds_u8* const st = sbuf + (c % L::kChunks) * L::kScales;
+    const int at = ((2 * p + half) ^ mx_turn(l32)) * 16;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      o.q[i] = *(const __attribute__((address_space(3))) u32x4*)(from + (brow + i * 32) * 128 + at);
+      o.s[i] = mx_scale(st[(brow + i * 32) * 8 + 2 * p + half]);
+    }
+  };
+  auto multiply = [&](const Rows& x, const Weights& w, int step, auto kind) {
+    if constexpr (decltype(kind)::value) {
+      f16x8 v[FN];
+#pragma unroll
+      for (int i = 0; i < FN; ++i) v[i] = mx_unpack_f16(w.q[i][step], w.s[i]);
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+          acc[i][j] = mx_mfma_f16(v[i], __builtin_bit_cast(f16x8, x.x[j][0]), acc[i][j]);
+    } else {
+      constexpr int kPieces = kF16 ? 2 : NP;
+      bf16x8 v[FN];
+#pragma unroll
+      for (int i = 0; i < FN; ++i) v[i] = mx_unpack(w.q[i][step], w.s[i]);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        bf16x8 xv[kPieces];
+        if constexpr (kF16)
+          MxFrag<f16_t>{x.x[j][0]}.split(xv);
+        else
+#pragma unroll
+          for (int n = 0; n < NP; ++n) xv[n] = __builtin_bit_cast(bf16x8, x.x[j][n]);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int n = 0; n < kPieces; ++n) acc[i][j] = mx_mfma_bf16(v[i], xv[n], acc[i][j]);
+      }
+    }
+  };
+  // the rows through registers: their pieces of stage s, the part before K
+  auto fetch = [&](MxFrag<T> (&f)[kSlots], int s) {
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      const int64_t k = (int64_t)s * 64 + piece(j) * 8, left = K - k;
+      f[j].load_n(px[kDirect ? 0 : j] + (left > 0 ? k : 0), left > 8 ? 8 : left < 0 ? 0 : (int)left);
+    }
+  };
+  auto fetch_full = [&](MxFrag<T> (&f)[kSlots], int s) {
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j)
+      f[j].load(px[kDirect ? 0 : j] + (int64_t)s * 64 + piece(j) * 8);
+  };
+  auto put = [&](const MxFrag<T> (&f)[kSlots], int s) {
+    lds_u8* const to = xbuf + (s % D) * L::kX;
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      lds_u8* const at = to + ((wave * kSlots + j) * 8 + lrow) * 128 + (lane & 7) * 16;
+      if constexpr (NP == 1) {
+        *(__attribute__((address_space(3))) u32x4*)at = f[j].v;
+      } else {
+        bf16x8 v[NP];
+        f[j].split(v);
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+          *(__attribute__((address_space(3))) bf16x8*)(at + i * BM * 128) = v[i];
+      }
+    }
+  };
+
+  using P0 = std::integral_constant<int, 0>;
+  using P1 = std::integral_constant<int, 1>;
+  using P2 = std::integral_constant<int, 2>;
+  using P3 = std::integral_constant<int, 3>;
+  using std::false_type;
+  using std::true_type;
+  // The next stage is there for everyone (D = 4: all but the loads of the two stages
+  // before this one are done, the weights' are four stages ahead of their use), and
+  // everyone has read all of this one.
+  auto arrive = [&](auto place) {
+    constexpr int P = decltype(place)::value;
+    wait_vmcnt<D == 2 ? 0 : 2 * (kA + 1) + (P < 2 ? 1 : 0)>();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  };
+#pragma unroll
+  for (int c = 0; c < L::kAhead; ++c) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) issue_w(c, q);
+    issue_s(c);
+  }
+  MxFrag<T> f[kSlots];
+  if constexpr (kDirect) {
+#pragma unroll
+    for (int s = 0; s < D - 1; ++s) issue_x(s);
+  } else if (full > 0) {
+    fetch_full(f, 0);
+    put(f, 0);
+  }
+  bool as_f16 = false;
+  if constexpr (kF16) {
+    bool fit = true;
+    for (int i = threadIdx.x; i < BN * words; i += NW * 64) {
+      const int n = i / words, j = i - n * words;
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(
+          swbase + (n < last_n ? n : last_n) * a.w.lds + j * 4);
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        fit = fit && (j * 4 + b >= G || ((v >> (8 * b)) & 0xffu) - 104u <= 36u);
+    }
+    as_f16 = __syncthreads_and(fit);
+  }
+  wait_vmcnt<0>();
+  __syncthreads();
+  if constexpr (kDirect) issue_x(D - 1);
+  issue_w(L::kAhead, 0);
+  issue_s(L::kAhead);
+  Rows even, odd;
+  Weights now, next;
+  auto each = [&](auto stage) {
+    int s = 0;
+    for (; s + 4 <= full; s += 4) {
+      stage(s, P0{});
+      stage(s + 1, P1{});
+      stage(s + 2, P2{});
+      stage(s + 3, P3{});
+    }
+    if (s < full) stage(s, P0{});
+    if (s + 1 < full) stage(s + 1, P1{});
+    if (s + 2 < full) stage(s + 2, P2{});
+  };
+  if constexpr (kDirect) {
+    read_x(even, 0, 0);
+    read_w(now, 0);
+    // (no branch between MFMAs: the compiler would move them past it, behind the
+    // barrier)
+    auto steps = [&](int s, auto place, auto kind) {
+      read_x(odd, s, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(even, now, 0, kind);
+      __builtin_amdgcn_sched_barrier(0);
+      read_x(even, s, 2);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(odd, now, 1, kind);
+      __builtin_amdgcn_sched_barrier(0);
+      read_x(odd, s, 3);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(even, now, 2, kind);
+      __builtin_amdgcn_sched_barrier(0);
+      arrive(place);
+      issue(s, place);
+      read_x(even, s + 1, 0);
+      read_w(next, s + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(odd, now, 3, kind);
+      __builtin_amdgcn_sched_barrier(0);
+      now = next;
+    };
+    if constexpr (kF16) {
+      if (as_f16) {
+        each([&](int s, auto place) { steps(s, place, true_type{}); });
+      } else {
+        each([&](int s, auto place) { steps(s, place, false_type{}); });
+      }
+    } else {
+      each([&](int s, auto place) { steps(s, place, false_type{}); });
+    }
+  } else {
+    auto steps = [&](int s, auto place, auto kind) {
+      fetch_full(f, s + 1 < full ? s + 1 : s);
+      read_w(now, s);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        read_x(even, s, t);
+        multiply(even, now, t, kind);
+      }
+      put(f, s + 1);
+      arrive(place);
+      issue(s, place);
+    };
+    if constexpr (kF16) {
+      if (as_f16) {
+        each([&](int s, auto place) { steps(s, place, true_type{}); });
+      } else {
+        each([&](int s, auto place) { steps(s, place, false_type{}); });
+      }
+    } else {
+      each([&](int s, auto place) { steps(s, place, false_type{}); });
+    }
+  }
+  wait_vmcnt<0>();
+  __syncthreads();
+  if ((int64_t)full * 64 < K) {
+    // the stage that K cuts: its rows through registers, zeros from K on; zero scales
+    // past the last block (what is found there could be a NaN)
+    if constexpr (kDirect) {
+      // (the pieces of a direct load's lanes, by plain loads)
+      lds_u8* const to = xbuf + (full % D) * L::kX;
+#pragma unroll 1
+      for (int j = 0; j < kA; ++j) {
+        const int row = (wave * kA + j) * 8 + lrow;
+        const int64_t k = (int64_t)full * 64 + piece(j) * 8, left = K - k;
+        const T* p = xbase + source(row) * a.ldx;
+        const Piece<T> one =
+            load_piece(p + (left > 0 ? k : 0), left > 8 ? 8 : left < 0 ? 0 : (int)left);
+        *(__attribute__((address_space(3))) u32x4*)(to + row * 128 + (lane & 7) * 16) = one.v;
+      }
+    } else {
+      fetch(f, full);
+      put(f, full);
+    }
+    __syncthreads();
+    read_w(now, full);
+    if (2 * full + half >= G) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i) now.s[i] = mx_scale(0);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      read_x(even, full, t);
+      multiply(even, now, t, false_type{});
+    }
+    __syncthreads();
+  }
+
+  mx_store_tile<FM, FN>(acc, a, tile, wm * FM * 32, n0 + wn * FN * 32,
+                        reinterpret_cast<float*>(mx_lds) + wave * 32 * mx_out_ld(FN));
+}
+
+template <typename T, bool kDirect, int BM, int BN, int WM, int WN, int D>
+qp_status mx_launch_w4_tile(const MxArgs& a, hipStream_t stream) {
+  using L = W4MxTile<T, BM, BN, WM, WN, D>;
+  const int64_t slots = w4_tile_slots(a.rows, BM), groups = ceil_div(a.w.rows, BN);
+  QP_REQUIRE(slots * groups * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
+             "qgemm_w4_mx: rows and channels for more than 2^32 threads");
+  auto kern = mx_w4_tile_kernel<T, kDirect, BM, BN, WM, WN, D>;
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds) != hipSuccess)
+    QP_FAIL(QP_EHIP, "qgemm_w4_mx: %d bytes of LDS are not to be had", L::kLds);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * groups)), dim3(L::NW * 64), L::kLds, stream, a,
+                     (uint32_t)slots, (uint32_t)groups);
+  return check_launch("qgemm_w4_mx (many rows)");
+}
+
+}  // namespace
+}  // namespace qp

@@ -508,3 +508,17 @@ def test_gradient_against_differences(qp):
         # linear: only the f32 sums' error is left, 2 sums of magnitude below 2000
         # over a step of one half
         assert torch.allclose(slope, D[:, k].double(), rtol=1e-4, atol=2000 * 96 * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("M", [4, 140, 520])
+@pytest.mark.parametrize("scales", [(104, 112), (103, 112), (133, 141), (133, 142), (100, 140)])
+def test_f16_rows_where_weights_stop_being_f16_values(qp, M, scales):
+    """Block scales of 2^-23 to 2^13 make every weight an f16, scales beyond do not:
+    as exact on both sides."""
+    import torch
+    rng = np.random.default_rng(M + scales[0])
+    for N, K in [(70, 256), (300, 416)]:
+        W, w = _matrix(qp, rng, N, K, scales=scales)
+        X, x = _rows(rng, M, K, "f16", 0.01)
+        _close(qp.qgemm_w4_mx(X, W, out_dtype=torch.float32), x @ w.T, np.abs(x) @ np.abs(w).T, K,
+               "f32", "w4")
