@@ -24,6 +24,7 @@ QP_PER_TENSOR, QP_PER_CHANNEL, QP_BLOCKWISE, QP_DYNAMIC_PER_ROW = 0, 1, 2, 3
 QP_BLOCKWISE_BF16, QP_BLOCKWISE_ASYM = 4, 5
 QP_ROUND_HALF_EVEN = 0
 QP_MX_FLOOR, QP_MX_CEIL = 0, 1
+QP_MX_A4W4, QP_MX_W4, QP_MX_W4_DX = 0, 1, 2
 
 _STATUS = {0: "QP_OK", -1: "QP_EINVAL", -2: "QP_EUNSUPPORTED", -3: "QP_EOVERFLOW",
            -4: "QP_ESIZE", -5: "QP_EALIGN", -6: "QP_EHIP"}
@@ -145,6 +146,7 @@ SIGNATURES = {
                                       _F, _P, _I32, _I64, _P]),
     "qgemm_w4_mx_dx_ws_size": (C.c_int, [_I64, _MX, _SZ]),
     "qgemm_w4_mx_dx": (C.c_int, [_P, _I32, _I64, _I64, _MX, _P, _I64, _P, C.c_size_t, _P]),
+    "qgemm_mx_kernel_name": (C.c_int, [_I32, _I64, _MX, _I32, C.c_char_p, C.c_size_t]),
     "qgemm_w4_mx_experts_dx": (C.c_int, [_P, _I32, _I64, _I64, _MX, _P, _P, _I64, _P, C.c_size_t,
                                          _P]),
 }
@@ -1209,3 +1211,12 @@ def qgemm_w4_mx_experts_dx(dY: torch.Tensor, W: MX4, offsets: torch.Tensor, out=
     _mx_call("qgemm_w4_mx_experts_dx", dY, _ptr(dY), dt, M, lddy, C.byref(W.desc), _ptr(offsets),
              _ptr(out), lddx, _ptr(ws), n)
     return out
+
+
+def qgemm_mx_kernel_name(product: str, M: int, W: MX4, dtype=torch.bfloat16) -> str:
+    """Which kernel "a4w4", "w4" or "w4_dx" takes for M rows (of `dtype`) and W."""
+    which = {"a4w4": QP_MX_A4W4, "w4": QP_MX_W4, "w4_dx": QP_MX_W4_DX}[product]
+    name = C.create_string_buffer(32)
+    _check(_lib.qgemm_mx_kernel_name(which, M, C.byref(W.desc), _FLOAT[dtype], name, len(name)),
+           "qgemm_mx_kernel_name")
+    return name.value.decode()

@@ -1,5 +1,7 @@
 // mx4.hip -- entry points of the products with MXFP4 weights: MXFP4 rows
 // (qgemm_a4w4_mx*) and float rows (qgemm_w4_mx*), dense or grouped by expert.
+#include <cstdio>
+
 #include "mx4.hpp"
 
 namespace qp {
@@ -40,7 +42,64 @@ qp_status run_float(const char* what, const MxArgs& a, int32_t dtype, hipStream_
   return run_mx_f16(a, stream);
 }
 
+// The products of float rows.  Measured with bf16 rows, cold weights, e.g. 16 x 4096
+// rows of 16 / 32 / 48 / 64 channels 8.2, 10.0, 12.0, 13.8 us, 32 x 64 tiles 14.9;
+// 16 x 11008 19.6, 18.2, 13.3, 15.5, 17.8; 64 x 11008 61, 46, 39, 40, 21.7, 64 x 64
+// tiles 21.6; 1024 x 4096 tiles of 32 / 64 / 128 / 256 rows 62, 57, 42, 87; 8192 x 11008
+// 1089, 1048, 667, 644.
+constexpr MxCost kW4Shapes[] = {
+    {kMxRows16x16, 16, 16, 8.2, 5.2, "rows16x16"},
+    {kMxRows16x32, 16, 32, 10.2, 7.0, "rows16x32"},
+    {kMxRows16x48, 16, 48, 12.2, 8.8, "rows16x48"},
+    {kMxRows16x64, 16, 64, 14.0, 12.6, "rows16x64"},
+    {kMxRows32x64, 32, 64, 18.0, 18.0, "rows32x64"},
+    {kMxTile32x64, 32, 64, 15.5, 6.5, "tile32x64"},
+    {kMxTile64x64, 64, 64, 20.5, 12.0, "tile64x64"},
+    {kMxTile128x128, 128, 128, 35.0, 30.0, "tile128x128"},
+    {kMxTile256x256, 256, 256, 84.0, 120.0, "tile256x256"},
+};
+// The same of f32 rows: 16 x 4096 13.6, 15.3, 17.2, 19.2; 64 x 11008 105, 71, 65, 55, rows
+// of 32 57, 128 x 128 tiles 125; 4096 x 4096 1440 (rows16x32) and 510.
+constexpr MxCost kW4ShapesF32[] = {
+    {kMxRows16x16, 16, 16, 13.6, 9.5, "rows16x16"},
+    {kMxRows16x32, 16, 32, 15.5, 11.0, "rows16x32"},
+    {kMxRows16x48, 16, 48, 17.5, 15.0, "rows16x48"},
+    {kMxRows16x64, 16, 64, 19.2, 17.7, "rows16x64"},
+    {kMxRows32x64, 32, 64, 27.0, 28.0, "rows32x64"},
+    {kMxTile128x128, 128, 128, 122.0, 125.0, "tile128x128"},
+};
+
 }  // namespace
+
+const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N) {
+  const double experts = (double)(parts < M ? parts : M);
+  const double each = (double)M / experts;  // rows of an expert, if all were alike
+  const MxCost* best = shapes;
+  double least = 1e300;
+  for (const MxCost* s = shapes; s < shapes + n; ++s) {
+    // row tiles of an expert: its last one is half empty on average
+    double tiles = (double)ceil_div(M, s->rows);
+    if (experts > 1.0) {
+      tiles = each / s->rows + 0.5;
+      tiles = experts * (tiles > 1.0 ? tiles : 1.0);
+    }
+    double rounds = tiles * (double)ceil_div(N, s->channels) / 256.0;
+    if (s->shape < kMxTile32x64) rounds = (double)(int64_t)(rounds + 255.0 / 256.0);
+    const double cost = s->first + s->more * (rounds > 1.0 ? rounds - 1.0 : 0.0);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return *best;
+}
+
+const MxCost& mx_w4_shape(int32_t dtype, int64_t M, int64_t parts, int64_t N) {
+  if (dtype == QP_F32)
+    return mx_choose(kW4ShapesF32, sizeof(kW4ShapesF32) / sizeof(MxCost), M, parts, N);
+  return mx_choose(kW4Shapes, sizeof(kW4Shapes) / sizeof(MxCost), M, parts, N);
+}
+
 }  // namespace qp
 
 extern "C" qp_status qgemm_a4w4_mx(const qp_mx4* a, const qp_mx4* w, const float* bias,
@@ -115,4 +174,27 @@ extern "C" qp_status qgemm_w4_mx_experts(const void* X, int32_t dtype, int64_t x
               W4Rows{offsets, (int32_t)w->matrices, M, rows, rows ? row_div : 1, x_rows},
               X, ldx, MxMat{}, bias, clamp_lo, clamp_hi, Y, y_dtype, ldy};
   return run_float(what, args, dtype, stream);
+}
+
+extern "C" qp_status qgemm_mx_kernel_name(int32_t product, int64_t M, const qp_mx4* w, int32_t dtype,
+                                          char* name, size_t bytes) {
+  using namespace qp;
+  clear_error();
+  const char* what = "qgemm_mx_kernel_name";
+  qp_status st = mx_check(what, "w", w);
+  if (st) return st;
+  QP_REQUIRE(M >= 1 && M <= kW4MaxRows && w->rows > 0, QP_EINVAL, "%s: needs a row and a channel",
+             what);
+  QP_REQUIRE(name && bytes >= 24, QP_EINVAL, "%s: needs room for 24 characters", what);
+  QP_REQUIRE(product >= QP_MX_A4W4 && product <= QP_MX_W4_DX, QP_EINVAL, "%s: no product %d", what,
+             product);
+  QP_REQUIRE(product == QP_MX_A4W4 || dtype == QP_F32 || dtype == QP_BF16 || dtype == QP_F16,
+             QP_EINVAL, "%s: rows must be QP_F32, QP_BF16 or QP_F16 (got %d)", what, dtype);
+  if (product == QP_MX_W4_DX)
+    mx_dx_kernel_name(w, dtype, M, name, bytes);
+  else
+    std::snprintf(name, bytes, "%s",
+                  product == QP_MX_A4W4 ? mx_a4w4_shape(M, w->matrices, w->rows).name
+                                        : mx_w4_shape(dtype, M, w->matrices, w->rows).name);
+  return QP_OK;
 }

@@ -124,6 +124,41 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t id, uint32_t n) {
 }
 
 // ---- host side ---------------------------------------------------------------
+// The shapes of the products' kernels, see mx_choose: rows x channels of a workgroup.
+enum MxShape {
+  kMxRows16x16,
+  kMxRows16x32,
+  kMxRows16x48,
+  kMxRows16x64,
+  kMxRows32x64,
+  kMxTile32x64,
+  kMxTile64x64,
+  kMxTile128x128,
+  kMxTile256x256
+};
+
+// What a shape takes: `first` microseconds for up to one workgroup a CU (256) and
+// `more` for every further round of them, at K = 4096 (both grow with K, which changes
+// no order); rounds are whole ones for the few-row kernels, whose workgroups all wait
+// for memory alike.
+struct MxCost {
+  MxShape shape;
+  int rows, channels;
+  double first, more;
+  const char* name;
+};
+const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N);
+const MxCost& mx_a4w4_shape(int64_t M, int64_t parts, int64_t N);
+const MxCost& mx_w4_shape(int32_t dtype, int64_t M, int64_t parts, int64_t N);
+void mx_dx_kernel_name(const qp_mx4* w, int32_t dtype, int64_t M, char* name, size_t bytes);
+
+// The tiles' direct loads take 32-bit offsets from a tile's first row (from row 0
+// through a map): rows `row_bytes` apart, x_rows of them.
+inline bool mx_tile_reaches(const W4Rows& rows, int64_t row_bytes) {
+  constexpr int64_t kMost = (INT64_C(1) << 31) - 1;
+  return row_bytes <= kMost / 256 && (!rows.map || rows.x_rows <= kMost / row_bytes);
+}
+
 MxMat mx_view(const qp_mx4* m);
 qp_status mx_check(const char* what, const char* name, const qp_mx4* m);
 qp_status run_mx_a4w4(const MxArgs& a, hipStream_t stream);

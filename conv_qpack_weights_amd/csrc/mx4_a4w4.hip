@@ -30,8 +30,6 @@ __device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, uint32_t sa, u32x4 b, uint3
 // 16-byte piece c of row r lies at place c ^ mx_turn(r) of the row's eight, so that the
 // rows an operand takes piece c of meet every bank alike.  The weights are the
 // MFMA's first operand: a lane ends with one row and runs of four channels.
-enum A4Shape { kA4Rows, kA4Tile64, kA4Tile128, kA4Tile256 };
-
 template <int BM, int BN, int WM, int WN, int D>
 struct A4Tile {
   static constexpr int NW = WM * WN, FM = BM / (32 * WM), FN = BN / (32 * WN);
@@ -305,63 +303,29 @@ qp_status launch_tile(const MxArgs& a, hipStream_t stream) {
   return check_launch("qgemm_a4w4_mx (many rows)");
 }
 
-// Which kernel: the one whose time the following estimate puts lowest.  A shape
-// takes `first` microseconds for up to one workgroup a CU (256) and `more` for every
-// further round of them, at K = 4096 (both grow with K, which changes no order).
-// Measured, cold weights: e.g. 1 x 4096 rows 5.2, 64 x 64 tiles 8.1 us; 32 x 4096
-// 10.1 and 8.4; 256 x 4096 59, 9.1, 128 x 128 tiles 16; 512 x 11008 tiles of 64 / 128 /
-// 256 31.9, 25.2, 36.9; 4096 x 4096 82, 53, 45.
-struct A4Cost {
-  A4Shape shape;
-  int rows, channels;
-  double first, more;
+// Which kernel (MxCost, mx_choose).  Measured, cold weights: e.g. 1 x 4096 rows 5.2,
+// 64 x 64 tiles 8.1 us; 32 x 4096 10.1 and 8.4; 256 x 4096 59, 9.1, 128 x 128 tiles 16;
+// 512 x 11008 tiles of 64 / 128 / 256 31.9, 25.2, 36.9; 4096 x 4096 82, 53, 45.
+constexpr MxCost kA4Shapes[] = {
+    {kMxRows16x16, 16, 16, 5.2, 3.0, "rows16x16"},
+    {kMxTile64x64, 64, 64, 8.1, 4.4, "tile64x64"},
+    {kMxTile128x128, 128, 128, 16.0, 11.5, "tile128x128"},
+    {kMxTile256x256, 256, 256, 35.0, 37.0, "tile256x256"},
 };
-constexpr A4Cost kA4Shapes[] = {
-    {kA4Rows, 16, 16, 5.2, 3.0},
-    {kA4Tile64, 64, 64, 8.1, 4.4},
-    {kA4Tile128, 128, 128, 16.0, 11.5},
-    {kA4Tile256, 256, 256, 35.0, 37.0},
-};
-
-A4Shape a4_choose(int64_t M, int64_t parts, int64_t N) {
-  const double experts = (double)(parts < M ? parts : M);
-  const double each = (double)M / experts;  // rows of an expert, if all were alike
-  A4Shape best = kA4Rows;
-  double least = 1e300;
-  for (const A4Cost& s : kA4Shapes) {
-    // row tiles of an expert: its last one is half empty on average
-    double tiles = (double)ceil_div(M, s.rows);
-    if (experts > 1.0) {
-      tiles = each / s.rows + 0.5;
-      tiles = experts * (tiles > 1.0 ? tiles : 1.0);
-    }
-    const double rounds = tiles * (double)ceil_div(N, s.channels) / 256.0;
-    const double cost = s.first + s.more * (rounds > 1.0 ? rounds - 1.0 : 0.0);
-    if (cost < least) {
-      least = cost;
-      best = s.shape;
-    }
-  }
-  return best;
-}
-
-// The tiles' direct loads take 32-bit offsets from a tile's first row (from row 0
-// through a map).
-bool tiles_reach(const MxArgs& a) {
-  const int64_t most = (INT64_C(1) << 31) - 1;
-  if (a.w.ldc * 256 > most || a.a.ldc * 256 > most) return false;
-  return !a.rows.map || (a.a.rows * a.a.ldc <= most && a.a.rows * a.a.lds <= most);
-}
 
 }  // namespace
 
+const MxCost& mx_a4w4_shape(int64_t M, int64_t parts, int64_t N) {
+  return mx_choose(kA4Shapes, sizeof(kA4Shapes) / sizeof(MxCost), M, parts, N);
+}
+
 qp_status run_mx_a4w4(const MxArgs& a, hipStream_t stream) {
-  if (tiles_reach(a)) {
-    switch (a4_choose(a.rows.M, a.rows.offsets ? a.rows.experts : 1, a.w.rows)) {
-      case kA4Tile256: return launch_tile<256, 256, 2, 4, 2>(a, stream);
-      case kA4Tile128: return launch_tile<128, 128, 2, 2, 2>(a, stream);
-      case kA4Tile64: return launch_tile<64, 64, 2, 2, 4>(a, stream);
-      case kA4Rows: break;
+  if (mx_tile_reaches(a.rows, a.a.ldc) && a.w.ldc < kMxMaxLd) {
+    switch (mx_a4w4_shape(a.rows.M, a.rows.offsets ? a.rows.experts : 1, a.w.rows).shape) {
+      case kMxTile256x256: return launch_tile<256, 256, 2, 4, 2>(a, stream);
+      case kMxTile128x128: return launch_tile<128, 128, 2, 2, 2>(a, stream);
+      case kMxTile64x64: return launch_tile<64, 64, 2, 2, 4>(a, stream);
+      default: break;
     }
   }
   return mx_launch_rows<mx4_t, 1, 1, 8, 1>(a, stream);

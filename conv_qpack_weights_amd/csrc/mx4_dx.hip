@@ -6,7 +6,7 @@
 // channels' scales, exactly, and pairs the channels' halves up (32 conversions
 // and 32 v_perm for eight operands, no LDS): operand j then holds column 8 i + j
 // in lane i of 16, and a lane ends with eight neighbouring columns of a row.
-#include <cstdlib>
+#include <cstdio>
 #include <type_traits>
 
 #include "mx4.hpp"
@@ -530,17 +530,45 @@ qp_status launch_dx_tile(const char* what, const MxDxArgs& a, hipStream_t stream
   return check_launch(what);
 }
 
-// In how many splits the channels go: enough workgroups for the card, no split
-// without a step of 32 channels for each of its waves.
+// Which kernel, and for few rows in how many splits the channels go: enough workgroups
+// for the card, no split without a step of 32 channels for each of its waves.
+//
+// Measured, bf16, 4096 x 4096 weights: 16 rows 11.9 us by the few-row kernel, 128 21 (128 x
+// 128 tiles 63), 256 32 (62), 1024 118 (76; 256 x 256 tiles 128), 4096 512 (199, 148); of 11008
+// columns 512 rows 166 (98, 131).  f32 rows: 1024 179 (160), 4096 737 (614).
 constexpr int kDxWaves = 8;
-uint32_t dx_splits(int64_t M, const qp_mx4* w, int64_t experts) {
-  const int64_t parts = experts < M ? experts : M;
-  const int64_t groups = (M / 16 + parts) * ceil_div(w->K, 128);
+struct DxPlan {
+  int tile;         // rows of a tile, 0: few rows
+  uint32_t splits;
+};
+DxPlan dx_plan(int32_t dtype, int64_t M, const qp_mx4* w) {
+  const int64_t parts = w->matrices < M ? w->matrices : M;
+  // row tiles of an expert: its last one is half empty on average
+  auto groups = [&](int rows, int cols) {
+    const double each = (double)M / (double)parts / rows;
+    const double tiles = parts > 1 ? (each > 0.5 ? each + 0.5 : 1.0) * (double)parts
+                                   : (double)ceil_div(M, rows);
+    return tiles * (double)ceil_div(w->K, cols) / 256.0;
+  };
+  const double few = groups(16, 128), t128 = groups(128, 128), t256 = groups(256, 256);
+  auto more = [](double g) { return g > 1.0 ? g - 1.0 : 0.0; };
+  // microseconds at 4096 channels (all grow with them)
+  const bool f32 = dtype == QP_F32;
+  const double c0 = 12.0 + (f32 ? 21.0 : 14.0) * few;
+  const double c128 = f32 ? 145.0 + 150.0 * more(t128) : 62.0 + 42.0 * more(t128);
+  const double c256 = f32 ? 1e300 : 126.0 + 85.0 * more(t256);
+  DxPlan p{0, 1};
+  if (c128 < c0 || c256 < c0) {
+    p.tile = c256 < c128 ? 256 : 128;
+    return p;
+  }
+  const int64_t wgs = (M / 16 + parts) * ceil_div(w->K, 128);
   const int64_t most = ceil_div(ceil_div(w->rows, 32), kDxWaves);
-  int64_t s = 512 / groups;
+  int64_t s = 512 / wgs;
   s = s > most ? most : s;
   s = s > 16 ? 16 : s;
-  return s < 1 ? 1u : (uint32_t)s;
+  p.splits = s < 1 ? 1u : (uint32_t)s;
+  return p;
 }
 
 template <typename T>
@@ -550,10 +578,29 @@ void launch_dx(const MxDxArgs& a, uint32_t slots, uint32_t splits, hipStream_t s
                      dim3(kDxWaves * 64), 0, stream, a, slots, splits);
 }
 
-qp_status dx_ws(int64_t M, const qp_mx4* w, int64_t experts, uint32_t* splits, size_t* bytes) {
-  *splits = M > 0 ? dx_splits(M, w, experts) : 1;
-  *bytes = *splits > 1 ? (size_t)(4 * (int64_t)*splits * M * w->K) : 0;
-  return QP_OK;
+template <typename T>
+qp_status run_dx_tile(const char* what, const MxDxArgs& a, int tile, hipStream_t stream) {
+  if constexpr (sizeof(T) == 4) {
+    return launch_dx_tile<T, false, 128, 128, 2, 2>(what, a, stream);
+  } else {
+    // rows that direct loads cannot take go through registers
+    if ((uintptr_t)a.dY % 4 || a.lddy % 2 || !mx_tile_reaches(a.rows, a.lddy * 2))
+      return launch_dx_tile<T, false, 128, 128, 2, 2>(what, a, stream);
+    if (tile == 256) return launch_dx_tile<T, true, 256, 256, 2, 4>(what, a, stream);
+    return launch_dx_tile<T, true, 128, 128, 2, 2>(what, a, stream);
+  }
+}
+
+// (the workspace does not depend on the row type: with f32 rows the few-row kernel
+// reaches further)
+size_t dx_ws(int64_t M, const qp_mx4* w) {
+  size_t most = 0;
+  for (int32_t dtype : {(int32_t)QP_F32, (int32_t)QP_BF16}) {
+    const DxPlan p = M > 0 ? dx_plan(dtype, M, w) : DxPlan{0, 1};
+    const size_t n = p.splits > 1 ? (size_t)(4 * (int64_t)p.splits * M * w->K) : 0;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 qp_status run_dx(const char* what, const void* dY, int32_t dtype, int64_t M, int64_t lddy,
@@ -568,26 +615,19 @@ qp_status run_dx(const char* what, const void* dY, int32_t dtype, int64_t M, int
   if (M == 0) return QP_OK;
   if ((st = w4_check_float(what, "dY", dY, dtype, lddy, w->rows))) return st;
   if ((st = w4_check_float(what, "dX", dX, dtype, lddx, w->K))) return st;
-  uint32_t splits;
-  size_t need;
-  dx_ws(M, w, w->matrices, &splits, &need);
+  const DxPlan plan = dx_plan(dtype, M, w);
+  const uint32_t splits = plan.splits;
+  const size_t need = dx_ws(M, w);
   QP_REQUIRE(ws_bytes >= need, QP_ESIZE, "%s: needs a workspace of %zu bytes, has %zu", what, need,
              ws_bytes);
   QP_REQUIRE(!need || (ws && (uintptr_t)ws % 256 == 0), QP_EALIGN,
              "%s: the workspace must be 256-byte aligned", what);
   MxDxArgs a{mx_view(w), W4Rows{offsets, (int32_t)w->matrices, M, nullptr, 1, M}, dY, lddy, dX,
              dtype, lddx, static_cast<float*>(ws)};
-  {
-    const char* e = getenv("MXD");
-    const int t = e ? atoi(e) : 0;
-    const bool al = (uintptr_t)dY % 4 == 0 && lddy % 2 == 0;
-    if (t == 1 && al && dtype == QP_BF16) return launch_dx_tile<bf16_t, true, 256, 256, 2, 4>(what, a, stream);
-    if (t == 1 && al && dtype == QP_F16) return launch_dx_tile<f16_t, true, 256, 256, 2, 4>(what, a, stream);
-    if (t == 2 && al && dtype == QP_BF16) return launch_dx_tile<bf16_t, true, 128, 128, 2, 2>(what, a, stream);
-    if (t == 2 && al && dtype == QP_F16) return launch_dx_tile<f16_t, true, 128, 128, 2, 2>(what, a, stream);
-    if (t && dtype == QP_BF16) return launch_dx_tile<bf16_t, false, 128, 128, 2, 2>(what, a, stream);
-    if (t && dtype == QP_F16) return launch_dx_tile<f16_t, false, 128, 128, 2, 2>(what, a, stream);
-    if (t) return launch_dx_tile<float, false, 128, 128, 2, 2>(what, a, stream);
+  if (plan.tile) {
+    if (dtype == QP_F32) return run_dx_tile<float>(what, a, plan.tile, stream);
+    if (dtype == QP_BF16) return run_dx_tile<bf16_t>(what, a, plan.tile, stream);
+    return run_dx_tile<f16_t>(what, a, plan.tile, stream);
   }
   const int64_t slots = w4_tile_slots(a.rows, 16), cols = ceil_div(w->K, 128);
   QP_REQUIRE(slots * cols * splits * kDxWaves * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
@@ -609,6 +649,15 @@ qp_status run_dx(const char* what, const void* dY, int32_t dtype, int64_t M, int
 }
 
 }  // namespace
+
+void mx_dx_kernel_name(const qp_mx4* w, int32_t dtype, int64_t M, char* name, size_t bytes) {
+  const DxPlan p = dx_plan(dtype, M, w);
+  if (p.tile)
+    std::snprintf(name, bytes, "tile%dx%d", p.tile, p.tile);
+  else
+    std::snprintf(name, bytes, "rows16x128/%u", p.splits);
+}
+
 }  // namespace qp
 
 extern "C" qp_status qgemm_w4_mx_dx_ws_size(int64_t M, const qp_mx4* w, size_t* bytes) {
@@ -620,8 +669,8 @@ extern "C" qp_status qgemm_w4_mx_dx_ws_size(int64_t M, const qp_mx4* w, size_t* 
   QP_REQUIRE(M <= kW4MaxRows, QP_EUNSUPPORTED, "%s: more than 2^30 rows", what);
   qp_status st = mx_check(what, "w", w);
   if (st) return st;
-  uint32_t splits;
-  return dx_ws(M, w, w->matrices, &splits, bytes);
+  *bytes = dx_ws(M, w);
+  return QP_OK;
 }
 
 extern "C" qp_status qgemm_w4_mx_dx(const void* dY, int32_t dtype, int64_t M, int64_t lddy,

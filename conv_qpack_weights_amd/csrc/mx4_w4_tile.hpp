@@ -285,15 +285,24 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
   }
   bool as_f16 = false;
   if constexpr (kF16) {
-    bool fit = true;
-    for (int i = threadIdx.x; i < BN * words; i += NW * 64) {
-      const int n = i / words, j = i - n * words;
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(
-          swbase + (n < last_n ? n : last_n) * a.w.lds + j * 4);
+    // two threads a channel, four words each at a time
+    static_assert(BN * 2 == NW * 64, "shares");
+    const int64_t n = threadIdx.x / 2;
+    const uint8_t* const row = swbase + (n < last_n ? n : last_n) * a.w.lds;
+    uint32_t out = 0;
+#pragma unroll 4
+    for (int j = threadIdx.x % 2 * 4; j < words; j += 8) {
+      uint32_t v[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        fit = fit && (j * 4 + b >= G || ((v >> (8 * b)) & 0xffu) - 104u <= 36u);
+      for (int i = 0; i < 4; ++i)
+        v[i] = *reinterpret_cast<const uint32_t*>(row + (j + i < words ? j + i : j) * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if ((j + i) * 4 + b < G) out |= ((v[i] >> (8 * b)) & 0xffu) - 104u > 36u;
     }
+    const bool fit = out == 0;
     as_f16 = __syncthreads_and(fit);
   }
   wait_vmcnt<0>();
@@ -426,6 +435,34 @@ qp_status mx_launch_w4_tile(const MxArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(kern, dim3((unsigned)(slots * groups)), dim3(L::NW * 64), L::kLds, stream, a,
                      (uint32_t)slots, (uint32_t)groups);
   return check_launch("qgemm_w4_mx (many rows)");
+}
+
+template <typename T>
+qp_status mx_run_rows(const MxArgs& a, MxShape shape, hipStream_t stream) {
+  switch (shape) {
+    case kMxRows16x16: return mx_launch_rows<T, 1, 1, 8, 1>(a, stream);
+    case kMxRows16x32: return mx_launch_rows<T, 1, 2, 8, 1>(a, stream);
+    case kMxRows16x48: return mx_launch_rows<T, 1, 3, 8, 1>(a, stream);
+    case kMxRows16x64: return mx_launch_rows<T, 1, 4, 8, 1>(a, stream);
+    default: return mx_launch_rows<T, 2, 4, 8, 1>(a, stream);
+  }
+}
+
+template <typename T>
+qp_status mx_run_16bit(const MxArgs& a, hipStream_t stream) {
+  const MxShape shape = mx_w4_shape(__is_same(T, f16_t) ? QP_F16 : QP_BF16, a.rows.M,
+                                    a.rows.offsets ? a.rows.experts : 1, a.w.rows)
+                            .shape;
+  if (shape < kMxTile32x64 || a.w.ldc >= kMxMaxLd) return mx_run_rows<T>(a, shape, stream);
+  // rows that direct loads cannot take go through registers
+  if ((uintptr_t)a.X % 4 || a.ldx % 2 || !mx_tile_reaches(a.rows, a.ldx * 2))
+    return mx_launch_w4_tile<T, false, 128, 128, 2, 2, 2>(a, stream);
+  switch (shape) {
+    case kMxTile32x64: return mx_launch_w4_tile<T, true, 32, 64, 1, 2, 4>(a, stream);
+    case kMxTile64x64: return mx_launch_w4_tile<T, true, 64, 64, 1, 2, 4>(a, stream);
+    case kMxTile128x128: return mx_launch_w4_tile<T, true, 128, 128, 2, 2, 2>(a, stream);
+    default: return mx_launch_w4_tile<T, true, 256, 256, 2, 4, 2>(a, stream);
+  }
 }
 
 }  // namespace
