@@ -181,10 +181,12 @@ __global__ __launch_bounds__(256) void mx_dx_sum_kernel(const float* __restrict_
 // A workgroup owns BM rows x BC columns, its WM x WN waves 32 FM x 64 each, in
 // registers.  The channels go by in stages of 64: dY's stage (of f32 rows a plane for
 // each of the three bf16 pieces) comes into one of two LDS buffers by direct loads or
-// through registers, as the rows of mx4_w4_tile.hpp; the weights' through registers:
-// a thread takes four columns (two bytes) of eight channels, a stage ahead, converts
-// and pairs them up, and writes for each of its columns the eight channels' values,
-// 16 bytes, to the other buffer, so that every weight is converted once in a
+// through registers, as the rows of mx4_w4_tile.hpp; the weights' codes and scales into
+// one of two small buffers, two stages ahead (loaded by their users instead, two
+// bytes at a time, they held a 256 x 256 tile up for a quarter of its time).  A stage
+// ahead a thread takes four columns (two bytes) of eight channels from there, converts
+// and pairs them up, and writes for each of its columns the eight channels' values, 16
+// bytes, to the other of two buffers, so that every weight is converted once in a
 // workgroup.  In that buffer column 4u + j of a wave's 64 is row 16 j + u: 16 threads
 // then write 16 rows, whose places meet every bank alike (mx_turn).
 // f16 rows: as there, with f16 weights where a look over the scales allows it.
@@ -193,7 +195,9 @@ struct MxDxTile {
   static constexpr int NW = WM * WN, FM = BM / (32 * WM);
   static constexpr int NP = sizeof(T) == 4 ? 3 : 1;
   static constexpr int kX = BM * 128 * NP, kW = BC * 128;
-  static constexpr int kRing = 2 * (kX + kW);
+  static constexpr int kRaw = 32 * BC, kScales = 2 * BC;   // 64 channels' codes and scales
+  static constexpr int kIdle = 256;  // where a wave without a share of the scales loads to
+  static constexpr int kRing = 2 * (kX + kW + kRaw + kScales) + kIdle;
   static constexpr int kOutLd = 64 + 4;
   static constexpr int kOut = NW * 32 * kOutLd * 4;
   static constexpr int kLds = kRing > kOut ? kRing : kOut;
@@ -210,6 +214,9 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
   extern __shared__ __attribute__((aligned(16))) uint8_t mx_lds[];
   lds_u8* const xbuf = (lds_u8*)mx_lds;
   lds_u8* const wbuf = xbuf + 2 * L::kX;
+  lds_u8* const raws = wbuf + 2 * L::kW;
+  lds_u8* const scs = raws + 2 * L::kRaw;
+  lds_u8* const idle = scs + 2 * L::kScales;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -273,31 +280,59 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
       f[j].load(px[kDirect ? 0 : j] + (int64_t)s * 64 + piece(j) * 8);
   };
 
-  // the weights: columns 4u .. 4u + 3 of channels 8g .. 8g + 7 of a stage
+  // the weights: a lane loads a piece of 32 columns of a channel, and a word of its
+  // scales; columns past the last block repeat the group's first (they are not stored)
+  const uint8_t* const codes = a.w.codes + tile.expert * a.w.cstride + k0 / 2;
+  const uint8_t* const scales = a.w.scales + tile.expert * a.w.sstride + k0 / 32;
+  constexpr int kPieces = BC / 32, kWords = BC / 128;  // of a channel
+  const int blocks = a.w.G - k0 / 32 < kPieces ? (int)(a.w.G - k0 / 32) : kPieces;
+  static_assert(64 * kPieces == 64 * NW, "one load of codes a wave");
+  uint32_t vq, vs;
+  {
+    const int row = threadIdx.x / kPieces, c = threadIdx.x % kPieces;
+    vq = (uint32_t)(row * a.w.ldc) + (c < blocks ? c : 0) * 16;
+    const int srow = threadIdx.x / kWords & 63, w = threadIdx.x % kWords;
+    vs = (uint32_t)(srow * a.w.lds) + (w * 4 < blocks ? w : 0) * 4;
+  }
+  auto issue_w = [&](int s) {
+    const int range = s < full ? 0x7fffffff : 0;
+    const int64_t row = s < full ? (int64_t)s * 64 : 0;
+    dma_to_lds<16>(codes + row * a.w.ldc, range, raws + (s & 1) * L::kRaw + wave * 1024, vq, 0);
+    const bool mine = wave < kWords;
+    dma_to_lds<4>(scales + row * a.w.lds, mine ? range : 0,
+                  mine ? scs + (s & 1) * L::kScales + wave * 256 : idle, vs, 0);
+  };
+  // a thread's share: columns 4u .. 4u + 3 of channels 8g .. 8g + 7 of a stage
   const int u = threadIdx.x % (BC / 4), g = threadIdx.x / (BC / 4);
-  const bool col_in = k0 / 32 + u / 8 < a.w.G;  // (else the row's first: not stored)
-  const uint8_t* const codes =
-      a.w.codes + tile.expert * a.w.cstride + (col_in ? k0 / 2 + 2 * u : 0);
-  const uint8_t* const scales =
-      a.w.scales + tile.expert * a.w.sstride + (col_in ? k0 / 32 + u / 8 : 0);
   struct Raw {
     uint32_t q[8], s[8];
   };
-  auto load_w = [&](Raw& w, int s) {
+  auto read_w = [&](Raw& w, int s) {
+    const lds_u8* const q = raws + (s & 1) * L::kRaw + g * 8 * (BC / 2) + 2 * u;
+    const lds_u8* const sc = scs + (s & 1) * L::kScales + g * 8 * kPieces + u / 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      int64_t n = (int64_t)s * 64 + g * 8 + i;
-      n = n < N ? n : N - 1;
-      w.q[i] = *reinterpret_cast<const uint16_t*>(codes + n * a.w.ldc);
-      w.s[i] = scales[n * a.w.lds];
+      w.q[i] = *(const __attribute__((address_space(3))) uint16_t*)(q + i * (BC / 2));
+      w.s[i] = sc[i * kPieces];
+    }
+  };
+  // the stage that N cuts: channels past the last have zero scales (what is found
+  // there could be a NaN)
+  auto load_w_cut = [&](Raw& w) {
+    const bool in = u / 8 < blocks;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t n = (int64_t)full * 64 + g * 8 + i, at = n < N ? n : N - 1;
+      w.q[i] = *reinterpret_cast<const uint16_t*>(codes + at * a.w.ldc + (in ? 2 * u : 0));
+      const uint32_t v = scales[at * a.w.lds + (in ? u / 8 : 0)];
+      w.s[i] = n < N ? v : 0u;
     }
   };
   auto convert = [&](const Raw& w, int s, auto kind) {
     uint32_t c[8][2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // (a channel past the last: its scale could be a NaN)
-      const float by = mx_scale((int64_t)s * 64 + g * 8 + i < N ? w.s[i] : 0u);
+      const float by = mx_scale(w.s[i]);
       if constexpr (decltype(kind)::value) {
         c[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 0));
         c[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 1));
@@ -383,65 +418,72 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
   auto run = [&](auto kind) {
     Raw raw;
     MxFrag<T> f[kA];
-    load_w(raw, 0);
-    if constexpr (kDirect) {
-      issue_x(0);
-    } else if (full > 0) {
-      fetch_full(f, 0);
-#pragma unroll
-      for (int j = 0; j < kA; ++j) put(f[j], 0, j);
-    }
-    convert(raw, 0, kind);
-    arrive();
-    load_w(raw, 1);
-    if constexpr (kDirect) issue_x(1);
     Operands even, odd;
-    if constexpr (kDirect) {
-      read(even, 0, 0);
-      // (no branch between MFMAs, as in the products)
-      for (int s = 0; s < full; ++s) {
-        read(odd, s, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(even, kind);
-        __builtin_amdgcn_sched_barrier(0);
-        read(even, s, 2);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(odd, kind);
-        __builtin_amdgcn_sched_barrier(0);
-        read(odd, s, 3);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(even, kind);
-        __builtin_amdgcn_sched_barrier(0);
-        convert(raw, s + 1, kind);
-        __builtin_amdgcn_sched_barrier(0);
-        arrive();
-        load_w(raw, s + 2);
-        issue_x(s + 2);
-        read(even, s + 1, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(odd, kind);
-        __builtin_amdgcn_sched_barrier(0);
+    if (full > 0) {
+      issue_w(0);
+      issue_w(1);
+      if constexpr (kDirect) {
+        issue_x(0);
+      } else {
+        fetch_full(f, 0);
+#pragma unroll
+        for (int j = 0; j < kA; ++j) put(f[j], 0, j);
       }
-    } else {
-      for (int s = 0; s < full; ++s) {
-        fetch_full(f, s + 1 < full ? s + 1 : s);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          read(even, s, t);
+      arrive();
+      read_w(raw, 0);
+      convert(raw, 0, kind);
+      arrive();
+      issue_w(2);
+      if constexpr (kDirect) {
+        issue_x(1);
+        read(even, 0, 0);
+        // (no branch between MFMAs, as in the products)
+        for (int s = 0; s < full; ++s) {
+          read(odd, s, 1);
+          __builtin_amdgcn_sched_barrier(0);
           multiply(even, kind);
+          __builtin_amdgcn_sched_barrier(0);
+          read(even, s, 2);
+          read_w(raw, s + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(odd, kind);
+          __builtin_amdgcn_sched_barrier(0);
+          read(odd, s, 3);
+          __builtin_amdgcn_sched_barrier(0);
+          convert(raw, s + 1, kind);
+          multiply(even, kind);
+          __builtin_amdgcn_sched_barrier(0);
+          arrive();
+          issue_w(s + 3);
+          issue_x(s + 2);
+          read(even, s + 1, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(odd, kind);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        convert(raw, s + 1, kind);
+      } else {
+        for (int s = 0; s < full; ++s) {
+          fetch_full(f, s + 1 < full ? s + 1 : s);
+          read_w(raw, s + 1);
+          convert(raw, s + 1, kind);
 #pragma unroll
-        for (int j = 0; j < kA; ++j) put(f[j], s + 1, j);
-        arrive();
-        load_w(raw, s + 2);
+          for (int t = 0; t < 4; ++t) {
+            read(even, s, t);
+            multiply(even, kind);
+          }
+#pragma unroll
+          for (int j = 0; j < kA; ++j) put(f[j], s + 1, j);
+          arrive();
+          issue_w(s + 3);
+        }
       }
     }
     wait_vmcnt<0>();
     __syncthreads();
     if ((int64_t)full * 64 < N) {
-      // the stage that N cuts: its rows through registers, zeros from N on (its weights
-      // are there)
+      // the stage that N cuts: its rows through registers, zeros from N on
+      load_w_cut(raw);
+      convert(raw, full, kind);
 #pragma unroll 1
       for (int j = 0; j < kA; ++j) {
         const int64_t n = (int64_t)full * 64 + piece(j) * 8, left = N - n;
@@ -461,14 +503,12 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
   };
   if constexpr (kF16) {
     bool fit = true;
-    const int blocks = a.w.G - k0 / 32 < BC / 32 ? (int)(a.w.G - k0 / 32) : BC / 32;
-    const uint8_t* const sc = a.w.scales + tile.expert * a.w.sstride + k0 / 32;
 #pragma unroll 4
     for (int64_t n = threadIdx.x; n < N; n += NW * 64) {
 #pragma unroll
       for (int w = 0; w < BC / 128; ++w) {  // (rows are whole words)
         const uint32_t v = w * 4 < blocks
-                               ? *reinterpret_cast<const uint32_t*>(sc + n * a.w.lds + w * 4) : 0u;
+                               ? *reinterpret_cast<const uint32_t*>(scales + n * a.w.lds + w * 4) : 0u;
 #pragma unroll
         for (int b = 0; b < 4; ++b)
           fit = fit && (w * 4 + b >= blocks || ((v >> (8 * b)) & 0xffu) - 104u <= 36u);

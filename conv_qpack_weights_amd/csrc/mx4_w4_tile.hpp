@@ -42,8 +42,10 @@ struct W4MxTile {
   static constexpr int NP = sizeof(T) == 4 ? 3 : 1;  // planes
   static constexpr int kX = BM * 128 * NP, kW = BN * 128, kScales = BN * 8;
   static constexpr int kAhead = D == 2 ? 1 : 2;       // chunks of 256 K under way
-  static constexpr int kChunks = 2 * kAhead;
-  static constexpr int kRing = D * kX + kChunks * (kW + kScales);
+  static constexpr int kChunks = kAhead + 1;
+  static constexpr int kA = (BM / 8 + NW - 1) / NW;   // direct loads of a stage's rows a wave
+  static constexpr int kIdle = kA * 8 * NW > BM ? 1024 : 0;  // where a wave without a share loads to
+  static constexpr int kRing = D * kX + kChunks * (kW + kScales) + kIdle;
   static constexpr int kOut = NW * 32 * mx_out_ld(FN) * 4;
   static constexpr int kLds = kRing > kOut ? kRing : kOut;
 };
@@ -56,15 +58,16 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
                                                                  uint32_t col_groups) {
   using L = W4MxTile<T, BM, BN, WM, WN, D>;
   constexpr int NW = L::NW, FM = L::FM, FN = L::FN, NP = L::NP;
-  constexpr int kA = BM / 8 / NW;  // direct loads of a stage's rows a wave
-  constexpr int kSlots = BM / (8 * NW);  // pieces of eight elements a thread and stage
+  constexpr int kA = L::kA;
+  constexpr int kSlots = kDirect ? 1 : kA;  // pieces of eight elements a thread and stage
   constexpr bool kF16 = __is_same(T, f16_t);
-  static_assert(kA * 8 * NW == BM && kA % 2 == 0 && BN == 32 * NW, "shares");
+  static_assert(BN == 32 * NW && (kDirect || kA * 8 * NW == BM), "shares");
   static_assert(D == 2 || (D == 4 && kDirect), "buffers of the rows");
   extern __shared__ __attribute__((aligned(16))) uint8_t mx_lds[];
   lds_u8* const xbuf = (lds_u8*)mx_lds;
   lds_u8* const wbuf = xbuf + D * L::kX;
   lds_u8* const sbuf = wbuf + L::kChunks * L::kW;
+  lds_u8* const idle = sbuf + L::kChunks * L::kScales;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -85,7 +88,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
   // what a lane loads: a piece of row lane / 8 of eight; rows past the tile's end
   // repeat its last row
   const int lrow = lane >> 3;
-  auto piece = [&](int j) { return (lane & 7) ^ mx_turn(j * 8 + lrow); };
+  auto piece = [&](int j) { return (lane & 7) ^ mx_turn((wave * kA + j) * 8 + lrow); };
   const T* xbase = static_cast<const T*>(a.X);
   int64_t first = 0;
   if (!a.rows.map) {
@@ -128,11 +131,14 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
 
   const int G = (int)a.w.G, full = (int)(K / 64), words = (G + 3) / 4;
   auto issue_x = [&](int s) {
-    const int range = s < full ? 0x7fffffff : 0;
     lds_u8* const to = xbuf + (s % D) * L::kX;
 #pragma unroll
-    for (int j = 0; j < kA; ++j)
-      dma_to_lds<16>(xbase, range, to + (wave * kA + j) * 1024, vx[j], s * 128);
+    for (int j = 0; j < kA; ++j) {
+      const int i = wave * kA + j;
+      const bool mine = L::kIdle == 0 || i < BM / 8;
+      dma_to_lds<16>(xbase, s < full && mine ? 0x7fffffff : 0, mine ? to + i * 1024 : idle, vx[j],
+                     s * 128);
+    }
   };
   // codes past the row's last block and words past its last scale are read from the
   // 256 K's first; past the last 256 K nothing is asked for
@@ -394,6 +400,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
 #pragma unroll 1
       for (int j = 0; j < kA; ++j) {
         const int row = (wave * kA + j) * 8 + lrow;
+        if (row >= BM) break;
         const int64_t k = (int64_t)full * 64 + piece(j) * 8, left = K - k;
         const T* p = xbase + source(row) * a.ldx;
         const Piece<T> one =
