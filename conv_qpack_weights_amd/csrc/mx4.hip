@@ -42,19 +42,18 @@ qp_status run_float(const char* what, const MxArgs& a, int32_t dtype, hipStream_
   return run_mx_f16(a, stream);
 }
 
-// The products of float rows.  Measured with bf16 rows, cold weights, e.g. 16 x 4096
-// rows of 16 / 32 / 48 / 64 channels 8.2, 10.0, 12.0, 13.8 us, 32 x 64 tiles 14.9;
-// 16 x 11008 19.6, 18.2, 13.3, 15.5, 17.8; 64 x 11008 61, 46, 39, 40, 21.7, 64 x 64
-// tiles 21.6; 1024 x 4096 tiles of 32 / 64 / 128 / 256 rows 62, 57, 42, 87; 8192 x 11008
-// 1089, 1048, 667, 644.
+// The products of float rows.  Measured with bf16 rows, cold weights: 16 x 4096 rows of
+// 16 / 32 / 48 / 64 channels 8.2, 10.0, 12.0, 13.8 us, tiles of 32 x 64 / 32 x 128 15.7, 17.1;
+// 16 x 11008 19.7, 18.2, 13.5, 15.5, 18.2, 19.8; 64 x 11008 61, 46, 39, 40, 22, 20.5; 64 tokens x 2 of
+// 16 experts of 11008 (1x3) 150, 122, 109, 128 x 128 tiles 185; 1024 x 4096 tiles of 32 x 64 /
+// 128 / 256 rows 62, 42, 87; 8192 x 11008 1089, 667, 644.
 constexpr MxCost kW4Shapes[] = {
     {kMxRows16x16, 16, 16, 8.2, 5.2, "rows16x16"},
     {kMxRows16x32, 16, 32, 10.2, 7.0, "rows16x32"},
     {kMxRows16x48, 16, 48, 12.2, 8.8, "rows16x48"},
     {kMxRows16x64, 16, 64, 14.0, 12.6, "rows16x64"},
-    {kMxRows32x64, 32, 64, 18.0, 18.0, "rows32x64"},
-    {kMxTile32x64, 32, 64, 15.5, 6.5, "tile32x64"},
-    {kMxTile64x64, 64, 64, 20.5, 12.0, "tile64x64"},
+    {kMxTile32x64, 32, 64, 15.7, 11.0, "tile32x64"},
+    {kMxTile32x128, 32, 128, 17.5, 20.8, "tile32x128"},
     {kMxTile128x128, 128, 128, 35.0, 30.0, "tile128x128"},
     {kMxTile256x256, 256, 256, 84.0, 120.0, "tile256x256"},
 };
@@ -71,7 +70,8 @@ constexpr MxCost kW4ShapesF32[] = {
 
 }  // namespace
 
-const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N) {
+const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N,
+                        double tile_first) {
   const double experts = (double)(parts < M ? parts : M);
   const double each = (double)M / experts;  // rows of an expert, if all were alike
   const MxCost* best = shapes;
@@ -84,8 +84,9 @@ const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, i
       tiles = experts * (tiles > 1.0 ? tiles : 1.0);
     }
     double rounds = tiles * (double)ceil_div(N, s->channels) / 256.0;
-    if (s->shape < kMxTile32x64) rounds = (double)(int64_t)(rounds + 255.0 / 256.0);
-    const double cost = s->first + s->more * (rounds > 1.0 ? rounds - 1.0 : 0.0);
+    const bool tile = s->shape >= kMxTile32x64;
+    if (!tile) rounds = (double)(int64_t)(rounds + 255.0 / 256.0);
+    const double cost = s->first + (tile ? tile_first : 0.0) + s->more * (rounds > 1.0 ? rounds - 1.0 : 0.0);
     if (cost < least) {
       least = cost;
       best = s;
@@ -97,7 +98,9 @@ const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, i
 const MxCost& mx_w4_shape(int32_t dtype, int64_t M, int64_t parts, int64_t N) {
   if (dtype == QP_F32)
     return mx_choose(kW4ShapesF32, sizeof(kW4ShapesF32) / sizeof(MxCost), M, parts, N);
-  return mx_choose(kW4Shapes, sizeof(kW4Shapes) / sizeof(MxCost), M, parts, N);
+  // (tiles of f16 rows look over their scales first)
+  return mx_choose(kW4Shapes, sizeof(kW4Shapes) / sizeof(MxCost), M, parts, N,
+                   dtype == QP_F16 ? 4.0 : 0.0);
 }
 
 }  // namespace qp

@@ -132,6 +132,7 @@ enum MxShape {
   kMxRows16x64,
   kMxRows32x64,
   kMxTile32x64,
+  kMxTile32x128,
   kMxTile64x64,
   kMxTile128x128,
   kMxTile256x256
@@ -147,7 +148,8 @@ struct MxCost {
   double first, more;
   const char* name;
 };
-const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N);
+const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N,
+                        double tile_first = 0.0);
 const MxCost& mx_a4w4_shape(int64_t M, int64_t parts, int64_t N);
 const MxCost& mx_w4_shape(int32_t dtype, int64_t M, int64_t parts, int64_t N);
 void mx_dx_kernel_name(const qp_mx4* w, int32_t dtype, int64_t M, char* name, size_t bytes);

@@ -573,9 +573,10 @@ qp_status launch_dx_tile(const char* what, const MxDxArgs& a, hipStream_t stream
 // Which kernel, and for few rows in how many splits the channels go: enough workgroups
 // for the card, no split without a step of 32 channels for each of its waves.
 //
-// Measured, bf16, 4096 x 4096 weights: 16 rows 11.9 us by the few-row kernel, 128 21 (128 x
-// 128 tiles 63), 256 32 (62), 1024 118 (76; 256 x 256 tiles 128), 4096 512 (199, 148); of 11008
-// columns 512 rows 166 (98, 131).  f32 rows: 1024 179 (160), 4096 737 (614).
+// Measured, bf16, 4096 x 4096 weights, cold: 16 rows 11.6 us by the few-row kernel (128 x
+// 128 tiles 46), 256 37 (47), 512 71 (49; 256 x 256 tiles 96), 1024 132 (52), 2048 248 (81, 97),
+// 4096 456 (156, 119); of 11008 columns 1024 rows 332 (118, 100).  f32 rows: 256 56 (147), 768
+// 147 (149), 4096 682 (572).
 constexpr int kDxWaves = 8;
 struct DxPlan {
   int tile;         // rows of a tile, 0: few rows
@@ -591,12 +592,15 @@ DxPlan dx_plan(int32_t dtype, int64_t M, const qp_mx4* w) {
     return tiles * (double)ceil_div(w->K, cols) / 256.0;
   };
   const double few = groups(16, 128), t128 = groups(128, 128), t256 = groups(256, 256);
-  auto more = [](double g) { return g > 1.0 ? g - 1.0 : 0.0; };
-  // microseconds at 4096 channels (all grow with them)
+  // microseconds at 4096 channels (all grow with them): up to one workgroup a CU, and
+  // for the further ones
+  auto cost = [](double g, double one, double filled, double more) {
+    return one + filled * (g < 1.0 ? g : 1.0) + more * (g > 1.0 ? g - 1.0 : 0.0);
+  };
   const bool f32 = dtype == QP_F32;
-  const double c0 = 12.0 + (f32 ? 21.0 : 14.0) * few;
-  const double c128 = f32 ? 145.0 + 150.0 * more(t128) : 62.0 + 42.0 * more(t128);
-  const double c256 = f32 ? 1e300 : 126.0 + 85.0 * more(t256);
+  const double c0 = f32 ? 9.0 + 21.5 * few : 9.0 + 15.0 * few;
+  const double c128 = f32 ? cost(t128, 142.0, 10.0, 140.0) : cost(t128, 46.0, 6.0, 36.0);
+  const double c256 = f32 ? 1e300 : cost(t256, 94.0, 25.0, 115.0);
   DxPlan p{0, 1};
   if (c128 < c0 || c256 < c0) {
     p.tile = c256 < c128 ? 256 : 128;

@@ -451,8 +451,9 @@ qp_status mx_run_rows(const MxArgs& a, MxShape shape, hipStream_t stream) {
     case kMxRows16x32: return mx_launch_rows<T, 1, 2, 8, 1>(a, stream);
     case kMxRows16x48: return mx_launch_rows<T, 1, 3, 8, 1>(a, stream);
     case kMxRows16x64: return mx_launch_rows<T, 1, 4, 8, 1>(a, stream);
-    default: return mx_launch_rows<T, 2, 4, 8, 1>(a, stream);
+    default: break;
   }
+  return mx_launch_rows<T, 2, 4, 8, 1>(a, stream);
 }
 
 template <typename T>
@@ -466,7 +467,7 @@ qp_status mx_run_16bit(const MxArgs& a, hipStream_t stream) {
     return mx_launch_w4_tile<T, false, 128, 128, 2, 2, 2>(a, stream);
   switch (shape) {
     case kMxTile32x64: return mx_launch_w4_tile<T, true, 32, 64, 1, 2, 4>(a, stream);
-    case kMxTile64x64: return mx_launch_w4_tile<T, true, 64, 64, 1, 2, 4>(a, stream);
+    case kMxTile32x128: return mx_launch_w4_tile<T, true, 32, 128, 1, 4, 4>(a, stream);
     case kMxTile128x128: return mx_launch_w4_tile<T, true, 128, 128, 2, 2, 2>(a, stream);
     default: return mx_launch_w4_tile<T, true, 256, 256, 2, 4, 2>(a, stream);
   }
