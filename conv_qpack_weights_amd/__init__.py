@@ -969,18 +969,18 @@ class MX4:
 
     def __init__(self, codes, scales, K):
         self.codes, self.scales, self.K = codes, scales, K
-        d = self.desc = Mx4Desc()
-        d.codes, d.scales = codes.data_ptr(), scales.data_ptr()
-        d.rows, d.K = codes.shape[-2], K
-        # (the stride of a single row means nothing to torch: the library gets the
-        # row's length)
-        G = scales.shape[-1]
-        one = codes.shape[-2] < 2
-        d.ld_codes = 16 * G if one else codes.stride(-2)
-        d.ld_scales = -(-G // 4) * 4 if one else scales.stride(-2)
-        d.matrices = codes.shape[0] if codes.dim() == 3 else 1
-        if codes.dim() == 3:
-            d.codes_stride, d.scales_stride = codes.stride(0), scales.stride(0)
+        *lead, rows, G = scales.shape
+        if rows < 2:
+            # (the stride of a single row means nothing to torch: the library gets the
+            # row's length)
+            ldc, lds = 16 * G, -(-G // 4) * 4
+        else:
+            ldc, lds = codes.stride(-2), scales.stride(-2)
+        if lead:
+            self.desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), rows, K, ldc, lds, lead[0],
+                                codes.stride(0), scales.stride(0))
+        else:
+            self.desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), rows, K, ldc, lds, 1, 0, 0)
 
     @property
     def shape(self):
@@ -1005,6 +1005,8 @@ def _mx4_codes(t, rows_shape, G):
 
 def _mx4_scales(rows_shape, G, like):
     """New scales: rows of whole words, the view of their G bytes."""
+    if G % 4 == 0:
+        return like.new_empty((*rows_shape, G), dtype=torch.uint8)
     return like.new_empty((*rows_shape, -(-G // 4) * 4), dtype=torch.uint8)[..., :G]
 
 
@@ -1061,10 +1063,10 @@ def qquantize_rows_mx4(X: torch.Tensor, rule="floor", out=None) -> MX4:
     an expert.  ``rule``: "floor" (a block's scale from its largest value's
     exponent; values above 6 scales become 6) or "ceil" (no value is cut)."""
     assert rule in _MX_RULES, "rule must be 'floor' or 'ceil'"
-    lead = X.shape[:-1]
-    if X.dim() == 3:
+    *lead, K = X.shape
+    if len(lead) == 2:
         assert X.is_contiguous(), "the matrices must be contiguous"
-        X = X.view(-1, X.shape[-1])
+        X = X.view(-1, K)
     dt, M, K, ldx = _rows(X, "X")
     G = -(-K // 32)
     if out is None:

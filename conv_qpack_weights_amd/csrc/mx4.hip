@@ -43,29 +43,30 @@ qp_status run_float(const char* what, const MxArgs& a, int32_t dtype, hipStream_
 }
 
 // The products of float rows.  Measured with bf16 rows, cold weights: 16 x 4096 rows of
-// 16 / 32 / 48 / 64 channels 8.2, 10.0, 12.0, 13.8 us, tiles of 32 x 64 / 32 x 128 15.7, 17.1;
-// 16 x 11008 19.7, 18.2, 13.5, 15.5, 18.2, 19.8; 64 x 11008 61, 46, 39, 40, 22, 20.5; 64 tokens x 2 of
-// 16 experts of 11008 (1x3) 150, 122, 109, 128 x 128 tiles 185; 1024 x 4096 tiles of 32 x 64 /
-// 128 / 256 rows 62, 42, 87; 8192 x 11008 1089, 667, 644.
+// 16 / 32 / 48 / 64 channels 5.6, 6.2, 7.4, 8.2 us, tiles of 32 x 64 / 32 x 128 15.7, 17.1;
+// 16 x 11008 15.7, 13.5, 10.3, 11.0, 18.2, 19.8; 64 x 4096 14.8, 10.1, 12.3, 8.3, 16.5, 17.5;
+// 64 x 11008 47, 31, 28, 24.5, 22, 20.5; 64 tokens x 2 of 16 experts of 11008 (32 channels on)
+// 152, 136, 119, 121, 107, 128 x 128 tiles 161; 4096 tokens x 2 of 8 of them tiles of 128 / 256
+// rows 776, 717; 1024 x 4096 tiles of 32 x 64 / 128 / 256 rows
+// 62, 42, 87; 8192 x 11008 1089, 667, 630.
 constexpr MxCost kW4Shapes[] = {
-    {kMxRows16x16, 16, 16, 8.2, 5.2, "rows16x16"},
-    {kMxRows16x32, 16, 32, 10.2, 7.0, "rows16x32"},
-    {kMxRows16x48, 16, 48, 12.2, 8.8, "rows16x48"},
-    {kMxRows16x64, 16, 64, 14.0, 12.6, "rows16x64"},
-    {kMxTile32x64, 32, 64, 15.7, 11.0, "tile32x64"},
-    {kMxTile32x128, 32, 128, 17.5, 20.8, "tile32x128"},
-    {kMxTile128x128, 128, 128, 35.0, 30.0, "tile128x128"},
-    {kMxTile256x256, 256, 256, 84.0, 120.0, "tile256x256"},
+    {kMxRows16x16, 16, 16, 5.6, 5.0, 3.1, "rows16x16"},
+    {kMxRows16x32, 16, 32, 6.3, 7.2, 3.8, "rows16x32"},
+    {kMxRows16x48, 16, 48, 7.4, 9.0, 5.0, "rows16x48"},
+    {kMxRows16x64, 16, 64, 8.3, 11.4, 6.0, "rows16x64"},
+    {kMxTile32x64, 32, 64, 15.7, 11.0, 6.5, "tile32x64"},
+    {kMxTile32x128, 32, 128, 19.8, 20.0, 14.0, "tile32x128"},
+    {kMxTile128x128, 128, 128, 35.0, 29.0, 30.0, "tile128x128"},
+    {kMxTile256x256, 256, 256, 90.0, 105.0, 105.0, "tile256x256"},
 };
-// The same of f32 rows: 16 x 4096 13.6, 15.3, 17.2, 19.2; 64 x 11008 105, 71, 65, 55, rows
-// of 32 57, 128 x 128 tiles 125; 4096 x 4096 1440 (rows16x32) and 510.
+// The same of f32 rows: 16 x 4096 14.1, 14.8, 15.4, 16.6; 16 x 11008 38, 34, 19.6, 20.8; 64 x
+// 11008 112, 84, 58, 52, 128 x 128 tiles 125; 128 x 4096 78, 56, 40, 33, 121; 4096 x 4096 tiles 510.
 constexpr MxCost kW4ShapesF32[] = {
-    {kMxRows16x16, 16, 16, 13.6, 9.5, "rows16x16"},
-    {kMxRows16x32, 16, 32, 15.5, 11.0, "rows16x32"},
-    {kMxRows16x48, 16, 48, 17.5, 15.0, "rows16x48"},
-    {kMxRows16x64, 16, 64, 19.2, 17.7, "rows16x64"},
-    {kMxRows32x64, 32, 64, 27.0, 28.0, "rows32x64"},
-    {kMxTile128x128, 128, 128, 122.0, 125.0, "tile128x128"},
+    {kMxRows16x16, 16, 16, 14.1, 9.2, 9.2, "rows16x16"},
+    {kMxRows16x32, 16, 32, 15.2, 13.5, 13.5, "rows16x32"},
+    {kMxRows16x48, 16, 48, 16.0, 13.5, 13.5, "rows16x48"},
+    {kMxRows16x64, 16, 64, 17.5, 16.0, 16.0, "rows16x64"},
+    {kMxTile128x128, 128, 128, 122.0, 125.0, 125.0, "tile128x128"},
 };
 
 }  // namespace
@@ -83,10 +84,18 @@ const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, i
       tiles = each / s->rows + 0.5;
       tiles = experts * (tiles > 1.0 ? tiles : 1.0);
     }
-    double rounds = tiles * (double)ceil_div(N, s->channels) / 256.0;
+    const double groups = (double)ceil_div(N, s->channels) / 256.0;
+    double rounds = tiles * groups, own = experts * groups;
     const bool tile = s->shape >= kMxTile32x64;
-    if (!tile) rounds = (double)(int64_t)(rounds + 255.0 / 256.0);
-    const double cost = s->first + (tile ? tile_first : 0.0) + s->more * (rounds > 1.0 ? rounds - 1.0 : 0.0);
+    // (experts of unlike sizes have more tiles than that)
+    if (tile && experts > 1.0) rounds *= 1.1;
+    if (!tile || (s->shape == kMxTile256x256 && rounds > 1.0)) {
+      rounds = (double)(int64_t)(rounds + 255.0 / 256.0);
+      own = (double)(int64_t)(own + 255.0 / 256.0);
+    }
+    own = own < 1.0 ? 1.0 : own;
+    const double cost = s->first + (tile ? tile_first : 0.0) + s->cold * (own - 1.0) +
+                        s->more * (rounds > own ? rounds - own : 0.0);
     if (cost < least) {
       least = cost;
       best = s;

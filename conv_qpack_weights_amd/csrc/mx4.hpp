@@ -57,6 +57,21 @@ __device__ __forceinline__ bf16x8 mx_unpack(uint32_t w, float scale) {
   return __builtin_bit_cast(bf16x8, o);
 }
 
+// Whether a block's weights are f16 values, exactly: its scale one of 2^-23 .. 2^13
+// (then 0.5 and 6 times it are), which the weights of layers have.
+__device__ __forceinline__ bool mx_f16_scale(float scale) {
+  return __builtin_bit_cast(uint32_t, scale) - (104u << 23) <= (36u << 23);
+}
+// The eight values of a word of codes as f16, where they are.
+__device__ __forceinline__ f16x8 mx_unpack_f16(uint32_t w, float scale) {
+  u32x4 o;
+  o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 0));
+  o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 1));
+  o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 2));
+  o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 3));
+  return __builtin_bit_cast(f16x8, o);
+}
+
 // d + a b^T over 128 K: lane l holds 32 values of row l%16 from 32 (l/16) on
 // and their scale in the low byte of sa / sb.
 __device__ __forceinline__ f32x4 mx_mfma16(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x4 d) {
@@ -130,7 +145,6 @@ enum MxShape {
   kMxRows16x32,
   kMxRows16x48,
   kMxRows16x64,
-  kMxRows32x64,
   kMxTile32x64,
   kMxTile32x128,
   kMxTile64x64,
@@ -138,14 +152,16 @@ enum MxShape {
   kMxTile256x256
 };
 
-// What a shape takes: `first` microseconds for up to one workgroup a CU (256) and
-// `more` for every further round of them, at K = 4096 (both grow with K, which changes
-// no order); rounds are whole ones for the few-row kernels, whose workgroups all wait
-// for memory alike.
+// What a shape takes at K = 4096 (all grow with K, which changes no order): `first`
+// microseconds for up to one workgroup a CU (256); `cold` for every further round of
+// workgroups that bring weights of their own, `more` for one that finds its weights in
+// the caches (further row tiles of the same matrix).  Rounds are whole ones for the
+// few-row kernels, whose workgroups all wait for memory alike, and for the largest
+// tile, one to a CU.
 struct MxCost {
   MxShape shape;
   int rows, channels;
-  double first, more;
+  double first, cold, more;
   const char* name;
 };
 const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N,

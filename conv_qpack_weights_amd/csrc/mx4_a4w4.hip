@@ -2,10 +2,11 @@
 // MFMA as they are,
 //   y[r,n] = clamp(sum_b 2^(sa[r,b] + sw[n,b] - 254) sum_{k in b} a[r,k] w[n,k] + bias[n], lo, hi)
 // with every product and scaling exact and the sums in f32.  Few rows: the kernel
-// of mx4_rows.hpp; many rows: tiles over LDS, below.
+// of mx4_stream.hpp; many rows: tiles over LDS, below.
 #include <type_traits>
 
 #include "mx4_rows.hpp"
+#include "mx4_stream.hpp"
 #include "mx4_tile.hpp"
 
 #pragma clang fp contract(off)
@@ -241,18 +242,31 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
     multiply(S2{}, even, now);
     __builtin_amdgcn_sched_barrier(0);
     arrive();
-    issue(s + D, with_scales);
+    // (which first: 8192^3 by 256 x 256 tiles 302 us loads first, 292 last; 1024 x 4096 x
+    // 4096 by 128 x 128 18.0 and 18.8)
+    if constexpr (BM < 256) issue(s + D, with_scales);
     read(even, s + 1, 0);
     read_scales(next, s + 1);
     __builtin_amdgcn_sched_barrier(0);
     multiply(S3{}, odd, now);
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (BM >= 256) issue(s + D, with_scales);
     now = next;
   };
   const int pairs = full / 2;
-  for (int t = 0; t < pairs; ++t) {
-    stage(2 * t, true_type{});
-    stage(2 * t + 1, false_type{});
+  if (tile.r0 + wm * 32 * FM < tile.r1) {
+    for (int t = 0; t < pairs; ++t) {
+      stage(2 * t, true_type{});
+      stage(2 * t + 1, false_type{});
+    }
+  } else {
+    // (a wave without rows only loads, and leaves its SIMD to the others)
+    for (int t = 0; t < pairs; ++t) {
+      arrive();
+      issue(2 * t + D, true_type{});
+      arrive();
+      issue(2 * t + 1 + D, false_type{});
+    }
   }
   wait_vmcnt<0>();
   __syncthreads();
@@ -303,14 +317,16 @@ qp_status launch_tile(const MxArgs& a, hipStream_t stream) {
   return check_launch("qgemm_a4w4_mx (many rows)");
 }
 
-// Which kernel (MxCost, mx_choose).  Measured, cold weights: e.g. 1 x 4096 rows 5.2,
-// 64 x 64 tiles 8.1 us; 32 x 4096 10.1 and 8.4; 256 x 4096 59, 9.1, 128 x 128 tiles 16;
-// 512 x 11008 tiles of 64 / 128 / 256 31.9, 25.2, 36.9; 4096 x 4096 82, 53, 45.
+// Which kernel (MxCost, mx_choose).  Measured, cold weights: e.g. 16 x 4096 rows of 16 / 32
+// channels 4.9, 5.5 us, 64 x 64 tiles 7.9; 64 x 4096 9.2, 7.3, 8.6; 64 x 11008 23, 18, 11.6; 64
+// tokens x 2 of 16 experts of 11008 rows of 32 channels 90, tiles of 64 / 128 / 256 91, 91, 106,
+// 256 x 2 of 16 of 4096 59, 47, 56, 66; 512 x 11008 tiles of 64 / 128 / 256 31.9, 25.2, 36.9; 4096 x 4096 82, 53, 45.
 constexpr MxCost kA4Shapes[] = {
-    {kMxRows16x16, 16, 16, 5.2, 3.0, "rows16x16"},
-    {kMxTile64x64, 64, 64, 8.1, 4.4, "tile64x64"},
-    {kMxTile128x128, 128, 128, 16.0, 11.5, "tile128x128"},
-    {kMxTile256x256, 256, 256, 35.0, 37.0, "tile256x256"},
+    {kMxRows16x16, 16, 16, 4.9, 2.4, 1.6, "rows16x16"},
+    {kMxRows16x32, 16, 32, 5.6, 4.1, 1.9, "rows16x32"},
+    {kMxTile64x64, 64, 64, 8.1, 10.0, 4.4, "tile64x64"},
+    {kMxTile128x128, 128, 128, 19.0, 26.0, 11.5, "tile128x128"},
+    {kMxTile256x256, 256, 256, 35.0, 37.0, 37.0, "tile256x256"},
 };
 
 }  // namespace
@@ -320,15 +336,16 @@ const MxCost& mx_a4w4_shape(int64_t M, int64_t parts, int64_t N) {
 }
 
 qp_status run_mx_a4w4(const MxArgs& a, hipStream_t stream) {
-  if (mx_tile_reaches(a.rows, a.a.ldc) && a.w.ldc < kMxMaxLd) {
-    switch (mx_a4w4_shape(a.rows.M, a.rows.offsets ? a.rows.experts : 1, a.w.rows).shape) {
-      case kMxTile256x256: return launch_tile<256, 256, 2, 4, 2>(a, stream);
-      case kMxTile128x128: return launch_tile<128, 128, 2, 2, 2>(a, stream);
-      case kMxTile64x64: return launch_tile<64, 64, 2, 2, 4>(a, stream);
-      default: break;
-    }
+  if (!mx_tile_reaches(a.rows, a.a.ldc) || a.w.ldc >= kMxMaxLd)
+    return mx_launch_rows<mx4_t, 1, 1, 8, 4>(a, stream);
+  switch (mx_a4w4_shape(a.rows.M, a.rows.offsets ? a.rows.experts : 1, a.w.rows).shape) {
+    case kMxTile256x256: return launch_tile<256, 256, 2, 4, 2>(a, stream);
+    case kMxTile128x128: return launch_tile<128, 128, 2, 2, 2>(a, stream);
+    case kMxTile64x64: return launch_tile<64, 64, 2, 2, 4>(a, stream);
+    case kMxRows16x32: return mx_launch_stream<mx4_t, 2, 4>(a, stream);
+    default: break;
   }
-  return mx_launch_rows<mx4_t, 1, 1, 8, 1>(a, stream);
+  return mx_launch_stream<mx4_t, 1, 4>(a, stream);
 }
 
 }  // namespace qp

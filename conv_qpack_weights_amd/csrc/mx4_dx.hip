@@ -438,28 +438,39 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
         issue_x(1);
         read(even, 0, 0);
         // (no branch between MFMAs, as in the products)
-        for (int s = 0; s < full; ++s) {
-          read(odd, s, 1);
-          __builtin_amdgcn_sched_barrier(0);
-          multiply(even, kind);
-          __builtin_amdgcn_sched_barrier(0);
-          read(even, s, 2);
-          read_w(raw, s + 1);
-          __builtin_amdgcn_sched_barrier(0);
-          multiply(odd, kind);
-          __builtin_amdgcn_sched_barrier(0);
-          read(odd, s, 3);
-          __builtin_amdgcn_sched_barrier(0);
-          convert(raw, s + 1, kind);
-          multiply(even, kind);
-          __builtin_amdgcn_sched_barrier(0);
-          arrive();
-          issue_w(s + 3);
-          issue_x(s + 2);
-          read(even, s + 1, 0);
-          __builtin_amdgcn_sched_barrier(0);
-          multiply(odd, kind);
-          __builtin_amdgcn_sched_barrier(0);
+        if (tile.r0 + wm * 32 * FM < tile.r1) {
+          for (int s = 0; s < full; ++s) {
+            read(odd, s, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(even, kind);
+            __builtin_amdgcn_sched_barrier(0);
+            read(even, s, 2);
+            read_w(raw, s + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(odd, kind);
+            __builtin_amdgcn_sched_barrier(0);
+            read(odd, s, 3);
+            __builtin_amdgcn_sched_barrier(0);
+            convert(raw, s + 1, kind);
+            multiply(even, kind);
+            __builtin_amdgcn_sched_barrier(0);
+            arrive();
+            issue_w(s + 3);
+            issue_x(s + 2);
+            read(even, s + 1, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(odd, kind);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        } else {
+          // (a wave without rows only brings its share of the weights)
+          for (int s = 0; s < full; ++s) {
+            read_w(raw, s + 1);
+            convert(raw, s + 1, kind);
+            arrive();
+            issue_w(s + 3);
+            issue_x(s + 2);
+          }
         }
       } else {
         for (int s = 0; s < full; ++s) {
@@ -511,7 +522,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
                                ? *reinterpret_cast<const uint32_t*>(scales + n * a.w.lds + w * 4) : 0u;
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-          fit = fit && (w * 4 + b >= blocks || ((v >> (8 * b)) & 0xffu) - 104u <= 36u);
+          fit = fit && (w * 4 + b >= blocks || mx_f16_scale(mx_scale((v >> (8 * b)) & 0xffu)));
       }
     }
     if (__syncthreads_and(fit))
@@ -591,7 +602,10 @@ DxPlan dx_plan(int32_t dtype, int64_t M, const qp_mx4* w) {
                                    : (double)ceil_div(M, rows);
     return tiles * (double)ceil_div(w->K, cols) / 256.0;
   };
-  const double few = groups(16, 128), t128 = groups(128, 128), t256 = groups(256, 256);
+  const double few = groups(16, 128), t128 = groups(128, 128);
+  // (one to a CU: whole rounds; experts of unlike sizes have more tiles than that)
+  double t256 = groups(256, 256) * (parts > 1 ? 1.1 : 1.0);
+  if (t256 > 1.0) t256 = (double)(int64_t)(t256 + 255.0 / 256.0);
   // microseconds at 4096 channels (all grow with them): up to one workgroup a CU, and
   // for the further ones
   auto cost = [](double g, double one, double filled, double more) {

@@ -9,32 +9,22 @@
 // l/32) and converts a word for each of the stage's four steps; the rows' operand of
 // step t is piece 4 (l/32) + t of the row.  Weights are the MFMA's first operand.
 //
-// f16 rows: a weight is an f16 exactly where its block's scale is one of 2^-23 ..
-// 2^13 (then 0.5 and 6 times it are), which weights of layers are.  Where a look over
-// the scales finds that all of a workgroup's are, its weights go in as f16 and the
-// rows as they are; else the weights as bf16 and the rows as two bf16 pieces, twice
-// the MFMAs and the cuts.  (Deciding stage by stage instead doubled the registers.)
+// f16 rows: where a look over the scales finds that all of a workgroup's weights are
+// f16 values (mx_f16_scale), they go in as f16 and the rows as they are; else the
+// weights as bf16 and the rows as two bf16 pieces, twice the MFMAs and the cuts.
+// (Deciding stage by stage instead doubled the registers.)
 #pragma once
 
 #include <type_traits>
 
 #include "mx4_rows.hpp"
+#include "mx4_stream.hpp"
 #include "mx4_tile.hpp"
 
 #pragma clang fp contract(off)
 
 namespace qp {
 namespace {
-
-// The eight values of a word of codes as f16, their scale one of 2^-23 .. 2^13.
-__device__ __forceinline__ f16x8 mx_unpack_f16(uint32_t w, float scale) {
-  u32x4 o;
-  o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 0));
-  o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 1));
-  o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 2));
-  o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 3));
-  return __builtin_bit_cast(f16x8, o);
-}
 
 template <typename T, int BM, int BN, int WM, int WN, int D>
 struct W4MxTile {
@@ -306,7 +296,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-          if ((j + i) * 4 + b < G) out |= ((v[i] >> (8 * b)) & 0xffu) - 104u > 36u;
+          if ((j + i) * 4 + b < G) out |= !mx_f16_scale(mx_scale((v[i] >> (8 * b)) & 0xffu));
     }
     const bool fit = out == 0;
     as_f16 = __syncthreads_and(fit);
@@ -349,20 +339,25 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
       multiply(even, now, 2, kind);
       __builtin_amdgcn_sched_barrier(0);
       arrive(place);
-      issue(s, place);
+      // (which first: 4096^3 by 256 x 256 tiles 106 us loads first, 103 last; 1024 x 4096 x
+      // 4096 by 128 x 128 40 and 47)
+      if constexpr (BM < 256) issue(s, place);
       read_x(even, s + 1, 0);
       read_w(next, s + 1);
       __builtin_amdgcn_sched_barrier(0);
       multiply(odd, now, 3, kind);
       __builtin_amdgcn_sched_barrier(0);
+      if constexpr (BM >= 256) issue(s, place);
       now = next;
     };
-    if constexpr (kF16) {
-      if (as_f16) {
-        each([&](int s, auto place) { steps(s, place, true_type{}); });
-      } else {
-        each([&](int s, auto place) { steps(s, place, false_type{}); });
-      }
+    if (tile.r0 + wm * 32 * FM >= tile.r1) {
+      // (a wave without rows only loads, and leaves its SIMD to the others)
+      each([&](int s, auto place) {
+        arrive(place);
+        issue(s, place);
+      });
+    } else if (kF16 && as_f16) {
+      each([&](int s, auto place) { steps(s, place, std::bool_constant<kF16>{}); });
     } else {
       each([&](int s, auto place) { steps(s, place, false_type{}); });
     }
@@ -379,15 +374,10 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
       arrive(place);
       issue(s, place);
     };
-    if constexpr (kF16) {
-      if (as_f16) {
-        each([&](int s, auto place) { steps(s, place, true_type{}); });
-      } else {
-        each([&](int s, auto place) { steps(s, place, false_type{}); });
-      }
-    } else {
+    if (kF16 && as_f16)
+      each([&](int s, auto place) { steps(s, place, std::bool_constant<kF16>{}); });
+    else
       each([&](int s, auto place) { steps(s, place, false_type{}); });
-    }
   }
   wait_vmcnt<0>();
   __syncthreads();
@@ -445,32 +435,28 @@ qp_status mx_launch_w4_tile(const MxArgs& a, hipStream_t stream) {
 }
 
 template <typename T>
-qp_status mx_run_rows(const MxArgs& a, MxShape shape, hipStream_t stream) {
-  switch (shape) {
-    case kMxRows16x16: return mx_launch_rows<T, 1, 1, 8, 1>(a, stream);
-    case kMxRows16x32: return mx_launch_rows<T, 1, 2, 8, 1>(a, stream);
-    case kMxRows16x48: return mx_launch_rows<T, 1, 3, 8, 1>(a, stream);
-    case kMxRows16x64: return mx_launch_rows<T, 1, 4, 8, 1>(a, stream);
-    default: break;
-  }
-  return mx_launch_rows<T, 2, 4, 8, 1>(a, stream);
-}
-
-template <typename T>
 qp_status mx_run_16bit(const MxArgs& a, hipStream_t stream) {
   const MxShape shape = mx_w4_shape(__is_same(T, f16_t) ? QP_F16 : QP_BF16, a.rows.M,
                                     a.rows.offsets ? a.rows.experts : 1, a.w.rows)
                             .shape;
-  if (shape < kMxTile32x64 || a.w.ldc >= kMxMaxLd) return mx_run_rows<T>(a, shape, stream);
-  // rows that direct loads cannot take go through registers
-  if ((uintptr_t)a.X % 4 || a.ldx % 2 || !mx_tile_reaches(a.rows, a.ldx * 2))
-    return mx_launch_w4_tile<T, false, 128, 128, 2, 2, 2>(a, stream);
+  // what direct loads cannot take goes through registers
+  const bool weights = a.w.ldc < kMxMaxLd;
+  if ((uintptr_t)a.X % 4 || a.ldx % 2 || !mx_tile_reaches(a.rows, a.ldx * 2) || !weights) {
+    if (shape >= kMxTile128x128 && weights)
+      return mx_launch_w4_tile<T, false, 128, 128, 2, 2, 2>(a, stream);
+    return mx_launch_rows<T, 1, 2, 8, 4>(a, stream);
+  }
   switch (shape) {
+    case kMxRows16x16: return mx_launch_stream<T, 1, 4>(a, stream);
+    case kMxRows16x32: return mx_launch_stream<T, 2, 4>(a, stream);
+    case kMxRows16x48: return mx_launch_stream<T, 3, 4>(a, stream);
+    case kMxRows16x64: return mx_launch_stream<T, 4, 4>(a, stream);
     case kMxTile32x64: return mx_launch_w4_tile<T, true, 32, 64, 1, 2, 4>(a, stream);
     case kMxTile32x128: return mx_launch_w4_tile<T, true, 32, 128, 1, 4, 4>(a, stream);
     case kMxTile128x128: return mx_launch_w4_tile<T, true, 128, 128, 2, 2, 2>(a, stream);
-    default: return mx_launch_w4_tile<T, true, 256, 256, 2, 4, 2>(a, stream);
+    default: break;
   }
+  return mx_launch_w4_tile<T, true, 256, 256, 2, 4, 2>(a, stream);
 }
 
 }  // namespace

@@ -1,0 +1,175 @@
+"""Every kernel of the MXFP4 products and their gradient, with every row type, dense
+and by expert, at sizes that cut its tiles, its steps of K and its last block -- and
+rows at odd addresses, which the kernels' direct loads cannot take.  The sizes are
+held to the kernels they are there for.  Tolerances as in test_gpu_mx4.py, against
+64-bit products on the card."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+ROUND = {"f32": 0.0, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+
+
+@pytest.fixture(scope="module")
+def qp():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need an MI355X"
+    import conv_qpack_weights_amd as qp
+    return qp
+
+
+def _dt(name):
+    import torch
+    return {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[name]
+
+
+def _matrix(qp, g, *shape):
+    """A random MX4, and its values in f64 on the card."""
+    import torch
+    *lead, K = shape
+    G = -(-K // 32)
+    codes = torch.randint(0, 256, (*lead, 16 * G), generator=g, dtype=torch.uint8)
+    if K % 32:
+        both = torch.stack((codes & 15, codes >> 4), -1).reshape(*lead, 32 * G)
+        both[..., K:] = 0
+        codes = both[..., 0::2] | (both[..., 1::2] << 4)
+    scales = torch.randint(118, 130, (*lead, G), generator=g, dtype=torch.uint8)
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
+    grid = torch.cat((grid, -grid))
+    v = grid[torch.stack((codes & 15, codes >> 4), -1).long()].reshape(*lead, 32 * G)
+    v = v * torch.pow(2.0, scales.double() - 127).repeat_interleave(32, -1)
+    return qp.mx4_tensor(codes.cuda(), scales.cuda(), K), v[..., :K].cuda()
+
+
+def _rows(g, M, K, dtype, odd=False):
+    import torch
+    x = torch.randn(M, K + 3, generator=g).to(_dt(dtype)).cuda()
+    x = x[:, 1:1 + K] if odd else x[:, :K].contiguous()
+    return x, x.double()
+
+
+def _close(got, want, A, terms, dtype, what):
+    import torch
+    got = got.double()
+    assert torch.isfinite(got).all(), what
+    tol = (3 * terms / 32 + 64) * 2.0 ** -23 * A + ROUND[dtype] * want.abs() * 1.01 \
+        + (2.0 ** -25 if dtype == "f16" else 0.0)
+    off = (got - want).abs()
+    assert (off <= tol).all(), "%s: %d outputs off, worst by %.3g of its tolerance" % (
+        what, int((off > tol).sum()), float((off / tol.clamp_min(1e-300)).max()))
+
+
+SMALL = [("rows16x16", 5, 300), ("rows16x32", 30, 4010), ("rows16x48", 13, 9000),
+         ("rows16x64", 61, 4030)]
+PRODUCTS = (
+    [("a4w4", t, k, M, N) for t in ("f32", "bf16", "f16") for k, M, N in
+     [("rows16x16", 5, 300), ("rows16x32", 45, 4010), ("tile64x64", 250, 4010),
+      ("tile128x128", 1100, 4010), ("tile256x256", 4090, 4090)]]
+    + [("w4", t, k, M, N) for t in ("bf16", "f16") for k, M, N in SMALL +
+       [("tile32x64", 146, 4900), ("tile32x128", 500, 4010), ("tile128x128", 1100, 4010),
+        ("tile256x256", 4090, 4090)]]
+    + [("w4", "f32", k, M, N) for k, M, N in SMALL + [("tile128x128", 1100, 4010)]])
+
+
+@pytest.mark.parametrize("product,dtype,kernel,M,N", PRODUCTS)
+def test_product_kernels(qp, product, dtype, kernel, M, N):
+    import torch
+    g = torch.Generator().manual_seed(M + N)
+    # whole steps and cut ones; a K below a step; many steps
+    for K in (31, 64, 330, 768, 1500):
+        if M * N > 8e6 and K not in (330, 768):
+            continue
+        W, w = _matrix(qp, g, N, K)
+        assert qp.qgemm_mx_kernel_name(product, M, W, _dt(dtype)) == kernel
+        print("mx4 kernel", product, dtype, kernel, M, N, K, flush=True)
+        bias = torch.randn(N, generator=g).cuda()
+        for odd in (False, True) if product == "w4" else (False,):
+            if product == "a4w4":
+                A, a = _matrix(qp, g, M, K)
+                got = qp.qgemm_a4w4_mx(A, W, bias, out_dtype=_dt(dtype))
+            else:
+                A, a = _rows(g, M, K, dtype, odd)
+                got = qp.qgemm_w4_mx(A, W, bias)
+            _close(got, a @ w.t().contiguous() + bias.double(),
+                   a.abs() @ w.abs().t().contiguous() + bias.double().abs(), K, dtype,
+                   "K=%d odd=%s" % (K, odd))
+
+
+@pytest.mark.parametrize("dtype,kernel,M,K", [
+    (t, k, M, K) for t in ("f32", "bf16", "f16") for k, M, K in
+    [("rows16x128", 5, 300), ("rows16x128", 140, 1500), ("tile128x128", 2100, 4010)]
+    + ([] if t == "f32" else [("tile256x256", 4090, 4090)])])
+def test_gradient_kernels(qp, dtype, kernel, M, K):
+    import torch
+    g = torch.Generator().manual_seed(M + K)
+    for N in (1, 63, 64, 330, 768, 1500):
+        if M * K > 8e6 and N not in (63, 330, 768):
+            continue
+        W, w = _matrix(qp, g, N, K)
+        assert qp.qgemm_mx_kernel_name("w4_dx", M, W, _dt(dtype)).split("/")[0] == kernel
+        print("mx4 gradient kernel", dtype, kernel, M, N, K, flush=True)
+        for odd in (False, True):
+            dY, dy = _rows(g, M, N, dtype, odd)
+            _close(qp.qgemm_w4_mx_dx(dY, W), dy @ w, dy.abs() @ w.abs(), N, dtype,
+                   "N=%d odd=%s" % (N, odd))
+
+
+EXPERTS = [  # product, kernel, slots, experts, channels (the gradient's columns)
+    ("a4w4", "rows16x16", 40, 8, 200), ("a4w4", "rows16x32", 128, 16, 5500),
+    ("a4w4", "tile64x64", 600, 3, 2000), ("a4w4", "tile128x128", 2600, 3, 2000),
+    ("a4w4", "tile256x256", 6000, 3, 4000),
+    ("w4", "rows16x16", 40, 8, 200), ("w4", "rows16x64", 64, 8, 4000),
+    ("w4", "tile32x128", 128, 16, 5500), ("w4", "tile128x128", 2600, 3, 2000),
+    ("w4", "tile256x256", 6000, 3, 4000),
+    ("w4_dx", "rows16x128", 300, 3, 300), ("w4_dx", "tile128x128", 2600, 3, 2000),
+    ("w4_dx", "tile256x256", 6000, 3, 2000)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("product,kernel,S,E,N", EXPERTS)
+def test_kernels_by_expert(qp, product, kernel, S, E, N, dtype):
+    """Ragged experts, one of them empty; rows behind the last; products through the
+    map, with slots that are no row."""
+    import torch
+    if dtype == "f32" and product != "a4w4" and kernel in ("tile256x256", "tile32x128"):
+        pytest.skip("f32 rows have no such kernel")
+    g = torch.Generator().manual_seed(S + N)
+    K = 330
+    cut = torch.sort(torch.randint(0, S - 2, (E,), generator=g)).values
+    cut[1] = cut[0]
+    off = torch.cat((torch.zeros(1, dtype=torch.long), cut))
+    offsets = off.int().cuda()
+    # (the gradient: N columns, 330 channels)
+    W, w = _matrix(qp, g, E, K, N) if product == "w4_dx" else _matrix(qp, g, E, N, K)
+    name = qp.qgemm_mx_kernel_name(product, S, W, _dt(dtype)).split("/")[0]
+    if dtype != "f32":
+        assert name == kernel
+    print("mx4 by expert", product, dtype, name, S, E, N, flush=True)
+    if product == "w4_dx":
+        X, x = _rows(g, S, K, dtype)
+        got, terms, cols = qp.qgemm_w4_mx_experts_dx(X, W, offsets), K, N
+        src, weights = torch.arange(S), w
+    else:
+        T = S // 2
+        slot = torch.randint(0, 2 * T, (S,), generator=g)
+        slot[1], slot[5] = -1, 2 * T
+        src = torch.where((slot >= 0) & (slot < 2 * T), slot // 2, torch.full_like(slot, -1))
+        through = dict(rows=slot.int().cuda(), row_div=2)
+        terms, cols = K, N
+        weights = w.transpose(1, 2).contiguous()
+        if product == "a4w4":
+            A, x = _matrix(qp, g, T, K)
+            got = qp.qgemm_a4w4_mx_experts(A, W, offsets, out_dtype=_dt(dtype), **through)
+        else:
+            X, x = _rows(g, T, K, dtype)
+            got = qp.qgemm_w4_mx_experts(X, W, offsets, **through)
+    x = torch.cat((x, torch.zeros_like(x[:1])))        # row -1: zeros
+    want = torch.zeros(S, cols, dtype=torch.float64, device="cuda")
+    A = torch.zeros_like(want)
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        rows = x[src[s].cuda()]
+        want[s], A[s] = rows @ weights[e], rows.abs() @ weights[e].abs()
+    _close(got, want, A, terms, dtype, "by expert")
+    assert (got[int(off[E]):] == 0).all()

@@ -24,23 +24,25 @@ def _weights(qp, N, K, E=1):
 # product, row type, M, N, K, experts, kernel
 CHOICES = [
     ("a4w4", "bf16", 1, 4096, 4096, 1, "rows16x16"),
-    ("a4w4", "bf16", 64, 11008, 4096, 1, "tile64x64"),
+    ("a4w4", "bf16", 64, 4096, 4096, 1, "rows16x32"),
+    ("a4w4", "bf16", 128, 11008, 4096, 16, "rows16x32"),
+    ("a4w4", "bf16", 256, 4096, 4096, 1, "tile64x64"),
     ("a4w4", "bf16", 512, 11008, 4096, 1, "tile128x128"),
     ("a4w4", "bf16", 8192, 8192, 8192, 1, "tile256x256"),
     ("w4", "bf16", 1, 4096, 4096, 1, "rows16x16"),
-    ("w4", "f16", 16, 8192, 4096, 1, "rows16x32"),
+    ("w4", "f16", 32, 4096, 4096, 1, "rows16x32"),
     ("w4", "bf16", 16, 11008, 4096, 1, "rows16x48"),
     ("w4", "f16", 64, 4096, 4096, 1, "rows16x64"),
-    ("w4", "bf16", 128, 4096, 4096, 1, "tile32x64"),
-    ("w4", "f16", 256, 11008, 4096, 1, "tile64x64"),
+    ("w4", "f16", 146, 4900, 4096, 1, "tile32x64"),
+    ("w4", "bf16", 512, 4096, 4096, 1, "tile32x128"),
     ("w4", "bf16", 1024, 4096, 4096, 1, "tile128x128"),
     ("w4", "f16", 8192, 11008, 4096, 1, "tile256x256"),
+    ("w4", "bf16", 128, 11008, 4096, 16, "tile32x128"),
     ("w4", "bf16", 8192, 11008, 4096, 8, "tile256x256"),
     ("w4", "f32", 1, 4096, 4096, 1, "rows16x16"),
-    ("w4", "f32", 16, 8192, 4096, 1, "rows16x32"),
+    ("w4", "f32", 32, 4096, 4096, 1, "rows16x32"),
     ("w4", "f32", 16, 11008, 4096, 1, "rows16x48"),
     ("w4", "f32", 64, 4096, 4096, 1, "rows16x64"),
-    ("w4", "f32", 128, 4096, 4096, 1, "rows32x64"),
     ("w4", "f32", 4096, 4096, 4096, 1, "tile128x128"),
     ("w4_dx", "bf16", 16, 4096, 4096, 1, "rows16x128/8"),
     ("w4_dx", "f16", 256, 4096, 4096, 1, "rows16x128/1"),
