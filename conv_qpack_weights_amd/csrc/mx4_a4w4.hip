@@ -242,15 +242,14 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
     multiply(S2{}, even, now);
     __builtin_amdgcn_sched_barrier(0);
     arrive();
-    // (which first: 8192^3 by 256 x 256 tiles 302 us loads first, 292 last; 1024 x 4096 x
-    // 4096 by 128 x 128 18.0 and 18.8)
-    if constexpr (BM < 256) issue(s + D, with_scales);
+    // (loads first: behind the MFMAs they made 8192^3 2% faster, but 4096 tokens x 2 of 8
+    // experts and 1024 x 4096 x 4096 4% slower)
+    issue(s + D, with_scales);
     read(even, s + 1, 0);
     read_scales(next, s + 1);
     __builtin_amdgcn_sched_barrier(0);
     multiply(S3{}, odd, now);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (BM >= 256) issue(s + D, with_scales);
     now = next;
   };
   const int pairs = full / 2;
@@ -336,7 +335,8 @@ const MxCost& mx_a4w4_shape(int64_t M, int64_t parts, int64_t N) {
 }
 
 qp_status run_mx_a4w4(const MxArgs& a, hipStream_t stream) {
-  if (!mx_tile_reaches(a.rows, a.a.ldc) || a.w.ldc >= kMxMaxLd)
+  const int64_t apart = a.a.ldc > a.a.lds ? a.a.ldc : a.a.lds;
+  if (!mx_tile_reaches(a.rows, apart) || a.w.ldc >= kMxMaxLd || a.w.lds >= kMxMaxLd)
     return mx_launch_rows<mx4_t, 1, 1, 8, 4>(a, stream);
   switch (mx_a4w4_shape(a.rows.M, a.rows.offsets ? a.rows.experts : 1, a.w.rows).shape) {
     case kMxTile256x256: return launch_tile<256, 256, 2, 4, 2>(a, stream);

@@ -10,7 +10,8 @@ qp_status run_mx_f32(const MxArgs& a, hipStream_t stream) {
     case kMxRows16x64: break;
     default:
       // (LDS holds three pieces of 128 rows)
-      if (a.w.ldc < kMxMaxLd) return mx_launch_w4_tile<float, false, 128, 128, 2, 2, 2>(a, stream);
+      if (a.w.ldc < kMxMaxLd && a.w.lds < kMxMaxLd)
+        return mx_launch_w4_tile<float, false, 128, 128, 2, 2, 2>(a, stream);
   }
   return mx_launch_rows<float, 1, 4, 8, 4>(a, stream);
 }

@@ -440,7 +440,7 @@ qp_status mx_run_16bit(const MxArgs& a, hipStream_t stream) {
                                     a.rows.offsets ? a.rows.experts : 1, a.w.rows)
                             .shape;
   // what direct loads cannot take goes through registers
-  const bool weights = a.w.ldc < kMxMaxLd;
+  const bool weights = a.w.ldc < kMxMaxLd && a.w.lds < kMxMaxLd;
   if ((uintptr_t)a.X % 4 || a.ldx % 2 || !mx_tile_reaches(a.rows, a.ldx * 2) || !weights) {
     if (shape >= kMxTile128x128 && weights)
       return mx_launch_w4_tile<T, false, 128, 128, 2, 2, 2>(a, stream);

@@ -126,14 +126,13 @@ EXPERTS = [  # product, kernel, slots, experts, channels (the gradient's columns
     ("w4_dx", "tile256x256", 6000, 3, 2000)]
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("product,kernel,S,E,N", EXPERTS)
+@pytest.mark.parametrize("product,kernel,S,E,N,dtype", [
+    (*c, t) for c in EXPERTS for t in ("bf16", "f16", "f32")
+    if t != "f32" or c[0] == "a4w4" or c[1] not in ("tile256x256", "tile32x128")])
 def test_kernels_by_expert(qp, product, kernel, S, E, N, dtype):
     """Ragged experts, one of them empty; rows behind the last; products through the
     map, with slots that are no row."""
     import torch
-    if dtype == "f32" and product != "a4w4" and kernel in ("tile256x256", "tile32x128"):
-        pytest.skip("f32 rows have no such kernel")
     g = torch.Generator().manual_seed(S + N)
     K = 330
     cut = torch.sort(torch.randint(0, S - 2, (E,), generator=g)).values
@@ -173,3 +172,91 @@ def test_kernels_by_expert(qp, product, kernel, S, E, N, dtype):
         want[s], A[s] = rows @ weights[e], rows.abs() @ weights[e].abs()
     _close(got, want, A, terms, dtype, "by expert")
     assert (got[int(off[E]):] == 0).all()
+
+
+@pytest.mark.parametrize("M", [3, 150])
+def test_rows_far_apart(qp, M):
+    """Rows 8 MiB apart, as far as the description allows: more than 32-bit offsets
+    within a tile reach."""
+    import torch
+    g = torch.Generator().manual_seed(M)
+    N, K, far = 40, 330, 1 << 23
+    W, w = _matrix(qp, g, N, K)
+    A, a = _matrix(qp, g, M, K)
+
+    def spread(m, codes, scales):
+        """The matrix with its codes' or scales' rows `far` bytes apart."""
+        c, s = m.codes, m.scales
+        if codes:
+            c = torch.zeros(c.shape[0] * far, dtype=torch.uint8, device="cuda").as_strided(
+                c.shape, (far, 1)).copy_(c)
+        if scales:
+            s = torch.zeros(s.shape[0] * far, dtype=torch.uint8, device="cuda").as_strided(
+                s.shape, (far, 1)).copy_(s)
+        return qp.MX4(c, s, m.K)
+
+    A_abs = a.abs() @ w.abs().t().contiguous()
+    for codes, scales in ((True, False), (False, True)):
+        print("mx4 far apart", M, codes, scales, flush=True)
+        Wf, Af = spread(W, codes, scales), spread(A, codes, scales)
+        for x, y in ((A, Wf), (Af, W)):
+            _close(qp.qgemm_a4w4_mx(x, y), a @ w.t().contiguous(), A_abs, K, "f32", "a4w4")
+        for dtype in ("f32", "bf16", "f16"):
+            X, x = _rows(g, M, K, dtype)
+            _close(qp.qgemm_w4_mx(X, Wf), x @ w.t().contiguous(), x.abs() @ w.abs().t().contiguous(),
+                   K, dtype, "w4")
+            dY, dy = _rows(g, M, N, dtype)
+            _close(qp.qgemm_w4_mx_dx(dY, Wf), dy @ w, dy.abs() @ w.abs(), N, dtype, "dx")
+    X, x = _rows(g, M, K, "bf16")
+    wide = torch.zeros(M * (far // 2 + 8), dtype=torch.bfloat16, device="cuda").as_strided(
+        (M, K), (far // 2 + 8, 1)).copy_(X)
+    _close(qp.qgemm_w4_mx(wide, W), x @ w.t().contiguous(), x.abs() @ w.abs().t().contiguous(), K,
+           "bf16", "w4")
+
+
+def test_rows_past_32_bits_through_the_map(qp):
+    """Tokens whose rows lie beyond 2^31 bytes, read through the map, and products of as
+    many rows in one call's place (sorted rows from far down)."""
+    import torch
+    g = torch.Generator().manual_seed(1)
+    E, N, K, T = 2, 70, 4096, 270000
+    W, w = _matrix(qp, g, E, N, K)
+    X = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    X[-40:] = torch.randn(40, K, generator=g).to(torch.bfloat16).cuda()
+    x = X[-40:].double()
+    offsets = torch.tensor([0, 15, 40], dtype=torch.int32, device="cuda")
+    rows = torch.arange(T - 40, T, dtype=torch.int32, device="cuda")
+    wt = w.transpose(1, 2).contiguous()
+    want = torch.cat((x[:15] @ wt[0], x[15:] @ wt[1]))
+    A = torch.cat((x[:15].abs() @ wt[0].abs(), x[15:].abs() @ wt[1].abs()))
+    _close(qp.qgemm_w4_mx_experts(X, W, offsets, rows=rows), want, A, K, "bf16", "w4")
+    q = qp.qquantize_rows_mx4(X)
+    back = qp.qdequantize_rows_mx4(qp.MX4(q.codes[-40:], q.scales[-40:], K)).double()
+    want = torch.cat((back[:15] @ wt[0], back[15:] @ wt[1]))
+    A = torch.cat((back[:15].abs() @ wt[0].abs(), back[15:].abs() @ wt[1].abs()))
+    _close(qp.qgemm_a4w4_mx_experts(q, W, offsets, rows=rows), want, A, K, "f32", "a4w4")
+    # the same rows at the end of a call of all of them
+    Y = qp.qgemm_w4_mx(X, W[0])
+    _close(Y[-40:], x @ wt[0], x.abs() @ wt[0].abs(), K, "bf16", "w4 of many rows")
+    assert (Y[:-40] == 0).all()
+
+
+def test_values_below_the_normal_range(qp):
+    """bf16 and f32 rows among the subnormal values, brought back by the weights."""
+    import torch
+    g = torch.Generator().manual_seed(5)
+    for M in (4, 600):
+        N, K = 4010 if M > 4 else 70, 256
+        W, w = _matrix(qp, g, N, K)
+        W.scales.add_(80)
+        w = w * 2.0 ** 80
+        for dtype in ("bf16", "f32"):
+            X = (torch.randn(M, K, generator=g) * 2.0 ** -126).to(_dt(dtype)).cuda()
+            x = X.double()
+            A = x.abs() @ w.abs().t().contiguous()
+            # f32 values are cut, not rounded, into bf16 pieces, whose smallest step is
+            # 2^-133: what is lost of one is below that
+            slack = 0.0 if dtype == "bf16" else 2.0 ** -133 * w.abs().sum(1)
+            off = (qp.qgemm_w4_mx(X, W, out_dtype=torch.float32).double()
+                   - x @ w.t().contiguous()).abs()
+            assert (off <= (3 * K / 32 + 64) * 2.0 ** -23 * A + slack).all(), (dtype, M)
