@@ -9,6 +9,10 @@ weights are int4 blobs (packed once), the rows stay in bf16:
               to the tokens and to the router's weights; the 4-bit weights are
               frozen (adapters or the router learn); first derivatives only
 
+MxExpertLayer is the same layer with MXFP4 weights, as a checkpoint holds them; it
+can also serve with MXFP4 rows: the tokens are quantized once, before their copies
+to the experts, and the gated rows once more between the products.
+
 Run it on an MI355X:  python examples/moe_w4_layer.py
 """
 import os
@@ -104,6 +108,14 @@ class ExpertLayer:
         gate, up = h.chunk(2, dim=1)
         return torch.nn.functional.silu(gate) * up
 
+    def _experts(self, x, which, offsets):
+        return _Experts.apply(x, *which, offsets)
+
+    def _matrices(self, which, dtype):
+        blobs, info = which
+        return [qp.qunpack_weights(b, info, values=False, scales=False, dequant=True)[3].to(dtype)
+                for b in blobs]
+
     def serve(self, x, ids, weights):
         """x [T, H], ids int [T, top_k] (negative: no expert), weights f32 [T, top_k]."""
         offsets, row_of_slot, slot_of_row = qp.qmoe_sort(ids, self.experts)
@@ -114,16 +126,13 @@ class ExpertLayer:
     def train(self, x, ids, weights):
         """The same with gradients to x and weights."""
         xs, offsets, row_of_slot, slot_of_row = _Dispatch.apply(x, ids, self.experts)
-        h = _Experts.apply(xs, *self.up, offsets)
-        z = _Experts.apply(self._gate(h), *self.down, offsets)
+        h = self._experts(xs, self.up, offsets)
+        z = self._experts(self._gate(h), self.down, offsets)
         return _Combine.apply(z, weights, row_of_slot, slot_of_row)
 
     def dense(self, x, ids, weights):
         """The layer from the formulas in x's type: a loop over tokens' choices."""
-        mats = []
-        for blobs, info in (self.up, self.down):
-            mats.append([qp.qunpack_weights(b, info, values=False, scales=False,
-                                            dequant=True)[3].to(x.dtype) for b in blobs])
+        mats = [self._matrices(which, x.dtype) for which in (self.up, self.down)]
         y = torch.zeros_like(x)
         for e in range(self.experts):
             for j in range(ids.shape[1]):
@@ -134,12 +143,56 @@ class ExpertLayer:
         return y
 
 
-def make(experts=8, H=512, F=1408, seed=0, device="cuda"):
+class _MxExperts(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        ctx.save_for_backward(offsets)
+        ctx.w = w
+        return qp.qgemm_w4_mx_experts(x, w, offsets)
+
+    @staticmethod
+    def backward(ctx, dy):
+        offsets, = ctx.saved_tensors
+        dx = _Once.apply(lambda d: qp.qgemm_w4_mx_experts_dx(d.contiguous(), ctx.w, offsets), dy)
+        return dx, None, None
+
+
+class MxExpertLayer(ExpertLayer):
+    """gate_up [E, 2F, H] and down [E, H, F]: MX4 matrices, or float weights that are
+    quantized to them.  With ``rows4`` serve() quantizes the rows of both products."""
+
+    def __init__(self, gate_up, down, rows4=False):
+        self.up, self.down = (w if isinstance(w, qp.MX4) else qp.qquantize_rows_mx4(w, "ceil")
+                              for w in (gate_up, down))
+        self.experts = self.up.shape[0]
+        self.rows4 = rows4
+
+    def serve(self, x, ids, weights):
+        offsets, row_of_slot, slot_of_row = qp.qmoe_sort(ids, self.experts)
+        k = ids.shape[1]
+        if self.rows4:
+            h = qp.qgemm_a4w4_mx_experts(qp.qquantize_rows_mx4(x, "ceil"), self.up, offsets,
+                                         rows=slot_of_row, row_div=k, out_dtype=x.dtype)
+            z = qp.qgemm_a4w4_mx_experts(qp.qquantize_rows_mx4(self._gate(h), "ceil"), self.down,
+                                         offsets, out_dtype=x.dtype)
+        else:
+            h = qp.qgemm_w4_mx_experts(x, self.up, offsets, rows=slot_of_row, row_div=k)
+            z = qp.qgemm_w4_mx_experts(self._gate(h), self.down, offsets)
+        return qp.qmoe_combine(z, row_of_slot, weights)
+
+    def _experts(self, x, which, offsets):
+        return _MxExperts.apply(x, which, offsets)
+
+    def _matrices(self, which, dtype):
+        return [qp.qdequantize_rows_mx4(which[e]).to(dtype) for e in range(self.experts)]
+
+
+def make(experts=8, H=512, F=1408, seed=0, device="cuda", mx=False, rows4=False):
     g = torch.Generator(device=device)
     g.manual_seed(seed)
     up = torch.randn(experts, 2 * F, H, generator=g, device=device) / H ** 0.5
     down = torch.randn(experts, H, F, generator=g, device=device) / F ** 0.5
-    return ExpertLayer(up, down), g
+    return (MxExpertLayer(up, down, rows4) if mx else ExpertLayer(up, down)), g
 
 
 def route(g, T, H, experts, top_k, device="cuda"):
@@ -149,10 +202,11 @@ def route(g, T, H, experts, top_k, device="cuda"):
     return x, ids, torch.softmax(top, dim=1).contiguous()
 
 
-def compare(T=64, experts=8, H=512, F=1408, top_k=2, dtype=torch.bfloat16, seed=0):
+def compare(T=64, experts=8, H=512, F=1408, top_k=2, dtype=torch.bfloat16, seed=0,
+            mx=False):
     """Relative errors (norms) of the served output, the trained output and the
     gradients against the f64 formulas on the same 4-bit weights."""
-    layer, g = make(experts, H, F, seed)
+    layer, g = make(experts, H, F, seed, mx=mx)
     x, ids, weights = route(g, T, H, experts, top_k)
     ids[0] = -1                                     # a padding token
     x = x.to(dtype)
@@ -171,22 +225,26 @@ def compare(T=64, experts=8, H=512, F=1408, top_k=2, dtype=torch.bfloat16, seed=
 
 
 def main():
-    for name, err in compare().items():
-        print("%-10s relative error against the formulas in 64 bits: %.2e" % (name, err))
-    layer, g = make(experts=16, H=4096, F=11008 // 2)
-    for T in (1, 16, 256):
-        x, ids, weights = route(g, T, 4096, 16, 2)
-        x = x.bfloat16()
-        for _ in range(3):
-            layer.serve(x, ids, weights)
-        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-        start.record()
-        for _ in range(20):
-            layer.serve(x, ids, weights)
-        end.record()
-        end.synchronize()
-        print("%4d tokens, 16 experts of 4096 x 5504, 2 a token: %.1f us a layer" %
-              (T, start.elapsed_time(end) / 20 * 1e3))
+    for what, mx in (("int4", False), ("MXFP4", True)):
+        for name, err in compare(mx=mx).items():
+            print("%-5s %-10s relative error against the formulas in 64 bits: %.2e" %
+                  (what, name, err))
+    for what, kind in (("int4 weights", {}), ("MXFP4 weights", {"mx": True}),
+                       ("MXFP4 weights and rows", {"mx": True, "rows4": True})):
+        layer, g = make(experts=16, H=4096, F=11008 // 2, **kind)
+        for T in (1, 16, 256):
+            x, ids, weights = route(g, T, 4096, 16, 2)
+            x = x.bfloat16()
+            for _ in range(3):
+                layer.serve(x, ids, weights)
+            start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            start.record()
+            for _ in range(20):
+                layer.serve(x, ids, weights)
+            end.record()
+            end.synchronize()
+            print("%-22s %4d tokens, 16 experts of 4096 x 5504, 2 a token: %.1f us a layer" %
+                  (what, T, start.elapsed_time(end) / 20 * 1e3))
 
 
 if __name__ == "__main__":
