@@ -71,8 +71,7 @@ constexpr MxCost kW4ShapesF32[] = {
 
 }  // namespace
 
-const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N,
-                        double tile_first) {
+const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N) {
   const double experts = (double)(parts < M ? parts : M);
   const double each = (double)M / experts;  // rows of an expert, if all were alike
   const MxCost* best = shapes;
@@ -94,7 +93,7 @@ const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, i
       own = (double)(int64_t)(own + 255.0 / 256.0);
     }
     own = own < 1.0 ? 1.0 : own;
-    const double cost = s->first + (tile ? tile_first : 0.0) + s->cold * (own - 1.0) +
+    const double cost = s->first + s->cold * (own - 1.0) +
                         s->more * (rounds > own ? rounds - own : 0.0);
     if (cost < least) {
       least = cost;
@@ -107,9 +106,7 @@ const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, i
 const MxCost& mx_w4_shape(int32_t dtype, int64_t M, int64_t parts, int64_t N) {
   if (dtype == QP_F32)
     return mx_choose(kW4ShapesF32, sizeof(kW4ShapesF32) / sizeof(MxCost), M, parts, N);
-  // (tiles of f16 rows look over their scales first)
-  return mx_choose(kW4Shapes, sizeof(kW4Shapes) / sizeof(MxCost), M, parts, N,
-                   dtype == QP_F16 ? 4.0 : 0.0);
+  return mx_choose(kW4Shapes, sizeof(kW4Shapes) / sizeof(MxCost), M, parts, N);
 }
 
 }  // namespace qp

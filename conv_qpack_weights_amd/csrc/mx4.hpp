@@ -164,8 +164,7 @@ struct MxCost {
   double first, cold, more;
   const char* name;
 };
-const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N,
-                        double tile_first = 0.0);
+const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N);
 const MxCost& mx_a4w4_shape(int64_t M, int64_t parts, int64_t N);
 const MxCost& mx_w4_shape(int32_t dtype, int64_t M, int64_t parts, int64_t N);
 void mx_dx_kernel_name(const qp_mx4* w, int32_t dtype, int64_t M, char* name, size_t bytes);
@@ -175,6 +174,11 @@ void mx_dx_kernel_name(const qp_mx4* w, int32_t dtype, int64_t M, char* name, si
 inline bool mx_tile_reaches(const W4Rows& rows, int64_t row_bytes) {
   constexpr int64_t kMost = (INT64_C(1) << 31) - 1;
   return row_bytes <= kMost / 256 && (!rows.map || rows.x_rows <= kMost / row_bytes);
+}
+
+// Whether tiles of `tile` rows are about one a matrix, so that each reads its weights alone.
+inline bool mx_read_once(const MxArgs& a, int64_t tile) {
+  return a.rows.M <= tile * (a.rows.offsets ? a.rows.experts : 1);
 }
 
 MxMat mx_view(const qp_mx4* m);

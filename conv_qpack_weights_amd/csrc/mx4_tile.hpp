@@ -12,17 +12,18 @@ namespace {
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 // kBytes per lane from base + voff + soff straight into LDS, lane after lane from dst
-// on; offsets of `range` bytes and more ask for nothing.  (The caller waits.)
-template <int kBytes>
+// on; offsets of `range` bytes and more ask for nothing.  kOnce: data that no one reads
+// again, which the caches need not keep.  (The caller waits.)
+template <int kBytes, bool kOnce = false>
 __device__ __forceinline__ void dma_to_lds(const void* base, int range, lds_u8* dst, uint32_t voff,
                                            uint32_t soff) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __amdgpu_buffer_rsrc_t r =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, range, 0x00020000);
   if constexpr (kBytes == 16)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)dst, 16, voff, soff, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)dst, 16, voff, soff, 0, kOnce ? 2 : 0);
   else
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)dst, 4, voff, soff, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t*)dst, 4, voff, soff, 0, kOnce ? 2 : 0);
 #endif
 }
 

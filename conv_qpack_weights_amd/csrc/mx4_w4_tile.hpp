@@ -9,10 +9,11 @@
 // l/32) and converts a word for each of the stage's four steps; the rows' operand of
 // step t is piece 4 (l/32) + t of the row.  Weights are the MFMA's first operand.
 //
-// f16 rows: where a look over the scales finds that all of a workgroup's weights are
-// f16 values (mx_f16_scale), they go in as f16 and the rows as they are; else the
-// weights as bf16 and the rows as two bf16 pieces, twice the MFMAs and the cuts.
-// (Deciding stage by stage instead doubled the registers.)
+// f16 rows: the weights go in as f16 and the rows as they are; where one of a
+// workgroup's scales turns out to be out of f16's reach (mx_f16_scale) it begins
+// again, with the weights as bf16 and the rows as two bf16 pieces, twice the MFMAs and
+// the cuts.  (Deciding stage by stage instead doubled the registers; a look over all
+// scales first took 64 tokens x 2 of 16 experts of 11008 x 4096 from 110 to 122 us.)
 #pragma once
 
 #include <type_traits>
@@ -43,7 +44,7 @@ struct W4MxTile {
 // kDirect (16-bit rows at multiples of 4 bytes): the rows come by direct loads, and
 // the first operands of a stage are read behind the barrier before the last MFMAs of
 // the stage before.  Else (D = 2) through registers, where f32 is cut into pieces.
-template <typename T, bool kDirect, int BM, int BN, int WM, int WN, int D>
+template <typename T, bool kDirect, int BM, int BN, int WM, int WN, int D, bool kOnce>
 __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint32_t row_slots,
                                                                  uint32_t col_groups) {
   using L = W4MxTile<T, BM, BN, WM, WN, D>;
@@ -135,7 +136,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
   auto issue_w = [&](int c, int q) {
     const int p = (lane & 7) ^ mx_turn(wave * 8 + lrow);
     const uint32_t back = c * 8 + p < G ? 0u : p * 16u;
-    dma_to_lds<16>(wbase, c * 8 < G ? 0x7fffffff : 0,
+    dma_to_lds<16, kOnce>(wbase, c * 8 < G ? 0x7fffffff : 0,
                    wbuf + (c % L::kChunks) * L::kW + (q * (BN / 4) + wave * 8) * 128, vw[q] - back, c * 128);
   };
   auto issue_s = [&](int c) {
@@ -153,12 +154,6 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
   };
 
   f32x16 acc[FN][FM];
-#pragma unroll
-  for (int i = 0; i < FN; ++i)
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
   const int l32 = lane & 31, half = lane >> 5;
   const uint32_t sel = half ? 0x07050301u : 0x06040200u;  // the half's scale of each 64 K
@@ -265,47 +260,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
     wait_vmcnt<D == 2 ? 0 : 2 * (kA + 1) + (P < 2 ? 1 : 0)>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
-#pragma unroll
-  for (int c = 0; c < L::kAhead; ++c) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) issue_w(c, q);
-    issue_s(c);
-  }
   MxFrag<T> f[kSlots];
-  if constexpr (kDirect) {
-#pragma unroll
-    for (int s = 0; s < D - 1; ++s) issue_x(s);
-  } else if (full > 0) {
-    fetch_full(f, 0);
-    put(f, 0);
-  }
-  bool as_f16 = false;
-  if constexpr (kF16) {
-    // two threads a channel, four words each at a time
-    static_assert(BN * 2 == NW * 64, "shares");
-    const int64_t n = threadIdx.x / 2;
-    const uint8_t* const row = swbase + (n < last_n ? n : last_n) * a.w.lds;
-    uint32_t out = 0;
-#pragma unroll 4
-    for (int j = threadIdx.x % 2 * 4; j < words; j += 8) {
-      uint32_t v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = *reinterpret_cast<const uint32_t*>(row + (j + i < words ? j + i : j) * 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if ((j + i) * 4 + b < G) out |= !mx_f16_scale(mx_scale((v[i] >> (8 * b)) & 0xffu));
-    }
-    const bool fit = out == 0;
-    as_f16 = __syncthreads_and(fit);
-  }
-  wait_vmcnt<0>();
-  __syncthreads();
-  if constexpr (kDirect) issue_x(D - 1);
-  issue_w(L::kAhead, 0);
-  issue_s(L::kAhead);
   Rows even, odd;
   Weights now, next;
   auto each = [&](auto stage) {
@@ -320,66 +275,101 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
     if (s + 1 < full) stage(s + 1, P1{});
     if (s + 2 < full) stage(s + 2, P2{});
   };
-  if constexpr (kDirect) {
-    read_x(even, 0, 0);
-    read_w(now, 0);
-    // (no branch between MFMAs: the compiler would move them past it, behind the
-    // barrier)
-    auto steps = [&](int s, auto place, auto kind) {
-      read_x(odd, s, 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(even, now, 0, kind);
-      __builtin_amdgcn_sched_barrier(0);
-      read_x(even, s, 2);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(odd, now, 1, kind);
-      __builtin_amdgcn_sched_barrier(0);
-      read_x(odd, s, 3);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(even, now, 2, kind);
-      __builtin_amdgcn_sched_barrier(0);
-      arrive(place);
-      // (which first: 4096^3 by 256 x 256 tiles 106 us loads first, 103 last; 1024 x 4096 x
-      // 4096 by 128 x 128 40 and 47)
-      if constexpr (BM < 256) issue(s, place);
-      read_x(even, s + 1, 0);
-      read_w(next, s + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(odd, now, 3, kind);
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (BM >= 256) issue(s, place);
-      now = next;
+  // All whole stages; with f16 weights, whether one of the wave's was no f16 value.
+  auto pass = [&](auto kind) {
+    bool out = false;
+#pragma unroll
+    for (int c = 0; c < L::kAhead; ++c) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) issue_w(c, q);
+      issue_s(c);
+    }
+    if constexpr (kDirect) {
+#pragma unroll
+      for (int s = 0; s < D - 1; ++s) issue_x(s);
+    } else if (full > 0) {
+      fetch_full(f, 0);
+      put(f, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    wait_vmcnt<0>();
+    __syncthreads();
+    if constexpr (kDirect) issue_x(D - 1);
+    issue_w(L::kAhead, 0);
+    issue_s(L::kAhead);
+    auto look = [&] {
+      if constexpr (decltype(kind)::value)
+#pragma unroll
+        for (int i = 0; i < FN; ++i) out |= !mx_f16_scale(now.s[i]);
     };
-    if (tile.r0 + wm * 32 * FM >= tile.r1) {
-      // (a wave without rows only loads, and leaves its SIMD to the others)
+    if constexpr (kDirect) {
+      read_x(even, 0, 0);
+      read_w(now, 0);
+      // (no branch between MFMAs: the compiler would move them past it, behind the
+      // barrier)
+      auto steps = [&](int s, auto place) {
+        read_x(odd, s, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(even, now, 0, kind);
+        __builtin_amdgcn_sched_barrier(0);
+        read_x(even, s, 2);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(odd, now, 1, kind);
+        look();
+        __builtin_amdgcn_sched_barrier(0);
+        read_x(odd, s, 3);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(even, now, 2, kind);
+        __builtin_amdgcn_sched_barrier(0);
+        arrive(place);
+        // (which first: 4096^3 by 256 x 256 tiles 106 us loads first, 103 last; 1024 x 4096 x
+        // 4096 by 128 x 128 40 and 47)
+        if constexpr (BM < 256) issue(s, place);
+        read_x(even, s + 1, 0);
+        read_w(next, s + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(odd, now, 3, kind);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (BM >= 256) issue(s, place);
+        now = next;
+      };
+      if (tile.r0 + wm * 32 * FM >= tile.r1) {
+        // (a wave without rows only loads, and leaves its SIMD to the others)
+        each([&](int s, auto place) {
+          arrive(place);
+          issue(s, place);
+        });
+      } else {
+        each(steps);
+      }
+    } else {
       each([&](int s, auto place) {
+        fetch_full(f, s + 1 < full ? s + 1 : s);
+        read_w(now, s);
+        look();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          read_x(even, s, t);
+          multiply(even, now, t, kind);
+        }
+        put(f, s + 1);
         arrive(place);
         issue(s, place);
       });
-    } else if (kF16 && as_f16) {
-      each([&](int s, auto place) { steps(s, place, std::bool_constant<kF16>{}); });
-    } else {
-      each([&](int s, auto place) { steps(s, place, false_type{}); });
     }
+    wait_vmcnt<0>();
+    return out;
+  };
+  if constexpr (kF16) {
+    if (__syncthreads_or(pass(true_type{}))) pass(false_type{});
   } else {
-    auto steps = [&](int s, auto place, auto kind) {
-      fetch_full(f, s + 1 < full ? s + 1 : s);
-      read_w(now, s);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        read_x(even, s, t);
-        multiply(even, now, t, kind);
-      }
-      put(f, s + 1);
-      arrive(place);
-      issue(s, place);
-    };
-    if (kF16 && as_f16)
-      each([&](int s, auto place) { steps(s, place, std::bool_constant<kF16>{}); });
-    else
-      each([&](int s, auto place) { steps(s, place, false_type{}); });
+    pass(false_type{});
   }
-  wait_vmcnt<0>();
   __syncthreads();
   if ((int64_t)full * 64 < K) {
     // the stage that K cuts: its rows through registers, zeros from K on; zero scales
@@ -419,13 +409,13 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
                         reinterpret_cast<float*>(mx_lds) + wave * 32 * mx_out_ld(FN));
 }
 
-template <typename T, bool kDirect, int BM, int BN, int WM, int WN, int D>
+template <typename T, bool kDirect, int BM, int BN, int WM, int WN, int D, bool kOnce = false>
 qp_status mx_launch_w4_tile(const MxArgs& a, hipStream_t stream) {
   using L = W4MxTile<T, BM, BN, WM, WN, D>;
   const int64_t slots = w4_tile_slots(a.rows, BM), groups = ceil_div(a.w.rows, BN);
   QP_REQUIRE(slots * groups * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
              "qgemm_w4_mx: rows and channels for more than 2^32 threads");
-  auto kern = mx_w4_tile_kernel<T, kDirect, BM, BN, WM, WN, D>;
+  auto kern = mx_w4_tile_kernel<T, kDirect, BM, BN, WM, WN, D, kOnce>;
   if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                           hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds) != hipSuccess)
     QP_FAIL(QP_EHIP, "qgemm_w4_mx: %d bytes of LDS are not to be had", L::kLds);
@@ -451,8 +441,14 @@ qp_status mx_run_16bit(const MxArgs& a, hipStream_t stream) {
     case kMxRows16x32: return mx_launch_stream<T, 2, 4>(a, stream);
     case kMxRows16x48: return mx_launch_stream<T, 3, 4>(a, stream);
     case kMxRows16x64: return mx_launch_stream<T, 4, 4>(a, stream);
-    case kMxTile32x64: return mx_launch_w4_tile<T, true, 32, 64, 1, 2, 4>(a, stream);
-    case kMxTile32x128: return mx_launch_w4_tile<T, true, 32, 128, 1, 4, 4>(a, stream);
+    // (loads for once: 32 x 11008 x 4096 bf16 16.1 -> 15.6 us, 256 tokens x 4 of 32 experts of
+    // 4096 x 2048 70.4 -> 67.6; 128 x 4096 x 11008 31.2 -> 33.3)
+    case kMxTile32x64:
+      return mx_read_once(a, 32) ? mx_launch_w4_tile<T, true, 32, 64, 1, 2, 4, true>(a, stream)
+                                 : mx_launch_w4_tile<T, true, 32, 64, 1, 2, 4>(a, stream);
+    case kMxTile32x128:
+      return mx_read_once(a, 32) ? mx_launch_w4_tile<T, true, 32, 128, 1, 4, 4, true>(a, stream)
+                                 : mx_launch_w4_tile<T, true, 32, 128, 1, 4, 4>(a, stream);
     case kMxTile128x128: return mx_launch_w4_tile<T, true, 128, 128, 2, 2, 2>(a, stream);
     default: break;
   }
