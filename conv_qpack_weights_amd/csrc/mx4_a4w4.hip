@@ -42,14 +42,16 @@ struct A4Tile {
   static constexpr int kLds = kRing > kOut ? kRing : kOut;
 };
 
-template <int BM, int BN, int WM, int WN, int D>
+// kWide (four words of scales a row and more): a row's scales of 512 K come by one
+// lane's 16 bytes; those of the last 512 K end with the row's last word.
+template <int BM, int BN, int WM, int WN, int D, bool kWide>
 __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, uint32_t row_slots,
                                                                    uint32_t col_groups) {
   using L = A4Tile<BM, BN, WM, WN, D>;
   constexpr int NW = L::NW, FM = L::FM, FN = L::FN;
-  constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW, kSI = (BM + BN) / 16,
-                kS = (kSI + NW - 1) / NW;
-  static_assert(kA * 8 * NW == BM && kB * 8 * NW == BN && BM % 16 == 0, "shares");
+  constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW, kSRows = kWide ? 64 : 16,
+                kSI = (BM + BN) / kSRows, kS = (kSI + NW - 1) / NW;
+  static_assert(kA * 8 * NW == BM && kB * 8 * NW == BN && BM % kSRows == 0, "shares");
   extern __shared__ __attribute__((aligned(16))) uint8_t mx_lds[];
   lds_u8* const ring = (lds_u8*)mx_lds;
   lds_u8* const scales = ring + D * L::kStage;
@@ -100,16 +102,16 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
     const int64_t n = (wave * kB + j) * 8 + lrow;
     vb[j] = (uint32_t)((n < last_n ? n : last_n) * a.w.ldc) + piece(j) * 16;
   }
-  // which 16 rows' scales a wave loads (the last ones twice where they do not go round)
-  const int sdw = lane & 3;
+  // which rows' scales a wave loads (the last ones twice where they do not go round)
+  const int sdw = kWide ? 0 : lane & 3, srow = kWide ? lane : lane >> 2;
   auto scale_part = [&](int j) {
     const int i = wave * kS + j;
     return i < kSI ? i : kSI - 1;
   };
 #pragma unroll
   for (int j = 0; j < kS; ++j) {
-    const int i = scale_part(j), row = i * 16 + (lane >> 2);
-    if (i * 16 < BM) {
+    const int i = scale_part(j), row = i * kSRows + srow;
+    if (i * kSRows < BM) {
       vs[j] = (uint32_t)(source(row) * a.a.lds) + sdw * 4;
     } else {
       const int64_t n = row - BM;
@@ -123,6 +125,8 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   // for nothing: its buffers' range is empty, so that every round of the loop has the
   // same loads to wait for.
   const int G = (int)a.w.G, full = G / 8, stages = (G + 7) / 8, words = (G + 3) / 4;
+  const int over = (words + 3) / 4 * 16 - words * 4;  // bytes that the last 512 K lack
+  auto late = [&](int s) { return kWide && (s >> 1) * 4 + 4 > words ? over : 0; };
   auto issue = [&](int s, auto with_scales) {
     lds_u8* const to = ring + (s % D) * L::kStage;
     const int range = s < stages ? 0x7fffffff : 0;
@@ -137,12 +141,12 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
                      s * 128);
     if constexpr (decltype(with_scales)::value) {
       lds_u8* const st = scales + ((s >> 1) % L::kSpans) * L::kScales;
-      const uint32_t sback = s * 2 + sdw < words ? 0u : sdw * 4u;
+      const uint32_t sback = kWide || s * 2 + sdw < words ? 0u : sdw * 4u;
 #pragma unroll
       for (int j = 0; j < kS; ++j) {
         const int i = scale_part(j);
-        dma_to_lds<4>(i * 16 < BM ? sabase : swbase, range, st + i * 256, vs[j] - sback,
-                      s * 8);
+        dma_to_lds<kWide ? 16 : 4>(i * kSRows < BM ? sabase : swbase, range,
+                                   st + i * kSRows * 16, vs[j] - sback, s * 8 - late(s));
       }
     }
   };
@@ -182,7 +186,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   };
   auto read_scales = [&](Scales& o, int s) {
     const lds_u8* const st =
-        scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8;
+        scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8 + late(s);
 #pragma unroll
     for (int j = 0; j < FM; ++j) o.a[j] = mine(st + (arow + j * 32) * 16);
 #pragma unroll
@@ -277,7 +281,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
     const int left = G - s * 8;
     if (left < 8) {
       lds_u8* const to = ring + (s % D) * L::kStage;
-      lds_u8* const st = scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8;
+      lds_u8* const st = scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8 + late(s);
       for (int i = threadIdx.x; i < (BM + BN) * 8; i += NW * 64) {
         if (((i & 7) ^ mx_turn(i >> 3)) >= left)
           *(__attribute__((address_space(3))) u32x4*)(to + i * 16) = u32x4{0, 0, 0, 0};
@@ -301,19 +305,25 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
                         reinterpret_cast<float*>(mx_lds) + wave * 32 * L::kOutLd);
 }
 
-template <int BM, int BN, int WM, int WN, int D>
-qp_status launch_tile(const MxArgs& a, hipStream_t stream) {
+template <int BM, int BN, int WM, int WN, int D, bool kWide>
+qp_status launch_tile_of(const MxArgs& a, hipStream_t stream) {
   using L = A4Tile<BM, BN, WM, WN, D>;
   const int64_t slots = w4_tile_slots(a.rows, BM), groups = ceil_div(a.w.rows, BN);
   QP_REQUIRE(slots * groups * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
              "qgemm_a4w4_mx: rows and channels for more than 2^32 threads");
-  auto kern = mx_a4w4_tile_kernel<BM, BN, WM, WN, D>;
+  auto kern = mx_a4w4_tile_kernel<BM, BN, WM, WN, D, kWide>;
   if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                           hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds) != hipSuccess)
     QP_FAIL(QP_EHIP, "qgemm_a4w4_mx: %d bytes of LDS are not to be had", L::kLds);
   hipLaunchKernelGGL(kern, dim3((unsigned)(slots * groups)), dim3(L::NW * 64), L::kLds, stream, a,
                      (uint32_t)slots, (uint32_t)groups);
   return check_launch("qgemm_a4w4_mx (many rows)");
+}
+
+template <int BM, int BN, int WM, int WN, int D>
+qp_status launch_tile(const MxArgs& a, hipStream_t stream) {
+  return a.w.G > 12 ? launch_tile_of<BM, BN, WM, WN, D, true>(a, stream)
+                    : launch_tile_of<BM, BN, WM, WN, D, false>(a, stream);
 }
 
 // Which kernel (MxCost, mx_choose).  Measured, cold weights: e.g. 16 x 4096 rows of 16 / 32

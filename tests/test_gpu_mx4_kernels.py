@@ -260,3 +260,24 @@ def test_values_below_the_normal_range(qp):
             off = (qp.qgemm_w4_mx(X, W, out_dtype=torch.float32).double()
                    - x @ w.t().contiguous()).abs()
             assert (off <= (3 * K / 32 + 64) * 2.0 ** -23 * A + slack).all(), (dtype, M)
+
+
+@pytest.mark.parametrize("kernel,M,N", [("tile64x64", 250, 4010), ("tile128x128", 1100, 4010),
+                                        ("tile256x256", 4090, 4090)])
+def test_tiles_at_every_end_of_a_rows_scales(qp, kernel, M, N):
+    """One to sixteen words of scales a row, whole and cut ones, rows apart and not."""
+    import torch
+    g = torch.Generator().manual_seed(M)
+    for K in (385, 416, 512, 520, 640, 770, 900, 1024, 1060, 1290, 1660):
+        if M * N > 8e6 and K not in (385, 640, 770, 1290):
+            continue
+        print("mx4 scales' end", kernel, M, N, K, flush=True)
+        W, w = _matrix(qp, g, N, K)
+        A, a = _matrix(qp, g, M, K)
+        assert qp.qgemm_mx_kernel_name("a4w4", M, W, torch.float32) == kernel
+        want, size = a @ w.t().contiguous(), a.abs() @ w.abs().t().contiguous()
+        _close(qp.qgemm_a4w4_mx(A, W), want, size, K, "f32", "K=%d" % K)
+        G = W.scales.shape[-1]
+        apart = torch.full((M, -(-G // 4) * 4 + 8), 255, dtype=torch.uint8, device="cuda")[:, :G]
+        B = qp.mx4_tensor(A.codes, apart.copy_(A.scales), K)
+        _close(qp.qgemm_a4w4_mx(B, W), want, size, K, "f32", "K=%d apart" % K)
