@@ -57,7 +57,7 @@ constexpr MxCost kW4Shapes[] = {
     {kMxTile32x64, 32, 64, 15.7, 11.0, 6.5, "tile32x64"},
     {kMxTile32x128, 32, 128, 19.8, 20.0, 14.0, "tile32x128"},
     {kMxTile128x128, 128, 128, 35.0, 29.0, 30.0, "tile128x128"},
-    {kMxTile256x256, 256, 256, 90.0, 105.0, 105.0, "tile256x256"},
+    {kMxTile256x256, 256, 256, 103.0, 100.0, 100.0, "tile256x256"},
 };
 // The same of f32 rows: 16 x 4096 14.1, 14.8, 15.4, 16.6; 16 x 11008 38, 34, 19.6, 20.8; 64 x
 // 11008 112, 84, 58, 52, 128 x 128 tiles 125; 128 x 4096 78, 56, 40, 33, 121; 4096 x 4096 tiles 510.
@@ -70,6 +70,12 @@ constexpr MxCost kW4ShapesF32[] = {
 };
 
 }  // namespace
+
+// Rounds of tiles one to a CU, the last one in halves where it is half empty.
+double mx_halved_rounds(double rounds) {
+  const double whole = (double)(int64_t)rounds, last = rounds - whole;
+  return rounds <= 1.0 || last == 0.0 ? rounds : whole + (last <= 0.5 ? 0.6 : 1.0);
+}
 
 const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N) {
   const double experts = (double)(parts < M ? parts : M);
@@ -88,9 +94,12 @@ const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, i
     const bool tile = s->shape >= kMxTile32x64;
     // (experts of unlike sizes have more tiles than that)
     if (tile && experts > 1.0) rounds *= 1.1;
-    if (!tile || (s->shape == kMxTile256x256 && rounds > 1.0)) {
+    if (!tile) {
       rounds = (double)(int64_t)(rounds + 255.0 / 256.0);
       own = (double)(int64_t)(own + 255.0 / 256.0);
+    } else if (s->shape == kMxTile256x256) {
+      rounds = mx_halved_rounds(rounds);
+      own = mx_halved_rounds(own);
     }
     own = own < 1.0 ? 1.0 : own;
     const double cost = s->first + s->cold * (own - 1.0) +

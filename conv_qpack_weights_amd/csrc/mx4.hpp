@@ -164,6 +164,7 @@ struct MxCost {
   double first, cold, more;
   const char* name;
 };
+double mx_halved_rounds(double rounds);
 const MxCost& mx_choose(const MxCost* shapes, int n, int64_t M, int64_t parts, int64_t N);
 const MxCost& mx_a4w4_shape(int64_t M, int64_t parts, int64_t N);
 const MxCost& mx_w4_shape(int32_t dtype, int64_t M, int64_t parts, int64_t N);

@@ -59,12 +59,11 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
 
-  uint32_t slot, group;
-  mx_place(row_slots, col_groups, slot, group);
+  W4Tile tile;
+  uint32_t group;
+  if (!mx_take_tile<BM, (BM >= 256)>(a.rows, row_slots, col_groups, tile, group)) return;
   const int64_t n0 = (int64_t)group * BN;
   const int64_t N = a.w.rows;
-  const W4Tile tile = w4_find_tile<BM>(a.rows, slot);
-  if (tile.expert < 0) return;
   if (a.rows.offsets && tile.expert == a.rows.experts) {  // rows of no expert
     for (int64_t r = tile.r0 + wave; r < tile.r1; r += NW)
       for (int64_t n = n0 + lane; n < n0 + BN && n < N; n += 64)
@@ -151,171 +150,183 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
     }
   };
 
-  f32x16 acc[FN][FM];
-#pragma unroll
-  for (int i = 0; i < FN; ++i)
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-
-  const int l32 = lane & 31, half = lane >> 5;
-  const uint32_t sel = half ? 0x07050301u : 0x06040200u;  // the half's scale of each 64 K
-  auto mine = [&](const lds_u8* at) {
-    const u32x2 v = *(const __attribute__((address_space(3))) u32x2*)at;
-    return __builtin_amdgcn_perm(v.y, v.x, sel);
-  };
-  const int arow = wm * 32 * FM + l32, brow = wn * 32 * FN + l32;
-  struct Operands {
-    u32x4 x[FM], w[FN];
-  };
-  struct Scales {
-    uint32_t a[FM], w[FN];
-  };
-  auto read = [&](Operands& o, int s, int step) {
-    const lds_u8* const from = ring + (s % D) * L::kStage;
-    const int at = ((2 * step + half) ^ mx_turn(l32)) * 16;
+  // F x FN operands a wave
+  auto run = [&](auto operands) {
+    constexpr int F = decltype(operands)::value;
+    f32x16 acc[FN][F];
 #pragma unroll
     for (int i = 0; i < FN; ++i)
-      o.w[i] = *(const __attribute__((address_space(3))) u32x4*)(
-          from + (BM + brow + i * 32) * 128 + at);
 #pragma unroll
-    for (int j = 0; j < FM; ++j)
-      o.x[j] = *(const __attribute__((address_space(3))) u32x4*)(
-          from + (arow + j * 32) * 128 + at);
-  };
-  auto read_scales = [&](Scales& o, int s) {
-    const lds_u8* const st =
-        scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8 + late(s);
+      for (int j = 0; j < F; ++j)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) o.a[j] = mine(st + (arow + j * 32) * 16);
-#pragma unroll
-    for (int i = 0; i < FN; ++i) o.w[i] = mine(st + (BM + brow + i * 32) * 16);
-  };
-  auto multiply = [&](auto which, const Operands& o, const Scales& c) {
-    constexpr int S = decltype(which)::value;
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    const int l32 = lane & 31, half = lane >> 5;
+    const uint32_t sel = half ? 0x07050301u : 0x06040200u;  // the half's scale of each 64 K
+    auto mine = [&](const lds_u8* at) {
+      const u32x2 v = *(const __attribute__((address_space(3))) u32x2*)at;
+      return __builtin_amdgcn_perm(v.y, v.x, sel);
+    };
+    const int arow = wm * 32 * F + l32, brow = wn * 32 * FN + l32;
+    struct Operands {
+      u32x4 x[F], w[FN];
+    };
+    struct Scales {
+      uint32_t a[F], w[FN];
+    };
+    auto read = [&](Operands& o, int s, int step) {
+      const lds_u8* const from = ring + (s % D) * L::kStage;
+      const int at = ((2 * step + half) ^ mx_turn(l32)) * 16;
 #pragma unroll
       for (int i = 0; i < FN; ++i)
-        acc[i][j] = mx_mfma32<S>(o.w[i], c.w[i], o.x[j], c.a[j], acc[i][j]);
-  };
-  using S0 = std::integral_constant<int, 0>;
-  using S1 = std::integral_constant<int, 1>;
-  using S2 = std::integral_constant<int, 2>;
-  using S3 = std::integral_constant<int, 3>;
-  using std::false_type;
-  using std::true_type;
-
-  // The next stage is in LDS for everyone (all loads but those of the D - 2 stages
-  // after it are done; of two stages running one brings scales), and everyone has
-  // read all of this one, whose buffer is filled next.
-  constexpr int kAllowed = (D - 2) * (kA + kB) + (D - 2) / 2 * kS;
-  static_assert((D == 2 || D == 4) && kAllowed < 64, "vmcnt range");
-  auto arrive = [&]() {
-    wait_vmcnt<kAllowed>();
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  };
-  issue(0, true_type{});
+        o.w[i] = *(const __attribute__((address_space(3))) u32x4*)(
+            from + (BM + brow + i * 32) * 128 + at);
 #pragma unroll
-  for (int s = 1; s < D - 1; ++s) {
-    if (s & 1)
-      issue(s, false_type{});
-    else
-      issue(s, true_type{});
-  }
-  arrive();
-  issue(D - 1, false_type{});
-  Operands even, odd;
-  Scales now, next;
-  read(even, 0, 0);
-  read_scales(now, 0);
-  // (no branch in the loop: the compiler would move the MFMAs past it, behind the
-  // barrier)
-  auto stage = [&](int s, auto with_scales) {
-    read(odd, s, 1);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(S0{}, even, now);
-    __builtin_amdgcn_sched_barrier(0);
-    read(even, s, 2);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(S1{}, odd, now);
-    __builtin_amdgcn_sched_barrier(0);
-    read(odd, s, 3);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(S2{}, even, now);
-    __builtin_amdgcn_sched_barrier(0);
-    arrive();
-    // (loads first: behind the MFMAs they made 8192^3 2% faster, but 4096 tokens x 2 of 8
-    // experts and 1024 x 4096 x 4096 4% slower)
-    issue(s + D, with_scales);
-    read(even, s + 1, 0);
-    read_scales(next, s + 1);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(S3{}, odd, now);
-    __builtin_amdgcn_sched_barrier(0);
-    now = next;
-  };
-  const int pairs = full / 2;
-  if (tile.r0 + wm * 32 * FM < tile.r1) {
-    for (int t = 0; t < pairs; ++t) {
-      stage(2 * t, true_type{});
-      stage(2 * t + 1, false_type{});
-    }
-  } else {
-    // (a wave without rows only loads, and leaves its SIMD to the others)
-    for (int t = 0; t < pairs; ++t) {
-      arrive();
-      issue(2 * t + D, true_type{});
-      arrive();
-      issue(2 * t + 1 + D, false_type{});
-    }
-  }
-  wait_vmcnt<0>();
-  __syncthreads();
-  // a last odd stage, and the one that K cuts: zero codes and scales past the last
-  // block (all their loads are done: at most two stages are left, and D were under
-  // way)
-#pragma unroll 1
-  for (int s = 2 * pairs; s < stages; ++s) {
-    const int left = G - s * 8;
-    if (left < 8) {
-      lds_u8* const to = ring + (s % D) * L::kStage;
-      lds_u8* const st = scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8 + late(s);
-      for (int i = threadIdx.x; i < (BM + BN) * 8; i += NW * 64) {
-        if (((i & 7) ^ mx_turn(i >> 3)) >= left)
-          *(__attribute__((address_space(3))) u32x4*)(to + i * 16) = u32x4{0, 0, 0, 0};
-        if ((i & 7) >= left) st[(i >> 3) * 16 + (i & 7)] = 0;
-      }
-      __syncthreads();
-    }
-    read_scales(now, s);
-    read(even, s, 0);
-    multiply(S0{}, even, now);
-    read(even, s, 1);
-    multiply(S1{}, even, now);
-    read(even, s, 2);
-    multiply(S2{}, even, now);
-    read(even, s, 3);
-    multiply(S3{}, even, now);
-  }
-  __syncthreads();
+      for (int j = 0; j < F; ++j)
+        o.x[j] = *(const __attribute__((address_space(3))) u32x4*)(
+            from + (arow + j * 32) * 128 + at);
+    };
+    auto read_scales = [&](Scales& o, int s) {
+      const lds_u8* const st =
+          scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8 + late(s);
+#pragma unroll
+      for (int j = 0; j < F; ++j) o.a[j] = mine(st + (arow + j * 32) * 16);
+#pragma unroll
+      for (int i = 0; i < FN; ++i) o.w[i] = mine(st + (BM + brow + i * 32) * 16);
+    };
+    auto multiply = [&](auto which, const Operands& o, const Scales& c) {
+      constexpr int S = decltype(which)::value;
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+          acc[i][j] = mx_mfma32<S>(o.w[i], c.w[i], o.x[j], c.a[j], acc[i][j]);
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    using S2 = std::integral_constant<int, 2>;
+    using S3 = std::integral_constant<int, 3>;
+    using std::false_type;
+    using std::true_type;
 
-  mx_store_tile<FM, FN>(acc, a, tile, wm * FM * 32, n0 + wn * FN * 32,
-                        reinterpret_cast<float*>(mx_lds) + wave * 32 * L::kOutLd);
+    // The next stage is in LDS for everyone (all loads but those of the D - 2 stages
+    // after it are done; of two stages running one brings scales), and everyone has
+    // read all of this one, whose buffer is filled next.
+    constexpr int kAllowed = (D - 2) * (kA + kB) + (D - 2) / 2 * kS;
+    static_assert((D == 2 || D == 4) && kAllowed < 64, "vmcnt range");
+    auto arrive = [&]() {
+      wait_vmcnt<kAllowed>();
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+    issue(0, true_type{});
+#pragma unroll
+    for (int s = 1; s < D - 1; ++s) {
+      if (s & 1)
+        issue(s, false_type{});
+      else
+        issue(s, true_type{});
+    }
+    arrive();
+    issue(D - 1, false_type{});
+    Operands even, odd;
+    Scales now, next;
+    read(even, 0, 0);
+    read_scales(now, 0);
+    // (no branch in the loop: the compiler would move the MFMAs past it, behind the
+    // barrier)
+    auto stage = [&](int s, auto with_scales) {
+      read(odd, s, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(S0{}, even, now);
+      __builtin_amdgcn_sched_barrier(0);
+      read(even, s, 2);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(S1{}, odd, now);
+      __builtin_amdgcn_sched_barrier(0);
+      read(odd, s, 3);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(S2{}, even, now);
+      __builtin_amdgcn_sched_barrier(0);
+      arrive();
+      // (loads first: behind the MFMAs they made 8192^3 2% faster, but 4096 tokens x 2 of 8
+      // experts and 1024 x 4096 x 4096 4% slower)
+      issue(s + D, with_scales);
+      read(even, s + 1, 0);
+      read_scales(next, s + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(S3{}, odd, now);
+      __builtin_amdgcn_sched_barrier(0);
+      now = next;
+    };
+    const int pairs = full / 2;
+    if (tile.r0 + wm * 32 * F < tile.r1) {
+      for (int t = 0; t < pairs; ++t) {
+        stage(2 * t, true_type{});
+        stage(2 * t + 1, false_type{});
+      }
+    } else {
+      // (a wave without rows only loads, and leaves its SIMD to the others)
+      for (int t = 0; t < pairs; ++t) {
+        arrive();
+        issue(2 * t + D, true_type{});
+        arrive();
+        issue(2 * t + 1 + D, false_type{});
+      }
+    }
+    wait_vmcnt<0>();
+    __syncthreads();
+    // a last odd stage, and the one that K cuts: zero codes and scales past the last
+    // block (all their loads are done: at most two stages are left, and D were under
+    // way)
+#pragma unroll 1
+    for (int s = 2 * pairs; s < stages; ++s) {
+      const int left = G - s * 8;
+      if (left < 8) {
+        lds_u8* const to = ring + (s % D) * L::kStage;
+        lds_u8* const st = scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8 + late(s);
+        for (int i = threadIdx.x; i < (BM + BN) * 8; i += NW * 64) {
+          if (((i & 7) ^ mx_turn(i >> 3)) >= left)
+            *(__attribute__((address_space(3))) u32x4*)(to + i * 16) = u32x4{0, 0, 0, 0};
+          if ((i & 7) >= left) st[(i >> 3) * 16 + (i & 7)] = 0;
+        }
+        __syncthreads();
+      }
+      read_scales(now, s);
+      read(even, s, 0);
+      multiply(S0{}, even, now);
+      read(even, s, 1);
+      multiply(S1{}, even, now);
+      read(even, s, 2);
+      multiply(S2{}, even, now);
+      read(even, s, 3);
+      multiply(S3{}, even, now);
+    }
+    __syncthreads();
+
+    mx_store_tile<F, FN>(acc, a, tile, wm * F * 32, n0 + wn * FN * 32,
+                          reinterpret_cast<float*>(mx_lds) + wave * 32 * L::kOutLd);
+  };
+  // (half the rows, half the operands: half a tile takes 0.53 of a whole one's time,
+  // with one wave of two at work on all of a wave's operands instead about 0.6)
+  constexpr int kHalf = FM > 1 ? FM / 2 : FM;
+  if (kHalf < FM && tile.r1 - tile.r0 <= BM / 2)
+    run(std::integral_constant<int, kHalf>{});
+  else
+    run(std::integral_constant<int, FM>{});
 }
 
 template <int BM, int BN, int WM, int WN, int D, bool kWide>
 qp_status launch_tile_of(const MxArgs& a, hipStream_t stream) {
   using L = A4Tile<BM, BN, WM, WN, D>;
   const int64_t slots = w4_tile_slots(a.rows, BM), groups = ceil_div(a.w.rows, BN);
-  QP_REQUIRE(slots * groups * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
+  const int64_t grid = mx_tile_grid(slots, groups, BM >= 256);
+  QP_REQUIRE(grid * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
              "qgemm_a4w4_mx: rows and channels for more than 2^32 threads");
   auto kern = mx_a4w4_tile_kernel<BM, BN, WM, WN, D, kWide>;
   if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                           hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds) != hipSuccess)
     QP_FAIL(QP_EHIP, "qgemm_a4w4_mx: %d bytes of LDS are not to be had", L::kLds);
-  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * groups)), dim3(L::NW * 64), L::kLds, stream, a,
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(L::NW * 64), L::kLds, stream, a,
                      (uint32_t)slots, (uint32_t)groups);
   return check_launch("qgemm_a4w4_mx (many rows)");
 }
@@ -335,7 +346,7 @@ constexpr MxCost kA4Shapes[] = {
     {kMxRows16x32, 16, 32, 5.6, 4.1, 1.9, "rows16x32"},
     {kMxTile64x64, 64, 64, 8.1, 10.0, 4.4, "tile64x64"},
     {kMxTile128x128, 128, 128, 19.0, 26.0, 11.5, "tile128x128"},
-    {kMxTile256x256, 256, 256, 35.0, 37.0, 37.0, "tile256x256"},
+    {kMxTile256x256, 256, 256, 44.0, 40.0, 40.0, "tile256x256"},
 };
 
 }  // namespace

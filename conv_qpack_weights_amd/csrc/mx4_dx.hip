@@ -189,7 +189,7 @@ __global__ __launch_bounds__(256) void mx_dx_sum_kernel(const float* __restrict_
 // bytes, to the other of two buffers, so that every weight is converted once in a
 // workgroup.  In that buffer column 4u + j of a wave's 64 is row 16 j + u: 16 threads
 // then write 16 rows, whose places meet every bank alike (mx_turn).
-// f16 rows: as there, with f16 weights where a look over the scales allows it.
+// f16 rows: as there, again from the start where a weight turns out to be no f16 value.
 template <typename T, int BM, int BC, int WM, int WN>
 struct MxDxTile {
   static constexpr int NW = WM * WN, FM = BM / (32 * WM);
@@ -221,12 +221,11 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
 
-  uint32_t slot, group;
-  mx_place(row_slots, col_groups, slot, group);
+  W4Tile tile;
+  uint32_t group;
+  if (!mx_take_tile<BM, (BM >= 256)>(a.rows, row_slots, col_groups, tile, group)) return;
   const int64_t k0 = (int64_t)group * BC;
   const int64_t N = a.w.rows, K = a.w.K;
-  const W4Tile tile = w4_find_tile<BM>(a.rows, slot);
-  if (tile.expert < 0) return;
   if (a.rows.offsets && tile.expert == a.rows.experts) {  // rows of no expert
     for (int64_t r = tile.r0 + wave; r < tile.r1; r += NW)
       for (int64_t k = k0 + lane; k < k0 + BC && k < K; k += 64)
@@ -316,24 +315,29 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
       w.s[i] = sc[i * kPieces];
     }
   };
-  // the stage that N cuts: channels past the last have zero scales (what is found
+  // the stage that N cuts: channels past the last are zeros of scale 1 (what is found
   // there could be a NaN)
   auto load_w_cut = [&](Raw& w) {
     const bool in = u / 8 < blocks;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t n = (int64_t)full * 64 + g * 8 + i, at = n < N ? n : N - 1;
-      w.q[i] = *reinterpret_cast<const uint16_t*>(codes + at * a.w.ldc + (in ? 2 * u : 0));
+      const uint32_t q = *reinterpret_cast<const uint16_t*>(codes + at * a.w.ldc + (in ? 2 * u : 0));
       const uint32_t v = scales[at * a.w.lds + (in ? u / 8 : 0)];
-      w.s[i] = n < N ? v : 0u;
+      w.q[i] = n < N ? q : 0u;
+      w.s[i] = n < N ? v : 127u;
     }
   };
-  auto convert = [&](const Raw& w, int s, auto kind) {
+  // (there: whether this is a stage at all; f16 weights: `out` is set where one is no
+  // f16 value)
+  bool out = false;
+  auto convert = [&](const Raw& w, int s, auto kind, bool there) {
     uint32_t c[8][2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float by = mx_scale(w.s[i]);
       if constexpr (decltype(kind)::value) {
+        out |= there && !mx_f16_scale(by);
         c[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 0));
         c[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 1));
       } else {
@@ -354,229 +358,225 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
     }
   };
 
-  f32x16 acc[FN][FM];
-#pragma unroll
-  for (int i = 0; i < FN; ++i)
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  // F x FN operands a wave
+  auto run = [&](auto operands) {
+    constexpr int F = decltype(operands)::value;
+    f32x16 acc[FN][F];
 
-  const int l32 = lane & 31, half = lane >> 5;
-  const int arow = wm * 32 * FM + l32, brow = wn * 64 + l32;
-  struct Operands {
-    u32x4 x[FM][NP], w[FN];
-  };
-  // 16 channels a step: lane l holds eight of row l%32 from 8 (l/32) on
-  auto read = [&](Operands& o, int s, int step) {
-    const lds_u8* const fx = xbuf + (s & 1) * L::kX;
-    const lds_u8* const fw = wbuf + (s & 1) * L::kW;
-    const int at = ((2 * step + half) ^ mx_turn(l32)) * 16;
+    const int l32 = lane & 31, half = lane >> 5;
+    const int arow = wm * 32 * F + l32, brow = wn * 64 + l32;
+    struct Operands {
+      u32x4 x[F][NP], w[FN];
+    };
+    // 16 channels a step: lane l holds eight of row l%32 from 8 (l/32) on
+    auto read = [&](Operands& o, int s, int step) {
+      const lds_u8* const fx = xbuf + (s & 1) * L::kX;
+      const lds_u8* const fw = wbuf + (s & 1) * L::kW;
+      const int at = ((2 * step + half) ^ mx_turn(l32)) * 16;
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
-      o.w[i] = *(const __attribute__((address_space(3))) u32x4*)(fw + (brow + i * 32) * 128 + at);
+      for (int i = 0; i < FN; ++i)
+        o.w[i] = *(const __attribute__((address_space(3))) u32x4*)(fw + (brow + i * 32) * 128 + at);
 #pragma unroll
-    for (int j = 0; j < FM; ++j)
+      for (int j = 0; j < F; ++j)
 #pragma unroll
-      for (int n = 0; n < NP; ++n)
-        o.x[j][n] = *(const __attribute__((address_space(3))) u32x4*)(
-            fx + (n * BM + arow + j * 32) * 128 + at);
-  };
-  auto multiply = [&](const Operands& o, auto kind) {
-    constexpr bool kAsF16 = decltype(kind)::value;
-    constexpr int kPieces = kF16 && !kAsF16 ? 2 : NP;
+        for (int n = 0; n < NP; ++n)
+          o.x[j][n] = *(const __attribute__((address_space(3))) u32x4*)(
+              fx + (n * BM + arow + j * 32) * 128 + at);
+    };
+    auto multiply = [&](const Operands& o, auto kind) {
+      constexpr bool kAsF16 = decltype(kind)::value;
+      constexpr int kPieces = kF16 && !kAsF16 ? 2 : NP;
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-      if constexpr (kAsF16) {
+      for (int j = 0; j < F; ++j) {
+        if constexpr (kAsF16) {
 #pragma unroll
-        for (int i = 0; i < FN; ++i)
-          acc[i][j] = mx_mfma_f16(__builtin_bit_cast(f16x8, o.w[i]),
-                                  __builtin_bit_cast(f16x8, o.x[j][0]), acc[i][j]);
-      } else {
-        bf16x8 xv[kPieces];
-        if constexpr (kF16)
-          MxFrag<f16_t>{o.x[j][0]}.split(xv);
-        else
+          for (int i = 0; i < FN; ++i)
+            acc[i][j] = mx_mfma_f16(__builtin_bit_cast(f16x8, o.w[i]),
+                                    __builtin_bit_cast(f16x8, o.x[j][0]), acc[i][j]);
+        } else {
+          bf16x8 xv[kPieces];
+          if constexpr (kF16)
+            MxFrag<f16_t>{o.x[j][0]}.split(xv);
+          else
 #pragma unroll
-          for (int n = 0; n < NP; ++n) xv[n] = __builtin_bit_cast(bf16x8, o.x[j][n]);
+            for (int n = 0; n < NP; ++n) xv[n] = __builtin_bit_cast(bf16x8, o.x[j][n]);
 #pragma unroll
-        for (int i = 0; i < FN; ++i)
+          for (int i = 0; i < FN; ++i)
 #pragma unroll
-          for (int n = 0; n < kPieces; ++n)
-            acc[i][j] = mx_mfma_bf16(__builtin_bit_cast(bf16x8, o.w[i]), xv[n], acc[i][j]);
+            for (int n = 0; n < kPieces; ++n)
+              acc[i][j] = mx_mfma_bf16(__builtin_bit_cast(bf16x8, o.w[i]), xv[n], acc[i][j]);
+        }
       }
-    }
-  };
+    };
 
-  using std::false_type;
-  using std::true_type;
-  // everyone's share of the next stage is there, and everyone has read all of this one
-  auto arrive = [&]() {
-    wait_vmcnt<0>();
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  };
-  auto run = [&](auto kind) {
-    Raw raw;
-    MxFrag<T> f[kA];
-    Operands even, odd;
-    if (full > 0) {
-      issue_w(0);
-      issue_w(1);
-      if constexpr (kDirect) {
-        issue_x(0);
-      } else {
-        fetch_full(f, 0);
+    using std::false_type;
+    using std::true_type;
+    // everyone's share of the next stage is there, and everyone has read all of this one
+    auto arrive = [&]() {
+      wait_vmcnt<0>();
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+    auto all = [&](auto kind) {
 #pragma unroll
-        for (int j = 0; j < kA; ++j) put(f[j], 0, j);
-      }
-      arrive();
-      read_w(raw, 0);
-      convert(raw, 0, kind);
-      arrive();
-      issue_w(2);
-      if constexpr (kDirect) {
-        issue_x(1);
-        read(even, 0, 0);
-        // (no branch between MFMAs, as in the products)
-        if (tile.r0 + wm * 32 * FM < tile.r1) {
-          for (int s = 0; s < full; ++s) {
-            read(odd, s, 1);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(even, kind);
-            __builtin_amdgcn_sched_barrier(0);
-            read(even, s, 2);
-            read_w(raw, s + 1);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(odd, kind);
-            __builtin_amdgcn_sched_barrier(0);
-            read(odd, s, 3);
-            __builtin_amdgcn_sched_barrier(0);
-            convert(raw, s + 1, kind);
-            multiply(even, kind);
-            __builtin_amdgcn_sched_barrier(0);
-            arrive();
-            issue_w(s + 3);
-            issue_x(s + 2);
-            read(even, s + 1, 0);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(odd, kind);
-            __builtin_amdgcn_sched_barrier(0);
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+      Raw raw;
+      MxFrag<T> f[kA];
+      Operands even, odd;
+      if (full > 0) {
+        issue_w(0);
+        issue_w(1);
+        if constexpr (kDirect) {
+          issue_x(0);
+        } else {
+          fetch_full(f, 0);
+#pragma unroll
+          for (int j = 0; j < kA; ++j) put(f[j], 0, j);
+        }
+        arrive();
+        read_w(raw, 0);
+        convert(raw, 0, kind, true);
+        arrive();
+        issue_w(2);
+        if constexpr (kDirect) {
+          issue_x(1);
+          read(even, 0, 0);
+          // (no branch between MFMAs, as in the products)
+          if (tile.r0 + wm * 32 * F < tile.r1) {
+            for (int s = 0; s < full; ++s) {
+              read(odd, s, 1);
+              __builtin_amdgcn_sched_barrier(0);
+              multiply(even, kind);
+              __builtin_amdgcn_sched_barrier(0);
+              read(even, s, 2);
+              read_w(raw, s + 1);
+              __builtin_amdgcn_sched_barrier(0);
+              multiply(odd, kind);
+              __builtin_amdgcn_sched_barrier(0);
+              read(odd, s, 3);
+              __builtin_amdgcn_sched_barrier(0);
+              convert(raw, s + 1, kind, s + 1 < full);
+              multiply(even, kind);
+              __builtin_amdgcn_sched_barrier(0);
+              arrive();
+              issue_w(s + 3);
+              issue_x(s + 2);
+              read(even, s + 1, 0);
+              __builtin_amdgcn_sched_barrier(0);
+              multiply(odd, kind);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          } else {
+            // (a wave without rows only brings its share of the weights)
+            for (int s = 0; s < full; ++s) {
+              read_w(raw, s + 1);
+              convert(raw, s + 1, kind, s + 1 < full);
+              arrive();
+              issue_w(s + 3);
+              issue_x(s + 2);
+            }
           }
         } else {
-          // (a wave without rows only brings its share of the weights)
           for (int s = 0; s < full; ++s) {
+            fetch_full(f, s + 1 < full ? s + 1 : s);
             read_w(raw, s + 1);
-            convert(raw, s + 1, kind);
+            convert(raw, s + 1, kind, s + 1 < full);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              read(even, s, t);
+              multiply(even, kind);
+            }
+#pragma unroll
+            for (int j = 0; j < kA; ++j) put(f[j], s + 1, j);
             arrive();
             issue_w(s + 3);
-            issue_x(s + 2);
           }
-        }
-      } else {
-        for (int s = 0; s < full; ++s) {
-          fetch_full(f, s + 1 < full ? s + 1 : s);
-          read_w(raw, s + 1);
-          convert(raw, s + 1, kind);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            read(even, s, t);
-            multiply(even, kind);
-          }
-#pragma unroll
-          for (int j = 0; j < kA; ++j) put(f[j], s + 1, j);
-          arrive();
-          issue_w(s + 3);
         }
       }
-    }
-    wait_vmcnt<0>();
-    __syncthreads();
-    if ((int64_t)full * 64 < N) {
-      // the stage that N cuts: its rows through registers, zeros from N on
-      load_w_cut(raw);
-      convert(raw, full, kind);
+      wait_vmcnt<0>();
+      __syncthreads();
+      if ((int64_t)full * 64 < N) {
+        // the stage that N cuts: its rows through registers, zeros from N on
+        load_w_cut(raw);
+        convert(raw, full, kind, true);
 #pragma unroll 1
-      for (int j = 0; j < kA; ++j) {
-        const int64_t n = (int64_t)full * 64 + piece(j) * 8, left = N - n;
-        const T* p = xbase + row_of(j);
-        MxFrag<T> one;
-        one.load_n(p + (left > 0 ? n : 0), left > 8 ? 8 : left < 0 ? 0 : (int)left);
-        put(one, full, j);
-      }
-      __syncthreads();
+        for (int j = 0; j < kA; ++j) {
+          const int64_t n = (int64_t)full * 64 + piece(j) * 8, left = N - n;
+          const T* p = xbase + row_of(j);
+          MxFrag<T> one;
+          one.load_n(p + (left > 0 ? n : 0), left > 8 ? 8 : left < 0 ? 0 : (int)left);
+          put(one, full, j);
+        }
+        __syncthreads();
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        read(even, full, t);
-        multiply(even, kind);
+        for (int t = 0; t < 4; ++t) {
+          read(even, full, t);
+          multiply(even, kind);
+        }
+        __syncthreads();
       }
-      __syncthreads();
+    };
+    if constexpr (kF16) {
+      all(true_type{});
+      if (__syncthreads_or(out)) all(false_type{});
+    } else {
+      all(false_type{});
+    }
+
+    // out: 32 rows at a time through the wave's own LDS
+    float* const out = reinterpret_cast<float*>(mx_lds) + wave * 32 * L::kOutLd;
+    const int p8 = lane & 7, row_in = lane >> 3;
+    const int64_t col = k0 + wn * 64 + p8 * 8;
+#pragma unroll 1
+    for (int f = 0; f < F; ++f) {
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+        if (j == f) {
+#pragma unroll
+          for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int at = i * 32 + 8 * (r / 4) + r % 4;  // + 4 half: the weights' row
+              out[l32 * L::kOutLd + 4 * (at % 16 + 4 * half) + at / 16] = acc[i][j][r];
+            }
+        }
+      wave_sync();
+#pragma unroll 1
+      for (int h = 0; h < 32; h += 8) {
+        const int64_t r = tile.r0 + (wm * F + f) * 32 + h + row_in;
+        if (r < tile.r1 && col < K) {
+          const float* src = out + (h + row_in) * L::kOutLd + p8 * 8;
+          const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
+          const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
+          const float y[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          w4_store8(a.dX, a.dtype, r * a.lddx + col, y, K - col < 8 ? (int)(K - col) : 8);
+        }
+      }
+      wave_sync();
     }
   };
-  if constexpr (kF16) {
-    bool fit = true;
-#pragma unroll 4
-    for (int64_t n = threadIdx.x; n < N; n += NW * 64) {
-#pragma unroll
-      for (int w = 0; w < BC / 128; ++w) {  // (rows are whole words)
-        const uint32_t v = w * 4 < blocks
-                               ? *reinterpret_cast<const uint32_t*>(scales + n * a.w.lds + w * 4) : 0u;
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          fit = fit && (w * 4 + b >= blocks || mx_f16_scale(mx_scale((v >> (8 * b)) & 0xffu)));
-      }
-    }
-    if (__syncthreads_and(fit))
-      run(true_type{});
-    else
-      run(false_type{});
-  } else {
-    run(false_type{});
-  }
-
-  // out: 32 rows at a time through the wave's own LDS
-  float* const out = reinterpret_cast<float*>(mx_lds) + wave * 32 * L::kOutLd;
-  const int p8 = lane & 7, row_in = lane >> 3;
-  const int64_t col = k0 + wn * 64 + p8 * 8;
-#pragma unroll 1
-  for (int f = 0; f < FM; ++f) {
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-      if (j == f) {
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int at = i * 32 + 8 * (r / 4) + r % 4;  // + 4 half: the weights' row
-            out[l32 * L::kOutLd + 4 * (at % 16 + 4 * half) + at / 16] = acc[i][j][r];
-          }
-      }
-    wave_sync();
-#pragma unroll 1
-    for (int h = 0; h < 32; h += 8) {
-      const int64_t r = tile.r0 + (wm * FM + f) * 32 + h + row_in;
-      if (r < tile.r1 && col < K) {
-        const float* src = out + (h + row_in) * L::kOutLd + p8 * 8;
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
-        const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
-        const float y[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-        w4_store8(a.dX, a.dtype, r * a.lddx + col, y, K - col < 8 ? (int)(K - col) : 8);
-      }
-    }
-    wave_sync();
-  }
+  constexpr int kHalf = kDirect && FM > 1 ? FM / 2 : FM;
+  if (kHalf < FM && tile.r1 - tile.r0 <= BM / 2)
+    run(std::integral_constant<int, kHalf>{});
+  else
+    run(std::integral_constant<int, FM>{});
 }
 
 template <typename T, bool kDirect, int BM, int BC, int WM, int WN>
 qp_status launch_dx_tile(const char* what, const MxDxArgs& a, hipStream_t stream) {
   using L = MxDxTile<T, BM, BC, WM, WN>;
   const int64_t slots = w4_tile_slots(a.rows, BM), groups = ceil_div(a.w.K, BC);
-  QP_REQUIRE(slots * groups * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
+  const int64_t grid = mx_tile_grid(slots, groups, BM >= 256);
+  QP_REQUIRE(grid * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
              "%s: rows and columns for more than 2^32 threads", what);
   auto kern = mx_dx_tile_kernel<T, kDirect, BM, BC, WM, WN>;
   if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                           hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds) != hipSuccess)
     QP_FAIL(QP_EHIP, "%s: %d bytes of LDS are not to be had", what, L::kLds);
-  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * groups)), dim3(L::NW * 64), L::kLds, stream, a,
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(L::NW * 64), L::kLds, stream, a,
                      (uint32_t)slots, (uint32_t)groups);
   return check_launch(what);
 }
@@ -605,7 +605,7 @@ DxPlan dx_plan(int32_t dtype, int64_t M, const qp_mx4* w) {
   const double few = groups(16, 128), t128 = groups(128, 128);
   // (one to a CU: whole rounds; experts of unlike sizes have more tiles than that)
   double t256 = groups(256, 256) * (parts > 1 ? 1.1 : 1.0);
-  if (t256 > 1.0) t256 = (double)(int64_t)(t256 + 255.0 / 256.0);
+  t256 = mx_halved_rounds(t256);
   // microseconds at 4096 channels (all grow with them): up to one workgroup a CU, and
   // for the further ones
   auto cost = [](double g, double one, double filled, double more) {

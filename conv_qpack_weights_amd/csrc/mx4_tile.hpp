@@ -42,13 +42,77 @@ __device__ __forceinline__ f32x16 mx_mfma_f16(f16x8 a, f16x8 b, f32x16 d) {
 
 // Which tile a workgroup takes: eight row tiles by neighbouring channel groups, in
 // runs per XCD.
-__device__ __forceinline__ void mx_place(uint32_t row_slots, uint32_t col_groups, uint32_t& slot,
-                                         uint32_t& group) {
-  const uint32_t id = xcd_run(blockIdx.x, gridDim.x);
+__device__ __forceinline__ void mx_place_of(uint32_t id, uint32_t row_slots, uint32_t col_groups,
+                                            uint32_t& slot, uint32_t& group) {
   const uint32_t band = id / (8 * col_groups), in_band = id - band * 8 * col_groups;
   const uint32_t band_rows = row_slots - band * 8 < 8 ? row_slots - band * 8 : 8;
   slot = band * 8 + in_band % band_rows;
   group = in_band / band_rows;
+}
+
+// How many BM-row tiles the rows have.
+template <int BM>
+__device__ __forceinline__ uint32_t mx_count_tiles(const W4Rows& rows) {
+  if (!rows.offsets) return (uint32_t)((rows.M + BM - 1) / BM);
+  const int lane = threadIdx.x & 63;
+  const int32_t M = (int32_t)rows.M;
+  uint32_t n = 0;
+  for (int e0 = 0; e0 <= rows.experts; e0 += 64) {  // (the clamps of w4_find_tile)
+    const int e = e0 + lane;
+    int32_t a = M, b = M;
+    if (e <= rows.experts) {
+      a = rows.offsets[e];
+      if (e < rows.experts) b = rows.offsets[e + 1];
+    }
+    a = a < 0 ? 0 : a > M ? M : a;
+    b = b < a ? a : b > M ? M : b;
+    n += (uint32_t)((b - a + BM - 1) / BM);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
+// Workgroups of BM-row tiles that are one to a CU: an XCD's tiles go by in rounds of its
+// 32 CUs, and those of a last round that leaves half of them idle and more are split in
+// two halves of the rows, which take 0.53 of the time.  (4096 tokens x 2 of 8 experts of
+// 11008 x 4096: a4w4 334 -> 322 us, bf16 rows 764 -> 741, their gradient 957 -> 841.)
+constexpr uint32_t kMxXcdCus = 32;
+
+// The tile of workgroup blockIdx.x; false: none.
+template <int BM, bool kHalves>
+__device__ __forceinline__ bool mx_take_tile(const W4Rows& rows, uint32_t row_slots,
+                                             uint32_t col_groups, W4Tile& tile, uint32_t& group) {
+  uint32_t slot;
+  if constexpr (!kHalves) {
+    mx_place_of(xcd_run(blockIdx.x, gridDim.x), row_slots, col_groups, slot, group);
+    tile = w4_find_tile<BM>(rows, slot);
+    return tile.expert >= 0;
+  } else {
+    const uint32_t slots = mx_count_tiles<BM>(rows), n = slots * col_groups;
+    const uint32_t x = blockIdx.x % 8, at = blockIdx.x / 8;
+    const uint32_t per = n / 8, rest = n % 8;
+    const uint32_t mine = per + (x < rest ? 1 : 0), first = x * per + (x < rest ? x : rest);
+    const uint32_t last = mine % kMxXcdCus, whole = mine - last;
+    const bool halved = last <= kMxXcdCus / 2 && at >= whole;
+    const uint32_t id = halved ? whole + (at - whole) / 2 : at;
+    if (id >= mine) return false;
+    mx_place_of(first + id, slots, col_groups, slot, group);
+    tile = w4_find_tile<BM>(rows, slot);
+    if (halved) {
+      const int64_t half = tile.r0 + BM / 2;
+      if ((at - whole) % 2)
+        tile.r0 = half;
+      else
+        tile.r1 = tile.r1 < half ? tile.r1 : half;
+    }
+    return tile.expert >= 0 && tile.r0 < tile.r1;
+  }
+}
+
+// How many workgroups `slots` row tiles (at most) by `groups` take.
+inline int64_t mx_tile_grid(int64_t slots, int64_t groups, bool halves) {
+  return halves ? (ceil_div(slots * groups, 8) + kMxXcdCus / 2) * 8 : slots * groups;
 }
 
 constexpr int mx_out_ld(int FN) { return 32 * FN + 4; }

@@ -63,12 +63,11 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
 
-  uint32_t slot, group;
-  mx_place(row_slots, col_groups, slot, group);
+  W4Tile tile;
+  uint32_t group;
+  if (!mx_take_tile<BM, (BM >= 256)>(a.rows, row_slots, col_groups, tile, group)) return;
   const int64_t n0 = (int64_t)group * BN;
   const int64_t N = a.w.rows, K = a.w.K;
-  const W4Tile tile = w4_find_tile<BM>(a.rows, slot);
-  if (tile.expert < 0) return;
   if (a.rows.offsets && tile.expert == a.rows.experts) {  // rows of no expert
     for (int64_t r = tile.r0 + wave; r < tile.r1; r += NW)
       for (int64_t n = n0 + lane; n < n0 + BN && n < N; n += 64)
@@ -153,273 +152,283 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
     if constexpr (kNext == 0) issue_s((s + 1) / 4 + L::kAhead);
   };
 
-  f32x16 acc[FN][FM];
+  // F x FN operands a wave
+  auto run = [&](auto operands) {
+    constexpr int F = decltype(operands)::value;
+    f32x16 acc[FN][F];
 
-  const int l32 = lane & 31, half = lane >> 5;
-  const uint32_t sel = half ? 0x07050301u : 0x06040200u;  // the half's scale of each 64 K
-  const int arow = wm * 32 * FM + l32, brow = wn * 32 * FN + l32;
-  struct Rows {
-    u32x4 x[FM][NP];
-  };
-  struct Weights {
-    u32x4 q[FN];
-    float s[FN];
-  };
-  auto read_x = [&](Rows& o, int s, int step) {
-    const lds_u8* const from = xbuf + (s % D) * L::kX;
-    const int at = ((4 * half + step) ^ mx_turn(l32)) * 16;
+    const int l32 = lane & 31, half = lane >> 5;
+    const uint32_t sel = half ? 0x07050301u : 0x06040200u;  // the half's scale of each 64 K
+    const int arow = wm * 32 * F + l32, brow = wn * 32 * FN + l32;
+    struct Rows {
+      u32x4 x[F][NP];
+    };
+    struct Weights {
+      u32x4 q[FN];
+      float s[FN];
+    };
+    auto read_x = [&](Rows& o, int s, int step) {
+      const lds_u8* const from = xbuf + (s % D) * L::kX;
+      const int at = ((4 * half + step) ^ mx_turn(l32)) * 16;
 #pragma unroll
-    for (int j = 0; j < FM; ++j)
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-        o.x[j][i] = *(const __attribute__((address_space(3))) u32x4*)(
-            from + (i * BM + arow + j * 32) * 128 + at);
-  };
-  auto read_w = [&](Weights& o, int s) {
-    const int c = s >> 2, p = s & 3;
-    const lds_u8* const from = wbuf + (c % L::kChunks) * L::kW;
-    const lds_u8* const st = sbuf + (c % L::kChunks) * L::kScales;
-    const int at = ((2 * p + half) ^ mx_turn(l32)) * 16;
-#pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      o.q[i] = *(const __attribute__((address_space(3))) u32x4*)(from + (brow + i * 32) * 128 + at);
-      o.s[i] = mx_scale(st[(brow + i * 32) * 8 + 2 * p + half]);
-    }
-  };
-  auto multiply = [&](const Rows& x, const Weights& w, int step, auto kind) {
-    if constexpr (decltype(kind)::value) {
-      f16x8 v[FN];
-#pragma unroll
-      for (int i = 0; i < FN; ++i) v[i] = mx_unpack_f16(w.q[i][step], w.s[i]);
-#pragma unroll
-      for (int j = 0; j < FM; ++j)
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-          acc[i][j] = mx_mfma_f16(v[i], __builtin_bit_cast(f16x8, x.x[j][0]), acc[i][j]);
-    } else {
-      constexpr int kPieces = kF16 ? 2 : NP;
-      bf16x8 v[FN];
-#pragma unroll
-      for (int i = 0; i < FN; ++i) v[i] = mx_unpack(w.q[i][step], w.s[i]);
-#pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        bf16x8 xv[kPieces];
-        if constexpr (kF16)
-          MxFrag<f16_t>{x.x[j][0]}.split(xv);
-        else
-#pragma unroll
-          for (int n = 0; n < NP; ++n) xv[n] = __builtin_bit_cast(bf16x8, x.x[j][n]);
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-          for (int n = 0; n < kPieces; ++n) acc[i][j] = mx_mfma_bf16(v[i], xv[n], acc[i][j]);
-      }
-    }
-  };
-  // the rows through registers: their pieces of stage s, the part before K
-  auto fetch = [&](MxFrag<T> (&f)[kSlots], int s) {
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
-      const int64_t k = (int64_t)s * 64 + piece(j) * 8, left = K - k;
-      f[j].load_n(px[kDirect ? 0 : j] + (left > 0 ? k : 0), left > 8 ? 8 : left < 0 ? 0 : (int)left);
-    }
-  };
-  auto fetch_full = [&](MxFrag<T> (&f)[kSlots], int s) {
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j)
-      f[j].load(px[kDirect ? 0 : j] + (int64_t)s * 64 + piece(j) * 8);
-  };
-  auto put = [&](const MxFrag<T> (&f)[kSlots], int s) {
-    lds_u8* const to = xbuf + (s % D) * L::kX;
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
-      lds_u8* const at = to + ((wave * kSlots + j) * 8 + lrow) * 128 + (lane & 7) * 16;
-      if constexpr (NP == 1) {
-        *(__attribute__((address_space(3))) u32x4*)at = f[j].v;
-      } else {
-        bf16x8 v[NP];
-        f[j].split(v);
+      for (int j = 0; j < F; ++j)
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-          *(__attribute__((address_space(3))) bf16x8*)(at + i * BM * 128) = v[i];
-      }
-    }
-  };
-
-  using P0 = std::integral_constant<int, 0>;
-  using P1 = std::integral_constant<int, 1>;
-  using P2 = std::integral_constant<int, 2>;
-  using P3 = std::integral_constant<int, 3>;
-  using std::false_type;
-  using std::true_type;
-  // The next stage is there for everyone (D = 4: all but the loads of the two stages
-  // before this one are done, the weights' are four stages ahead of their use), and
-  // everyone has read all of this one.
-  auto arrive = [&](auto place) {
-    constexpr int P = decltype(place)::value;
-    wait_vmcnt<D == 2 ? 0 : 2 * (kA + 1) + (P < 2 ? 1 : 0)>();
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  };
-  MxFrag<T> f[kSlots];
-  Rows even, odd;
-  Weights now, next;
-  auto each = [&](auto stage) {
-    int s = 0;
-    for (; s + 4 <= full; s += 4) {
-      stage(s, P0{});
-      stage(s + 1, P1{});
-      stage(s + 2, P2{});
-      stage(s + 3, P3{});
-    }
-    if (s < full) stage(s, P0{});
-    if (s + 1 < full) stage(s + 1, P1{});
-    if (s + 2 < full) stage(s + 2, P2{});
-  };
-  // All whole stages; with f16 weights, whether one of the wave's was no f16 value.
-  auto pass = [&](auto kind) {
-    bool out = false;
-#pragma unroll
-    for (int c = 0; c < L::kAhead; ++c) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) issue_w(c, q);
-      issue_s(c);
-    }
-    if constexpr (kDirect) {
-#pragma unroll
-      for (int s = 0; s < D - 1; ++s) issue_x(s);
-    } else if (full > 0) {
-      fetch_full(f, 0);
-      put(f, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-      for (int j = 0; j < FM; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-    wait_vmcnt<0>();
-    __syncthreads();
-    if constexpr (kDirect) issue_x(D - 1);
-    issue_w(L::kAhead, 0);
-    issue_s(L::kAhead);
-    auto look = [&] {
-      if constexpr (decltype(kind)::value)
-#pragma unroll
-        for (int i = 0; i < FN; ++i) out |= !mx_f16_scale(now.s[i]);
+          o.x[j][i] = *(const __attribute__((address_space(3))) u32x4*)(
+              from + (i * BM + arow + j * 32) * 128 + at);
     };
-    if constexpr (kDirect) {
-      read_x(even, 0, 0);
-      read_w(now, 0);
-      // (no branch between MFMAs: the compiler would move them past it, behind the
-      // barrier)
-      auto steps = [&](int s, auto place) {
-        read_x(odd, s, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(even, now, 0, kind);
-        __builtin_amdgcn_sched_barrier(0);
-        read_x(even, s, 2);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(odd, now, 1, kind);
-        look();
-        __builtin_amdgcn_sched_barrier(0);
-        read_x(odd, s, 3);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(even, now, 2, kind);
-        __builtin_amdgcn_sched_barrier(0);
-        arrive(place);
-        // (which first: 4096^3 by 256 x 256 tiles 106 us loads first, 103 last; 1024 x 4096 x
-        // 4096 by 128 x 128 40 and 47)
-        if constexpr (BM < 256) issue(s, place);
-        read_x(even, s + 1, 0);
-        read_w(next, s + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(odd, now, 3, kind);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (BM >= 256) issue(s, place);
-        now = next;
+    auto read_w = [&](Weights& o, int s) {
+      const int c = s >> 2, p = s & 3;
+      const lds_u8* const from = wbuf + (c % L::kChunks) * L::kW;
+      const lds_u8* const st = sbuf + (c % L::kChunks) * L::kScales;
+      const int at = ((2 * p + half) ^ mx_turn(l32)) * 16;
+#pragma unroll
+      for (int i = 0; i < FN; ++i) {
+        o.q[i] = *(const __attribute__((address_space(3))) u32x4*)(from + (brow + i * 32) * 128 + at);
+        o.s[i] = mx_scale(st[(brow + i * 32) * 8 + 2 * p + half]);
+      }
+    };
+    auto multiply = [&](const Rows& x, const Weights& w, int step, auto kind) {
+      if constexpr (decltype(kind)::value) {
+        f16x8 v[FN];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) v[i] = mx_unpack_f16(w.q[i][step], w.s[i]);
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+#pragma unroll
+          for (int i = 0; i < FN; ++i)
+            acc[i][j] = mx_mfma_f16(v[i], __builtin_bit_cast(f16x8, x.x[j][0]), acc[i][j]);
+      } else {
+        constexpr int kPieces = kF16 ? 2 : NP;
+        bf16x8 v[FN];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) v[i] = mx_unpack(w.q[i][step], w.s[i]);
+#pragma unroll
+        for (int j = 0; j < F; ++j) {
+          bf16x8 xv[kPieces];
+          if constexpr (kF16)
+            MxFrag<f16_t>{x.x[j][0]}.split(xv);
+          else
+#pragma unroll
+            for (int n = 0; n < NP; ++n) xv[n] = __builtin_bit_cast(bf16x8, x.x[j][n]);
+#pragma unroll
+          for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int n = 0; n < kPieces; ++n) acc[i][j] = mx_mfma_bf16(v[i], xv[n], acc[i][j]);
+        }
+      }
+    };
+    // the rows through registers: their pieces of stage s, the part before K
+    auto fetch = [&](MxFrag<T> (&f)[kSlots], int s) {
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        const int64_t k = (int64_t)s * 64 + piece(j) * 8, left = K - k;
+        f[j].load_n(px[kDirect ? 0 : j] + (left > 0 ? k : 0), left > 8 ? 8 : left < 0 ? 0 : (int)left);
+      }
+    };
+    auto fetch_full = [&](MxFrag<T> (&f)[kSlots], int s) {
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        f[j].load(px[kDirect ? 0 : j] + (int64_t)s * 64 + piece(j) * 8);
+    };
+    auto put = [&](const MxFrag<T> (&f)[kSlots], int s) {
+      lds_u8* const to = xbuf + (s % D) * L::kX;
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        lds_u8* const at = to + ((wave * kSlots + j) * 8 + lrow) * 128 + (lane & 7) * 16;
+        if constexpr (NP == 1) {
+          *(__attribute__((address_space(3))) u32x4*)at = f[j].v;
+        } else {
+          bf16x8 v[NP];
+          f[j].split(v);
+#pragma unroll
+          for (int i = 0; i < NP; ++i)
+            *(__attribute__((address_space(3))) bf16x8*)(at + i * BM * 128) = v[i];
+        }
+      }
+    };
+
+    using P0 = std::integral_constant<int, 0>;
+    using P1 = std::integral_constant<int, 1>;
+    using P2 = std::integral_constant<int, 2>;
+    using P3 = std::integral_constant<int, 3>;
+    using std::false_type;
+    using std::true_type;
+    // The next stage is there for everyone (D = 4: all but the loads of the two stages
+    // before this one are done, the weights' are four stages ahead of their use), and
+    // everyone has read all of this one.
+    auto arrive = [&](auto place) {
+      constexpr int P = decltype(place)::value;
+      wait_vmcnt<D == 2 ? 0 : 2 * (kA + 1) + (P < 2 ? 1 : 0)>();
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+    MxFrag<T> f[kSlots];
+    Rows even, odd;
+    Weights now, next;
+    auto each = [&](auto stage) {
+      int s = 0;
+      for (; s + 4 <= full; s += 4) {
+        stage(s, P0{});
+        stage(s + 1, P1{});
+        stage(s + 2, P2{});
+        stage(s + 3, P3{});
+      }
+      if (s < full) stage(s, P0{});
+      if (s + 1 < full) stage(s + 1, P1{});
+      if (s + 2 < full) stage(s + 2, P2{});
+    };
+    // All whole stages; with f16 weights, whether one of the wave's was no f16 value.
+    auto pass = [&](auto kind) {
+      bool out = false;
+#pragma unroll
+      for (int c = 0; c < L::kAhead; ++c) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) issue_w(c, q);
+        issue_s(c);
+      }
+      if constexpr (kDirect) {
+#pragma unroll
+        for (int s = 0; s < D - 1; ++s) issue_x(s);
+      } else if (full > 0) {
+        fetch_full(f, 0);
+        put(f, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+      wait_vmcnt<0>();
+      __syncthreads();
+      if constexpr (kDirect) issue_x(D - 1);
+      issue_w(L::kAhead, 0);
+      issue_s(L::kAhead);
+      auto look = [&] {
+        if constexpr (decltype(kind)::value)
+#pragma unroll
+          for (int i = 0; i < FN; ++i) out |= !mx_f16_scale(now.s[i]);
       };
-      if (tile.r0 + wm * 32 * FM >= tile.r1) {
-        // (a wave without rows only loads, and leaves its SIMD to the others)
+      if constexpr (kDirect) {
+        read_x(even, 0, 0);
+        read_w(now, 0);
+        // (no branch between MFMAs: the compiler would move them past it, behind the
+        // barrier)
+        auto steps = [&](int s, auto place) {
+          read_x(odd, s, 1);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(even, now, 0, kind);
+          __builtin_amdgcn_sched_barrier(0);
+          read_x(even, s, 2);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(odd, now, 1, kind);
+          look();
+          __builtin_amdgcn_sched_barrier(0);
+          read_x(odd, s, 3);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(even, now, 2, kind);
+          __builtin_amdgcn_sched_barrier(0);
+          arrive(place);
+          // (which first: 4096^3 by 256 x 256 tiles 106 us loads first, 103 last; 1024 x 4096 x
+          // 4096 by 128 x 128 40 and 47)
+          if constexpr (BM < 256) issue(s, place);
+          read_x(even, s + 1, 0);
+          read_w(next, s + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(odd, now, 3, kind);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (BM >= 256) issue(s, place);
+          now = next;
+        };
+        if (tile.r0 + wm * 32 * F >= tile.r1) {
+          // (a wave without rows only loads, and leaves its SIMD to the others)
+          each([&](int s, auto place) {
+            arrive(place);
+            issue(s, place);
+          });
+        } else {
+          each(steps);
+        }
+      } else {
         each([&](int s, auto place) {
+          fetch_full(f, s + 1 < full ? s + 1 : s);
+          read_w(now, s);
+          look();
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            read_x(even, s, t);
+            multiply(even, now, t, kind);
+          }
+          put(f, s + 1);
           arrive(place);
           issue(s, place);
         });
-      } else {
-        each(steps);
       }
+      wait_vmcnt<0>();
+      return out;
+    };
+    if constexpr (kF16) {
+      if (__syncthreads_or(pass(true_type{}))) pass(false_type{});
     } else {
-      each([&](int s, auto place) {
-        fetch_full(f, s + 1 < full ? s + 1 : s);
-        read_w(now, s);
-        look();
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          read_x(even, s, t);
-          multiply(even, now, t, kind);
-        }
-        put(f, s + 1);
-        arrive(place);
-        issue(s, place);
-      });
+      pass(false_type{});
     }
-    wait_vmcnt<0>();
-    return out;
-  };
-  if constexpr (kF16) {
-    if (__syncthreads_or(pass(true_type{}))) pass(false_type{});
-  } else {
-    pass(false_type{});
-  }
-  __syncthreads();
-  if ((int64_t)full * 64 < K) {
-    // the stage that K cuts: its rows through registers, zeros from K on; zero scales
-    // past the last block (what is found there could be a NaN)
-    if constexpr (kDirect) {
-      // (the pieces of a direct load's lanes, by plain loads)
-      lds_u8* const to = xbuf + (full % D) * L::kX;
+    __syncthreads();
+    if ((int64_t)full * 64 < K) {
+      // the stage that K cuts: its rows through registers, zeros from K on; zero scales
+      // past the last block (what is found there could be a NaN)
+      if constexpr (kDirect) {
+        // (the pieces of a direct load's lanes, by plain loads)
+        lds_u8* const to = xbuf + (full % D) * L::kX;
 #pragma unroll 1
-      for (int j = 0; j < kA; ++j) {
-        const int row = (wave * kA + j) * 8 + lrow;
-        if (row >= BM) break;
-        const int64_t k = (int64_t)full * 64 + piece(j) * 8, left = K - k;
-        const T* p = xbase + source(row) * a.ldx;
-        const Piece<T> one =
-            load_piece(p + (left > 0 ? k : 0), left > 8 ? 8 : left < 0 ? 0 : (int)left);
-        *(__attribute__((address_space(3))) u32x4*)(to + row * 128 + (lane & 7) * 16) = one.v;
+        for (int j = 0; j < kA; ++j) {
+          const int row = (wave * kA + j) * 8 + lrow;
+          if (row >= BM) break;
+          const int64_t k = (int64_t)full * 64 + piece(j) * 8, left = K - k;
+          const T* p = xbase + source(row) * a.ldx;
+          const Piece<T> one =
+              load_piece(p + (left > 0 ? k : 0), left > 8 ? 8 : left < 0 ? 0 : (int)left);
+          *(__attribute__((address_space(3))) u32x4*)(to + row * 128 + (lane & 7) * 16) = one.v;
+        }
+      } else {
+        fetch(f, full);
+        put(f, full);
       }
-    } else {
-      fetch(f, full);
-      put(f, full);
-    }
-    __syncthreads();
-    read_w(now, full);
-    if (2 * full + half >= G) {
+      __syncthreads();
+      read_w(now, full);
+      if (2 * full + half >= G) {
 #pragma unroll
-      for (int i = 0; i < FN; ++i) now.s[i] = mx_scale(0);
-    }
+        for (int i = 0; i < FN; ++i) now.s[i] = mx_scale(0);
+      }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      read_x(even, full, t);
-      multiply(even, now, t, false_type{});
+      for (int t = 0; t < 4; ++t) {
+        read_x(even, full, t);
+        multiply(even, now, t, false_type{});
+      }
+      __syncthreads();
     }
-    __syncthreads();
-  }
 
-  mx_store_tile<FM, FN>(acc, a, tile, wm * FM * 32, n0 + wn * FN * 32,
-                        reinterpret_cast<float*>(mx_lds) + wave * 32 * mx_out_ld(FN));
+    mx_store_tile<F, FN>(acc, a, tile, wm * F * 32, n0 + wn * FN * 32,
+                          reinterpret_cast<float*>(mx_lds) + wave * 32 * mx_out_ld(FN));
+  };
+  constexpr int kHalf = kDirect && FM > 1 ? FM / 2 : FM;
+  if (kHalf < FM && tile.r1 - tile.r0 <= BM / 2)
+    run(std::integral_constant<int, kHalf>{});
+  else
+    run(std::integral_constant<int, FM>{});
 }
 
 template <typename T, bool kDirect, int BM, int BN, int WM, int WN, int D, bool kOnce = false>
 qp_status mx_launch_w4_tile(const MxArgs& a, hipStream_t stream) {
   using L = W4MxTile<T, BM, BN, WM, WN, D>;
   const int64_t slots = w4_tile_slots(a.rows, BM), groups = ceil_div(a.w.rows, BN);
-  QP_REQUIRE(slots * groups * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
+  const int64_t grid = mx_tile_grid(slots, groups, BM >= 256);
+  QP_REQUIRE(grid * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
              "qgemm_w4_mx: rows and channels for more than 2^32 threads");
   auto kern = mx_w4_tile_kernel<T, kDirect, BM, BN, WM, WN, D, kOnce>;
   if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                           hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds) != hipSuccess)
     QP_FAIL(QP_EHIP, "qgemm_w4_mx: %d bytes of LDS are not to be had", L::kLds);
-  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * groups)), dim3(L::NW * 64), L::kLds, stream, a,
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(L::NW * 64), L::kLds, stream, a,
                      (uint32_t)slots, (uint32_t)groups);
   return check_launch("qgemm_w4_mx (many rows)");
 }

@@ -118,10 +118,10 @@ def test_gradient_kernels(qp, dtype, kernel, M, K):
 EXPERTS = [  # product, kernel, slots, experts, channels (the gradient's columns)
     ("a4w4", "rows16x16", 40, 8, 200), ("a4w4", "rows16x32", 128, 16, 5500),
     ("a4w4", "tile64x64", 600, 3, 2000), ("a4w4", "tile128x128", 2600, 3, 2000),
-    ("a4w4", "tile256x256", 6000, 3, 4000),
+    ("a4w4", "tile256x256", 7000, 3, 4000),
     ("w4", "rows16x16", 40, 8, 200), ("w4", "rows16x64", 64, 8, 4000),
     ("w4", "tile32x128", 128, 16, 5500), ("w4", "tile128x128", 2600, 3, 2000),
-    ("w4", "tile256x256", 6000, 3, 4000),
+    ("w4", "tile256x256", 7000, 3, 4000),
     ("w4_dx", "rows16x128", 300, 3, 300), ("w4_dx", "tile128x128", 2600, 3, 2000),
     ("w4_dx", "tile256x256", 6000, 3, 2000)]
 
@@ -281,3 +281,34 @@ def test_tiles_at_every_end_of_a_rows_scales(qp, kernel, M, N):
         apart = torch.full((M, -(-G // 4) * 4 + 8), 255, dtype=torch.uint8, device="cuda")[:, :G]
         B = qp.mx4_tensor(A.codes, apart.copy_(A.scales), K)
         _close(qp.qgemm_a4w4_mx(B, W), want, size, K, "f32", "K=%d apart" % K)
+
+
+@pytest.mark.parametrize("product,dtype", [("a4w4", "f32"), ("w4", "bf16"), ("w4", "f16"),
+                                           ("w4_dx", "bf16"), ("w4_dx", "f16")])
+def test_a_last_round_in_half_tiles(qp, product, dtype):
+    """19 x 32 tiles of 256 x 256: 76 to each of 8 times 32 CUs, the last 12 in halves,
+    some of which have no rows; and few rows of many given."""
+    import torch
+    g = torch.Generator().manual_seed(5)
+    M, N, K = 4700, 8190, 330
+    print("mx4 half tiles", product, dtype, flush=True)
+    W, w = _matrix(qp, g, K, N) if product == "w4_dx" else _matrix(qp, g, N, K)
+    assert qp.qgemm_mx_kernel_name(product, M, W, _dt(dtype)).split("/")[0] == "tile256x256"
+    wt = w if product == "w4_dx" else w.t().contiguous()
+    if product == "a4w4":
+        X, x = _matrix(qp, g, M, K)
+    else:
+        X, x = _rows(g, M, K, dtype)
+    run = {"a4w4": qp.qgemm_a4w4_mx, "w4": qp.qgemm_w4_mx, "w4_dx": qp.qgemm_w4_mx_dx}[product]
+    want, size = x @ wt, x.abs() @ wt.abs()
+    _close(run(X, W), want, size, K, dtype, "dense")
+    one = qp.mx4_tensor(W.codes[None], W.scales[None], W.K)
+    assert one.shape[0] == 1
+    for rows in (0, 1, 300, 4000):
+        offsets = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+        run = {"a4w4": qp.qgemm_a4w4_mx_experts, "w4": qp.qgemm_w4_mx_experts,
+               "w4_dx": qp.qgemm_w4_mx_experts_dx}[product]
+        got = run(X, one, offsets)
+        assert not got[rows:].any()
+        if rows:
+            _close(got[:rows], want[:rows], size[:rows], K, dtype, "%d rows" % rows)
