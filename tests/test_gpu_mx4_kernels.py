@@ -312,3 +312,39 @@ def test_a_last_round_in_half_tiles(qp, product, dtype):
         assert not got[rows:].any()
         if rows:
             _close(got[:rows], want[:rows], size[:rows], K, dtype, "%d rows" % rows)
+
+
+@pytest.mark.parametrize("product,kernel,M,N", [
+    ("w4", "rows16x16", 5, 300), ("w4", "rows16x64", 61, 4030), ("w4", "tile32x64", 146, 4900),
+    ("w4", "tile32x128", 500, 4010), ("w4", "tile128x128", 1100, 4010),
+    ("w4", "tile256x256", 4090, 4090), ("w4_dx", "rows16x128", 5, 300),
+    ("w4_dx", "tile128x128", 2100, 4010), ("w4_dx", "tile256x256", 4090, 4090)])
+def test_one_block_that_is_no_f16_values(qp, product, kernel, M, N):
+    """f16 rows: a single scale out of f16's reach, in the first block, before the last
+    and in a cut one, rows by direct loads and through registers."""
+    import torch
+    K = 330
+    for where in (0, 1, 2):
+        g = torch.Generator().manual_seed(M + where)
+        # (the gradient: N columns, 330 channels)
+        shape = (K, N) if product == "w4_dx" else (N, K)
+        W, w = _matrix(qp, g, *shape)
+        rows, G = W.scales.shape
+        r, b = [(0, 0), (rows // 2, G - 2), (rows - 1, G - 1)][where]
+        old = int(W.scales[r, b])
+        W.scales[r, b] = 150
+        w[r, 32 * b:32 * b + 32] *= 2.0 ** (150 - old)
+        assert qp.qgemm_mx_kernel_name(product, M, W, torch.float16).split("/")[0] == kernel
+        print("mx4 one block", product, kernel, M, N, where, flush=True)
+        for odd in (False, True):
+            X, x = _rows(g, M, K, "f16", odd)
+            X, x = X * 2.0 ** -14, x * 2.0 ** -14  # (so that f16 gradients stay finite)
+            x = X.double()
+            if odd:
+                X = torch.cat((torch.zeros_like(X[:, :1]), X), 1)[:, 1:]
+            if product == "w4_dx":
+                got, v = qp.qgemm_w4_mx_dx(X, W), w
+                _close(got, x @ v, x.abs() @ v.abs(), K, "f16", "odd=%s" % odd)
+            else:
+                got, v = qp.qgemm_w4_mx(X, W, out_dtype=torch.float32), w.t().contiguous()
+                _close(got, x @ v, x.abs() @ v.abs(), K, "f32", "odd=%s" % odd)
