@@ -323,9 +323,9 @@ qp_status launch_tile_of(const MxArgs& a, hipStream_t stream) {
   QP_REQUIRE(grid * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
              "qgemm_a4w4_mx: rows and channels for more than 2^32 threads");
   auto kern = mx_a4w4_tile_kernel<BM, BN, WM, WN, D, kWide>;
-  if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds) != hipSuccess)
-    QP_FAIL(QP_EHIP, "qgemm_a4w4_mx: %d bytes of LDS are not to be had", L::kLds);
+  static std::atomic<uint64_t> reserved{0};
+  if (qp_status st = mx_reserve_lds("qgemm_a4w4_mx", reinterpret_cast<const void*>(kern), L::kLds, reserved))
+    return st;
   hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(L::NW * 64), L::kLds, stream, a,
                      (uint32_t)slots, (uint32_t)groups);
   return check_launch("qgemm_a4w4_mx (many rows)");

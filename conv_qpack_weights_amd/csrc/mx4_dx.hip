@@ -573,9 +573,9 @@ qp_status launch_dx_tile(const char* what, const MxDxArgs& a, hipStream_t stream
   QP_REQUIRE(grid * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
              "%s: rows and columns for more than 2^32 threads", what);
   auto kern = mx_dx_tile_kernel<T, kDirect, BM, BC, WM, WN>;
-  if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds) != hipSuccess)
-    QP_FAIL(QP_EHIP, "%s: %d bytes of LDS are not to be had", what, L::kLds);
+  static std::atomic<uint64_t> reserved{0};
+  if (qp_status st = mx_reserve_lds(what, reinterpret_cast<const void*>(kern), L::kLds, reserved))
+    return st;
   hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(L::NW * 64), L::kLds, stream, a,
                      (uint32_t)slots, (uint32_t)groups);
   return check_launch(what);

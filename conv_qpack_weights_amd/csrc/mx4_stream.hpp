@@ -172,9 +172,10 @@ qp_status mx_launch_stream_of(const MxArgs& a, hipStream_t stream) {
   QP_REQUIRE(slots * groups * kWaves * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
              "qgemm_mx: rows and channels for more than 2^32 threads");
   auto kern = mx_stream_kernel<T, kTiles, kWaves, kOnce>;
-  if (hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, L::kLds) != hipSuccess)
-    QP_FAIL(QP_EHIP, "qgemm_mx: %d bytes of LDS are not to be had", L::kLds);
+  static std::atomic<uint64_t> reserved{0};
+  if (qp_status st =
+          mx_reserve_lds("qgemm_mx", reinterpret_cast<const void*>(kern), L::kLds, reserved))
+    return st;
   hipLaunchKernelGGL(kern, dim3((unsigned)(slots * groups)), dim3(kWaves * 64), L::kLds, stream, a,
                      (uint32_t)slots);
   return check_launch("qgemm_mx (few rows)");

@@ -2,6 +2,8 @@
 // loads into LDS, the order of the tiles, the way out.
 #pragma once
 
+#include <atomic>
+
 #include "mx4.hpp"
 
 #pragma clang fp contract(off)
@@ -113,6 +115,19 @@ __device__ __forceinline__ bool mx_take_tile(const W4Rows& rows, uint32_t row_sl
 // How many workgroups `slots` row tiles (at most) by `groups` take.
 inline int64_t mx_tile_grid(int64_t slots, int64_t groups, bool halves) {
   return halves ? (ceil_div(slots * groups, 8) + kMxXcdCus / 2) * 8 : slots * groups;
+}
+
+// A kernel's LDS reserved once per device: `reserved` has a bit for each that it is for.
+inline qp_status mx_reserve_lds(const char* what, const void* kern, int bytes,
+                                std::atomic<uint64_t>& reserved) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) QP_FAIL(QP_EHIP, "%s: hipGetDevice failed", what);
+  const uint64_t bit = dev >= 0 && dev < 64 ? UINT64_C(1) << dev : 0;
+  if (bit && (reserved.load(std::memory_order_acquire) & bit)) return QP_OK;
+  if (hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+    QP_FAIL(QP_EHIP, "%s: cannot reserve %d bytes of LDS", what, bytes);
+  reserved.fetch_or(bit, std::memory_order_release);
+  return QP_OK;
 }
 
 constexpr int mx_out_ld(int FN) { return 32 * FN + 4; }
