@@ -7,7 +7,8 @@
 namespace qp {
 namespace {
 
-qp_status check_common(const char* what, int64_t M, const qp_mx4* w, int64_t K, float lo, float hi) {
+qp_status check_common(const char* what, int64_t M, const qp_mx4* w, int64_t K, float lo,
+                       float hi) {
   QP_REQUIRE(M >= 0, QP_EINVAL, "%s: M is negative", what);
   QP_REQUIRE(M <= kW4MaxRows, QP_EUNSUPPORTED, "%s: more than 2^30 rows", what);
   qp_status st = mx_check(what, "w", w);
@@ -60,7 +61,8 @@ constexpr MxCost kW4Shapes[] = {
     {kMxTile256x256, 256, 256, 103.0, 100.0, 100.0, "tile256x256"},
 };
 // The same of f32 rows: 16 x 4096 14.1, 14.8, 15.4, 16.6; 16 x 11008 38, 34, 19.6, 20.8; 64 x
-// 11008 112, 84, 58, 52, 128 x 128 tiles 125; 128 x 4096 78, 56, 40, 33, 121; 4096 x 4096 tiles 510.
+// 11008 112, 84, 58, 52, 128 x 128 tiles 125; 128 x 4096 78, 56, 40, 33, 121; 4096 x 4096 tiles
+// 510.
 constexpr MxCost kW4ShapesF32[] = {
     {kMxRows16x16, 16, 16, 14.1, 9.2, 9.2, "rows16x16"},
     {kMxRows16x32, 16, 32, 15.2, 13.5, 13.5, "rows16x32"},
@@ -194,7 +196,8 @@ extern "C" qp_status qgemm_w4_mx_experts(const void* X, int32_t dtype, int64_t x
   return run_float(what, args, dtype, stream);
 }
 
-extern "C" qp_status qgemm_mx_kernel_name(int32_t product, int64_t M, const qp_mx4* w, int32_t dtype,
+extern "C" qp_status qgemm_mx_kernel_name(int32_t product, int64_t M, const qp_mx4* w,
+                                          int32_t dtype,
                                           char* name, size_t bytes) {
   using namespace qp;
   clear_error();

@@ -322,7 +322,8 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t n = (int64_t)full * 64 + g * 8 + i, at = n < N ? n : N - 1;
-      const uint32_t q = *reinterpret_cast<const uint16_t*>(codes + at * a.w.ldc + (in ? 2 * u : 0));
+      const uint32_t q =
+          *reinterpret_cast<const uint16_t*>(codes + at * a.w.ldc + (in ? 2 * u : 0));
       const uint32_t v = scales[at * a.w.lds + (in ? u / 8 : 0)];
       w.q[i] = n < N ? q : 0u;
       w.s[i] = n < N ? v : 127u;
@@ -338,11 +339,15 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
       const float by = mx_scale(w.s[i]);
       if constexpr (decltype(kind)::value) {
         out |= there && !mx_f16_scale(by);
-        c[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 0));
-        c[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 1));
+        c[i][0] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 0));
+        c[i][1] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 1));
       } else {
-        c[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.q[i], by, 0));
-        c[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.q[i], by, 1));
+        c[i][0] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.q[i], by, 0));
+        c[i][1] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.q[i], by, 1));
       }
     }
     lds_u8* const to = wbuf + (s & 1) * L::kW;

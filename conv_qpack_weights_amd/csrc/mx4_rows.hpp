@@ -1,5 +1,6 @@
-// mx4_rows.hpp -- the products with MXFP4 weights for few rows: of float rows or
-// MXFP4 rows, instantiated per row type.
+// mx4_rows.hpp -- the products with MXFP4 weights for few rows, operands straight from
+// memory: of f32 rows, and of the 16-bit and MXFP4 rows that the direct loads of
+// mx4_stream.hpp cannot take (rows at odd addresses, or too far apart).
 //
 //   y[r,n] = clamp(sum_k x[r,k] w[n,k] + bias[n], lo, hi)
 //
@@ -10,6 +11,11 @@
 // values of 32-block l/16: one operand of the scaled 4-bit MFMA, or, word t of
 // them with the rows' elements 32 (l/16) + 8t .. + 7, of four bf16 MFMAs (which
 // of the block's K meet in which MFMA does not matter to the sum).
+//
+// A row's four scales of a block come in words, for four blocks at a time 16 bytes: a
+// load of 16 rows looks up 16 lines, however few bytes of each it takes, and those
+// look-ups bound the kernel (16 x 11008 x 4096 f32 19.6 us by 48 channels, 38 by 16).
+// f32 rows are three bf16 pieces, each product of a piece exact.
 #pragma once
 
 #include "mx4.hpp"
