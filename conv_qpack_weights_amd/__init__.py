@@ -1013,7 +1013,8 @@ def _mx4_scales(rows_shape, G, like):
 def mx4_tensor(codes: torch.Tensor, scales: torch.Tensor, K=None) -> MX4:
     """An MXFP4 matrix (or one an expert) from codes uint8 [.., rows, 16*ceil(K/32)]
     and scales uint8 [.., rows, ceil(K/32)], as checkpoints hold them: taken as they
-    are where the kernels can read them, else laid out anew (once, at load time)."""
+    are where the kernels can read them, else laid out anew (once, at load time).  The
+    values that fill up the last block of a ``K`` not a multiple of 32 must be zeros."""
     assert codes.dtype == torch.uint8 and scales.dtype == torch.uint8, \
         "codes and scales must be uint8"
     assert codes.dim() in (2, 3) and codes.shape[:-1] == scales.shape[:-1], \

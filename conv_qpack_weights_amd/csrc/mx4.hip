@@ -197,8 +197,7 @@ extern "C" qp_status qgemm_w4_mx_experts(const void* X, int32_t dtype, int64_t x
 }
 
 extern "C" qp_status qgemm_mx_kernel_name(int32_t product, int64_t M, const qp_mx4* w,
-                                          int32_t dtype,
-                                          char* name, size_t bytes) {
+                                          int32_t dtype, char* name, size_t bytes) {
   using namespace qp;
   clear_error();
   const char* what = "qgemm_mx_kernel_name";

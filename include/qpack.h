@@ -820,7 +820,8 @@ qp_status qgemm_w4_mx_experts_dx(const void* dY, int32_t dtype, int64_t M, int64
  *   QP_MX_A4W4: MXFP4 rows) and weights of w's shape, dense or (matrices > 1) by
  *   expert: for profiles and tests, on the host alone.  "rows16x48" is 16 rows by 48
  *   channels a workgroup, "tile128x128" that many over LDS; gradients "rows16x128/4"
- *   (the channels in 4 splits) or a tile.
+ *   (the channels in 4 splits) or a tile.  (Rows at odd addresses, and ones too far
+ *   apart for 32-bit offsets, take kernels with other loads.)
  */
 typedef enum { QP_MX_A4W4 = 0, QP_MX_W4 = 1, QP_MX_W4_DX = 2 } qp_mx_product;
 qp_status qgemm_mx_kernel_name(int32_t product, int64_t M, const qp_mx4* w, int32_t dtype,

@@ -348,3 +348,34 @@ def test_one_block_that_is_no_f16_values(qp, product, kernel, M, N):
             else:
                 got, v = qp.qgemm_w4_mx(X, W, out_dtype=torch.float32), w.t().contiguous()
                 _close(got, x @ v, x.abs() @ v.abs(), K, "f32", "odd=%s" % odd)
+
+
+@pytest.mark.parametrize("product,dtype", [("a4w4", "bf16"), ("w4", "f16"), ("w4_dx", "bf16")])
+def test_large_tiles_of_many_experts(qp, product, dtype):
+    """More experts than a wave has lanes, in 256 x 256 tiles, a last round in halves."""
+    import torch
+    g = torch.Generator().manual_seed(70)
+    E, K, N = 130, 130, 1000
+    counts = torch.randint(0, 2000, (E,), generator=g)
+    counts[3] = counts[64] = counts[129] = 0
+    off = torch.cat((torch.zeros(1, dtype=torch.long), counts.cumsum(0)))
+    S = int(off[E]) + 77
+    W, w = _matrix(qp, g, E, K, N) if product == "w4_dx" else _matrix(qp, g, E, N, K)
+    print("mx4 many experts", product, dtype, S, flush=True)
+    assert qp.qgemm_mx_kernel_name(product, S, W, _dt(dtype)).split("/")[0] == "tile256x256"
+    offsets = off.int().cuda()
+    if product == "a4w4":
+        X, x = _matrix(qp, g, S, K)
+        got = qp.qgemm_a4w4_mx_experts(X, W, offsets, out_dtype=_dt(dtype))
+    else:
+        X, x = _rows(g, S, K, dtype)
+        got = (qp.qgemm_w4_mx_experts if product == "w4" else qp.qgemm_w4_mx_experts_dx)(
+            X, W, offsets)
+    want = torch.zeros(S, N, dtype=torch.float64, device="cuda")
+    A = torch.zeros_like(want)
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        v = w[e] if product == "w4_dx" else w[e].t().contiguous()
+        want[s], A[s] = x[s] @ v, x[s].abs() @ v.abs()
+    _close(got, want, A, K, dtype, "many experts")
+    assert not got[int(off[E]):].any()
