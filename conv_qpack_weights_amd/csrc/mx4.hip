@@ -57,7 +57,7 @@ constexpr MxCost kW4Shapes[] = {
     {kMxRows16x64, 16, 64, 8.3, 11.4, 6.0, "rows16x64"},
     {kMxTile32x64, 32, 64, 15.7, 11.0, 6.5, "tile32x64"},
     {kMxTile32x128, 32, 128, 19.8, 20.0, 14.0, "tile32x128"},
-    {kMxTile128x128, 128, 128, 35.0, 29.0, 30.0, "tile128x128"},
+    {kMxTile128x128, 128, 128, 34.0, 29.0, 29.0, "tile128x128"},
     {kMxTile256x256, 256, 256, 103.0, 100.0, 100.0, "tile256x256"},
 };
 // The same of f32 rows: 16 x 4096 14.1, 14.8, 15.4, 16.6; 16 x 11008 38, 34, 19.6, 20.8; 64 x

@@ -89,19 +89,10 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
     abase += first * a.a.ldc;
     sabase += first * a.a.lds;
   }
-  auto source = [&](int row) {
-    int64_t r = tile.r0 + row;
-    r = r < tile.r1 ? r : tile.r1 - 1;
-    const int64_t x = w4_source_row(a.rows, r);
-    return x < 0 ? INT64_C(0) : x - first;
-  };
   const uint8_t* const wbase = a.w.codes + tile.expert * a.w.cstride + n0 * a.w.ldc;
   const uint8_t* const swbase = a.w.scales + tile.expert * a.w.sstride + n0 * a.w.lds;
   const int64_t last_n = N - 1 - n0;
   uint32_t va[kA], vb[kB], vs[kS];
-#pragma unroll
-  for (int j = 0; j < kA; ++j)
-    va[j] = (uint32_t)(source((wave * kA + j) * 8 + lrow) * a.a.ldc) + piece(j) * 16;
 #pragma unroll
   for (int j = 0; j < kB; ++j) {
     const int64_t n = (wave * kB + j) * 8 + lrow;
@@ -113,13 +104,19 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
     const int i = wave * kS + j;
     return i < kSI ? i : kSI - 1;
   };
+  int64_t x[kA + kS];
+  mx_sources(a.rows, tile, first, [&](int i) {
+    return i < kA ? (wave * kA + i) * 8 + lrow : scale_part(i - kA) * kSRows + srow;
+  }, x);
+#pragma unroll
+  for (int j = 0; j < kA; ++j) va[j] = (uint32_t)(x[j] * a.a.ldc) + piece(j) * 16;
 #pragma unroll
   for (int j = 0; j < kS; ++j) {
-    const int i = scale_part(j), row = i * kSRows + srow;
+    const int i = scale_part(j);
     if (i * kSRows < BM) {
-      vs[j] = (uint32_t)(source(row) * a.a.lds) + sdw * 4;
+      vs[j] = (uint32_t)(x[kA + j] * a.a.lds) + sdw * 4;
     } else {
-      const int64_t n = row - BM;
+      const int64_t n = i * kSRows + srow - BM;
       vs[j] = (uint32_t)((n < last_n ? n : last_n) * a.w.lds) + sdw * 4;
     }
   }
@@ -353,7 +350,7 @@ constexpr MxCost kA4Shapes[] = {
     {kMxRows16x16, 16, 16, 4.9, 2.4, 1.6, "rows16x16"},
     {kMxRows16x32, 16, 32, 5.6, 4.1, 1.9, "rows16x32"},
     {kMxTile64x64, 64, 64, 8.1, 10.0, 4.4, "tile64x64"},
-    {kMxTile128x128, 128, 128, 19.0, 26.0, 11.5, "tile128x128"},
+    {kMxTile128x128, 128, 128, 18.0, 25.0, 11.0, "tile128x128"},
     {kMxTile256x256, 256, 256, 44.0, 40.0, 40.0, "tile256x256"},
 };
 

@@ -531,7 +531,36 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
       all(false_type{});
     }
 
-    // out: 32 rows at a time through the wave's own LDS
+    // where all the wave's columns are there a lane has 16 neighbouring ones of a row, twice
+    if (k0 + wn * 64 + 64 <= K) {
+      auto store = [&](auto* X) {
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          const int64_t r = tile.r0 + (wm * F + f) * 32 + l32;
+          if (r < tile.r1) {
+            auto* const at = X + r * a.lddx + k0 + wn * 64 + 16 * half;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float y[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                  y[t] = acc[t % 4 / 2][f][t % 2 * 8 + 4 * s + 2 * h + t / 4];
+                mx_store8(at + 32 * s + 8 * h, y);
+              }
+          }
+        }
+      };
+      if (a.dtype == QP_F32)
+        store(static_cast<float*>(a.dX));
+      else if (a.dtype == QP_BF16)
+        store(static_cast<bf16_t*>(a.dX));
+      else
+        store(static_cast<f16_t*>(a.dX));
+      return;
+    }
+    // else 32 rows at a time through the wave's own LDS
     float* const out = reinterpret_cast<float*>(mx_lds) + wave * 32 * L::kOutLd;
     const int p8 = lane & 7, row_in = lane >> 3;
     const int64_t col = k0 + wn * 64 + p8 * 8;

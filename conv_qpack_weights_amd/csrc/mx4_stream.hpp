@@ -53,12 +53,9 @@ __global__ __launch_bounds__(kWaves * 64) void mx_stream_kernel(MxArgs a, uint32
   // repeat its last row
   const int lrow = lane >> 3;
   int64_t first = a.rows.map ? 0 : tile.r0;
-  auto source = [&](int row) {
-    int64_t r = tile.r0 + row;
-    r = r < tile.r1 ? r : tile.r1 - 1;
-    const int64_t x = w4_source_row(a.rows, r);
-    return x < 0 ? INT64_C(0) : x - first;
-  };
+  int64_t source[kA4 ? 3 : 2];
+  mx_sources(a.rows, tile, first,
+             [&](int i) { return i < 2 ? i * 8 + lrow : lane >> 1 & 15; }, source);
   auto piece = [&](int h) { return (lane & 7) ^ mx_turn(h * 8 + lrow); };
   const uint8_t* const wbase = a.w.codes + tile.expert * a.w.cstride + n0 * a.w.ldc;
   const uint8_t* const swbase = a.w.scales + tile.expert * a.w.sstride + n0 * a.w.lds;
@@ -76,7 +73,7 @@ __global__ __launch_bounds__(kWaves * 64) void mx_stream_kernel(MxArgs a, uint32
   uint32_t vx[2], vw[kTiles][2], vs[L::kScaleLoads], vsx = 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    vx[h] = (uint32_t)(source(h * 8 + lrow) * xld) + piece(h) * 16;
+    vx[h] = (uint32_t)(source[h] * xld) + piece(h) * 16;
 #pragma unroll
     for (int c = 0; c < kTiles; ++c) {
       const int64_t n = c * 16 + h * 8 + lrow;
@@ -88,7 +85,7 @@ __global__ __launch_bounds__(kWaves * 64) void mx_stream_kernel(MxArgs a, uint32
     const int64_t n = i * 32 + (lane >> 1);
     vs[i] = (uint32_t)((n < last_n ? n : last_n) * a.w.lds) + (lane & 1) * 4;
   }
-  if constexpr (kA4) vsx = (uint32_t)(source((lane >> 1) & 15) * a.a.lds) + (lane & 1) * 4;
+  if constexpr (kA4) vsx = (uint32_t)(source[2] * a.a.lds) + (lane & 1) * 4;
 
   // 256 K from 256 g on into buffer g & 1; past the wave's last nothing is asked for
   const int groups = (int)(a.w.K / 256), per = (groups + kWaves - 1) / kWaves;

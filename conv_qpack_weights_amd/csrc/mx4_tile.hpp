@@ -42,6 +42,37 @@ __device__ __forceinline__ f32x16 mx_mfma_f16(f16x8 a, f16x8 b, f32x16 d) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, d, 0, 0, 0);
 }
 
+// Entry m of a map of rows (w4_source_row without branches: a lane's entries are loaded
+// one after another and waited for once): the row it stands for, 0 where it is none.
+__device__ __forceinline__ bool mx_has_source(const W4Rows& rows, int32_t m) {
+  return m >= 0 && (uint32_t)m / (uint32_t)rows.map_div < rows.x_rows;
+}
+__device__ __forceinline__ int64_t mx_source(const W4Rows& rows, int32_t m) {
+  return mx_has_source(rows, m) ? (uint32_t)m / (uint32_t)rows.map_div : 0;
+}
+
+// The rows of X that rows r0 + row(i), i < kN, of a tile read, from row `first` on: those
+// past the tile's end repeat its last row.
+template <int kN, typename Row>
+__device__ __forceinline__ void mx_sources(const W4Rows& rows, const W4Tile& tile, int64_t first,
+                                           Row row, int64_t (&x)[kN]) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int64_t r = tile.r0 + row(i);
+    x[i] = r < tile.r1 ? r : tile.r1 - 1;
+  }
+  if (rows.map) {
+    int32_t m[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) m[i] = rows.map[x[i]];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) x[i] = mx_source(rows, m[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) x[i] -= first;
+  }
+}
+
 // Which tile a workgroup takes: eight row tiles by neighbouring channel groups, in
 // runs per XCD.
 __device__ __forceinline__ void mx_place_of(uint32_t id, uint32_t row_slots, uint32_t col_groups,
@@ -132,6 +163,92 @@ inline qp_status mx_reserve_lds(const char* what, const void* kern, int bytes,
 
 constexpr int mx_out_ld(int FN) { return 32 * FN + 4; }
 
+// Eight neighbouring outputs to p.
+template <typename T>
+__device__ __forceinline__ void mx_store8(T* p, const float (&y)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
+    store_piece(p, lo, 4);
+    store_piece(p + 4, hi, 4);
+  } else {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    u32x4_any v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 two = {y[2 * i], y[2 * i + 1]};
+      if constexpr (__is_same(T, f16_t)) {
+        typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+        v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, f16x2));
+      } else {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, bf16x2));
+      }
+    }
+    *reinterpret_cast<u32x4_any*>(p) = v;
+  }
+}
+
+// (Against the way through LDS below, 128 x 128 tiles: a4w4 2048 x 4096 x 4096 26.7 -> 24.9
+// us, bf16 2048 tokens x 2 of 8 experts of 4096 x 4096 165 -> 159.  256 x 256 tiles, whose
+// CUs all store at once, took 3 us longer with its 32 bytes of a row at a time.)
+// A wave's sums to Y where all its channels are there: a lane holds one row and, of 16
+// channels, runs of four 8 apart, the other half of the wave the runs between; halves
+// swapped, each has eight neighbouring channels.
+template <typename T, int FM, int FN>
+__device__ __forceinline__ void mx_store_whole(const f32x16 (&acc)[FN][FM], const MxArgs& a,
+                                               const W4Tile& tile, int row0, int64_t col0) {
+  const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
+  int64_t row[FM];
+#pragma unroll
+  for (int j = 0; j < FM; ++j) row[j] = tile.r0 + row0 + j * 32 + l32;
+  bool none[FM] = {};
+  if (a.rows.map) {
+    int32_t m[FM];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) m[j] = a.rows.map[row[j] < tile.r1 ? row[j] : tile.r1 - 1];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) none[j] = !mx_has_source(a.rows, m[j]);
+  }
+  const bool bounds = a.lo > -INFINITY || a.hi < INFINITY;
+  T* const Y = static_cast<T*>(a.Y) + col0 + half * 8;
+  const float* const bias = a.bias ? a.bias + tile.expert * a.w.rows + col0 + half * 8 : nullptr;
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      const int c = i * 32 + q * 8;
+      float b[8] = {};
+      if (bias) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) b[t] = bias[c + t];
+      }
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        float y[8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float lo = acc[i][j][4 * q + t], hi = acc[i][j][4 * q + 4 + t];
+          const auto two = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, lo),
+                                                            __builtin_bit_cast(uint32_t, hi),
+                                                            false, false);
+          const uint32_t mine = two[0], other = two[1];
+          y[t] = __builtin_bit_cast(float, mine);
+          y[4 + t] = __builtin_bit_cast(float, other);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) y[t] = (none[j] ? 0.0f : y[t]) + b[t];
+        if (bounds) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const float v = y[t] < a.lo ? a.lo : y[t];
+            y[t] = v > a.hi ? a.hi : v;
+          }
+        }
+        if (row[j] < tile.r1) mx_store8(Y + row[j] * a.ldy + c, y);
+      }
+    }
+}
+
 // A wave's sums (weights the first operand of its 32x32 MFMAs: a lane holds one row
 // and runs of four channels) to Y: 32 rows at a time through `out`, the wave's own
 // LDS of 32 mx_out_ld(FN) floats, so that a lane stores eight neighbouring channels.
@@ -143,6 +260,15 @@ __device__ __forceinline__ void mx_store_tile(const f32x16 (&acc)[FN][FM], const
                                               float* out) {
   constexpr int kLd = mx_out_ld(FN);
   constexpr int kPieces8 = 4 * FN, kRowsPass = 64 / kPieces8;
+  if (FM <= 2 && col0 + 32 * FN <= a.w.rows) {
+    if (a.y_dtype == QP_F32)
+      mx_store_whole<float, FM, FN>(acc, a, tile, row0, col0);
+    else if (a.y_dtype == QP_BF16)
+      mx_store_whole<bf16_t, FM, FN>(acc, a, tile, row0, col0);
+    else
+      mx_store_whole<f16_t, FM, FN>(acc, a, tile, row0, col0);
+    return;
+  }
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
   const int p8 = lane % kPieces8, row_in = lane / kPieces8;
   const int64_t N = a.w.rows, col = col0 + p8 * 8;
@@ -150,6 +276,22 @@ __device__ __forceinline__ void mx_store_tile(const f32x16 (&acc)[FN][FM], const
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     bias[j] = a.bias && col + j < N ? a.bias[tile.expert * N + col + j] : 0.0f;
+  // which of the lane's rows have no source
+  uint32_t none = 0;
+  if (a.rows.map) {
+    constexpr int kPasses = FM * (32 / kRowsPass);
+    int32_t m[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int64_t r = tile.r0 + row0 + i * kRowsPass + row_in;
+      m[i] = a.rows.map[r < tile.r1 ? r : tile.r1 - 1];
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) none |= mx_has_source(a.rows, m[i]) ? 0u : 1u << i;
+  }
+  // (no load is under way in the loop: waiting for one would be waiting for the stores
+  // before it, a microsecond a pass)
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
 #pragma unroll 1
   for (int f = 0; f < FM; ++f) {
 #pragma unroll
@@ -171,16 +313,24 @@ __device__ __forceinline__ void mx_store_tile(const f32x16 (&acc)[FN][FM], const
         const float* src = out + (h + row_in) * kLd + p8 * 8;
         const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
         const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 4);
-        const bool none = w4_source_row(a.rows, r) < 0;
         float y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float v = (none ? 0.0f : j < 4 ? lo[j % 4] : hi[j % 4]) + bias[j];
+          float v = (none & 1 ? 0.0f : j < 4 ? lo[j % 4] : hi[j % 4]) + bias[j];
           v = v < a.lo ? a.lo : v;
           y[j] = v > a.hi ? a.hi : v;
         }
-        w4_store8(a.Y, a.y_dtype, r * a.ldy + col, y, N - col < 8 ? (int)(N - col) : 8);
+        const int64_t at = r * a.ldy + col;
+        if (N - col < 8)
+          w4_store8(a.Y, a.y_dtype, at, y, (int)(N - col));
+        else if (a.y_dtype == QP_F32)
+          mx_store8(static_cast<float*>(a.Y) + at, y);
+        else if (a.y_dtype == QP_BF16)
+          mx_store8(static_cast<bf16_t*>(a.Y) + at, y);
+        else
+          mx_store8(static_cast<f16_t*>(a.Y) + at, y);
       }
+      none >>= 1;
     }
     wave_sync();
   }

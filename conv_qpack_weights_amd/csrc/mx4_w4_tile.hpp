@@ -90,23 +90,18 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
     first = tile.r0;
     xbase += first * a.ldx;
   }
-  auto source = [&](int row) {
-    int64_t r = tile.r0 + row;
-    r = r < tile.r1 ? r : tile.r1 - 1;
-    const int64_t x = w4_source_row(a.rows, r);
-    return x < 0 ? INT64_C(0) : x - first;
-  };
+  int64_t source[kA];
+  mx_sources(a.rows, tile, first, [&](int j) { return (wave * kA + j) * 8 + lrow; }, source);
   uint32_t vx[kDirect ? kA : 1];
   const T* px[kDirect ? 1 : kSlots];
   if constexpr (kDirect) {
 #pragma unroll
     for (int j = 0; j < kA; ++j)
-      vx[j] = (uint32_t)(source((wave * kA + j) * 8 + lrow) * a.ldx * (int64_t)sizeof(T)) +
-              piece(j) * 16;
+      vx[j] = (uint32_t)(source[j] * a.ldx * (int64_t)sizeof(T)) + piece(j) * 16;
   } else {
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
-      px[j] = xbase + source((wave * kSlots + j) * 8 + lrow) * a.ldx;
+      px[j] = xbase + source[j] * a.ldx;
   }
   const uint8_t* const wbase = a.w.codes + tile.expert * a.w.cstride + n0 * a.w.ldc;
   const uint8_t* const swbase = a.w.scales + tile.expert * a.w.sstride + n0 * a.w.lds;
@@ -393,7 +388,9 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
           const int row = (wave * kA + j) * 8 + lrow;
           if (row >= BM) break;
           const int64_t k = (int64_t)full * 64 + piece(j) * 8, left = K - k;
-          const T* p = xbase + source(row) * a.ldx;
+          int64_t x[1];
+          mx_sources(a.rows, tile, first, [&](int) { return row; }, x);
+          const T* p = xbase + x[0] * a.ldx;
           const Piece<T> one =
               load_piece(p + (left > 0 ? k : 0), left > 8 ? 8 : left < 0 ? 0 : (int)left);
           *(__attribute__((address_space(3))) u32x4*)(to + row * 128 + (lane & 7) * 16) = one.v;
