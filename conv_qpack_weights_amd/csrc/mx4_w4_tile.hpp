@@ -191,23 +191,27 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
         o.s[i] = mx_scale(st[(brow + i * 32) * 8 + 2 * p + half]);
       }
     };
-    auto multiply = [&](const Rows& x, const Weights& w, int step, auto kind) {
-      if constexpr (decltype(kind)::value) {
-        f16x8 v[FN];
+    // a step's weights as operands, and the step
+    auto unpack = [&](u32x4 (&v)[FN], const Weights& w, int step, auto kind) {
 #pragma unroll
-        for (int i = 0; i < FN; ++i) v[i] = mx_unpack_f16(w.q[i][step], w.s[i]);
+      for (int i = 0; i < FN; ++i) {
+        if constexpr (decltype(kind)::value)
+          v[i] = __builtin_bit_cast(u32x4, mx_unpack_f16(w.q[i][step], w.s[i]));
+        else
+          v[i] = __builtin_bit_cast(u32x4, mx_unpack(w.q[i][step], w.s[i]));
+      }
+    };
+    auto multiply = [&](const Rows& x, const u32x4 (&v)[FN], auto kind) {
+      constexpr bool kAsF16 = decltype(kind)::value;
+      constexpr int kPieces = kAsF16 ? 1 : kF16 ? 2 : NP;
 #pragma unroll
-        for (int j = 0; j < F; ++j)
+      for (int j = 0; j < F; ++j) {
+        if constexpr (kAsF16) {
 #pragma unroll
           for (int i = 0; i < FN; ++i)
-            acc[i][j] = mx_mfma_f16(v[i], __builtin_bit_cast(f16x8, x.x[j][0]), acc[i][j]);
-      } else {
-        constexpr int kPieces = kF16 ? 2 : NP;
-        bf16x8 v[FN];
-#pragma unroll
-        for (int i = 0; i < FN; ++i) v[i] = mx_unpack(w.q[i][step], w.s[i]);
-#pragma unroll
-        for (int j = 0; j < F; ++j) {
+            acc[i][j] = mx_mfma_f16(__builtin_bit_cast(f16x8, v[i]),
+                                    __builtin_bit_cast(f16x8, x.x[j][0]), acc[i][j]);
+        } else {
           bf16x8 xv[kPieces];
           if constexpr (kF16)
             MxFrag<f16_t>{x.x[j][0]}.split(xv);
@@ -217,7 +221,8 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
 #pragma unroll
           for (int i = 0; i < FN; ++i)
 #pragma unroll
-            for (int n = 0; n < kPieces; ++n) acc[i][j] = mx_mfma_bf16(v[i], xv[n], acc[i][j]);
+            for (int n = 0; n < kPieces; ++n)
+              acc[i][j] = mx_mfma_bf16(__builtin_bit_cast(bf16x8, v[i]), xv[n], acc[i][j]);
         }
       }
     };
@@ -308,29 +313,46 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
       if constexpr (kDirect) issue_x(D - 1);
       issue_w(L::kAhead, 0);
       issue_s(L::kAhead);
+      // a step's unpacking in between the MFMAs of the one before (4096 tokens x 2 of 8 experts
+      // of 11008 x 4096 bf16 688 us without, 671 with)
+      auto mix = [&] {
+#pragma unroll
+        for (int i = 0; i < F * FN; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // an MFMA
+          __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);  // VALU instructions
+        }
+      };
       auto look = [&] {
         if constexpr (decltype(kind)::value)
 #pragma unroll
           for (int i = 0; i < FN; ++i) out |= !mx_f16_scale(now.s[i]);
       };
       if constexpr (kDirect) {
+        u32x4 va[FN], vb[FN];
         read_x(even, 0, 0);
         read_w(now, 0);
+        unpack(va, now, 0, kind);
         // (no branch between MFMAs: the compiler would move them past it, behind the
         // barrier)
         auto steps = [&](int s, auto place) {
           read_x(odd, s, 1);
           __builtin_amdgcn_sched_barrier(0);
-          multiply(even, now, 0, kind);
+          unpack(vb, now, 1, kind);
+          multiply(even, va, kind);
+          mix();
           __builtin_amdgcn_sched_barrier(0);
           read_x(even, s, 2);
           __builtin_amdgcn_sched_barrier(0);
-          multiply(odd, now, 1, kind);
+          unpack(va, now, 2, kind);
+          multiply(odd, vb, kind);
           look();
+          mix();
           __builtin_amdgcn_sched_barrier(0);
           read_x(odd, s, 3);
           __builtin_amdgcn_sched_barrier(0);
-          multiply(even, now, 2, kind);
+          unpack(vb, now, 3, kind);
+          multiply(even, va, kind);
+          mix();
           __builtin_amdgcn_sched_barrier(0);
           arrive(place);
           // (which first: 4096^3 by 256 x 256 tiles 106 us loads first, 103 last; 1024 x 4096 x
@@ -339,10 +361,11 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
           read_x(even, s + 1, 0);
           read_w(next, s + 1);
           __builtin_amdgcn_sched_barrier(0);
-          multiply(odd, now, 3, kind);
+          multiply(odd, vb, kind);
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (BM >= 256) issue(s, place);
           now = next;
+          unpack(va, now, 0, kind);
         };
         if (tile.r0 + wm * 32 * F >= tile.r1) {
           // (a wave without rows only loads, and leaves its SIMD to the others)
@@ -360,8 +383,10 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
           look();
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
+            u32x4 v[FN];
             read_x(even, s, t);
-            multiply(even, now, t, kind);
+            unpack(v, now, t, kind);
+            multiply(even, v, kind);
           }
           put(f, s + 1);
           arrive(place);
@@ -407,8 +432,10 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
+        u32x4 v[FN];
         read_x(even, full, t);
-        multiply(even, now, t, false_type{});
+        unpack(v, now, t, false_type{});
+        multiply(even, v, false_type{});
       }
       __syncthreads();
     }

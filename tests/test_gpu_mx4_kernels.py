@@ -379,3 +379,24 @@ def test_large_tiles_of_many_experts(qp, product, dtype):
         want[s], A[s] = x[s] @ v, x[s].abs() @ v.abs()
     _close(got, want, A, K, dtype, "many experts")
     assert not got[int(off[E]):].any()
+
+
+@pytest.mark.parametrize("product,dtype,kernel,M,N", [c for c in PRODUCTS if c[4] < 9000])
+def test_bounds_in_every_kernel(qp, product, dtype, kernel, M, N):
+    """Bounds on either side and both, after the bias, are a clamp of the result without."""
+    import torch
+    g = torch.Generator().manual_seed(M)
+    K = 330
+    W, w = _matrix(qp, g, N, K)
+    assert qp.qgemm_mx_kernel_name(product, M, W, _dt(dtype)) == kernel
+    print("mx4 bounds", product, dtype, kernel, M, N, flush=True)
+    bias = torch.randn(N, generator=g).cuda()
+    if product == "a4w4":
+        X, run = _matrix(qp, g, M, K)[0], qp.qgemm_a4w4_mx
+    else:
+        X, run = _rows(g, M, K, dtype)[0], qp.qgemm_w4_mx
+    free = run(X, W, bias, out_dtype=torch.float32)
+    inf = float("inf")
+    for lo, hi in ((-0.5, inf), (-inf, 0.25), (-0.5, 0.25), (0.0, 0.0)):
+        got = run(X, W, bias, lo, hi, out_dtype=_dt(dtype))
+        assert torch.equal(got, free.clamp(lo, hi).to(_dt(dtype))), (lo, hi)
