@@ -492,7 +492,13 @@ qp_status mx_run_16bit(const MxArgs& a, hipStream_t stream) {
     case kMxTile32x128:
       return mx_read_once(a, 32) ? mx_launch_w4_tile<T, true, 32, 128, 1, 4, 4, true>(a, stream)
                                  : mx_launch_w4_tile<T, true, 32, 128, 1, 4, 4>(a, stream);
-    case kMxTile128x128: return mx_launch_w4_tile<T, true, 128, 128, 2, 2, 2>(a, stream);
+    // Up to one to a CU, with loads of rows and weights further ahead; else two to a CU
+    // (256 x 11008 x 4096 bf16 38 and 49 us, 1024 x 4096 x 4096 39.4 and 40.4; two rounds of
+    // the first, 1536 x 4096 x 4096, 70 and 54).
+    case kMxTile128x128:
+      return w4_tile_slots(a.rows, 128) * ceil_div(a.w.rows, 128) <= 256
+                 ? mx_launch_w4_tile<T, true, 128, 128, 2, 2, 4>(a, stream)
+                 : mx_launch_w4_tile<T, true, 128, 128, 2, 2, 2>(a, stream);
     default: break;
   }
   return mx_launch_w4_tile<T, true, 256, 256, 2, 4, 2>(a, stream);
