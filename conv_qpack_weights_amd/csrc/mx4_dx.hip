@@ -190,6 +190,9 @@ __global__ __launch_bounds__(256) void mx_dx_sum_kernel(const float* __restrict_
 // workgroup.  In that buffer column 4u + j of a wave's 64 is row 16 j + u: 16 threads
 // then write 16 rows, whose places meet every bank alike (mx_turn).
 // f16 rows: as there, again from the start where a weight turns out to be no f16 value.
+// 4096^3, 256 x 256 tiles: bf16 117 us (1.17 PFLOP/s), f16 122; 1024 x 4096 x 4096 by 128 x 128
+// 49 (rows loaded further ahead: no faster, one wave a SIMD has the conversion, 16 small LDS
+// reads and 4 writes, between its MFMAs).
 template <typename T, int BM, int BC, int WM, int WN>
 struct MxDxTile {
   static constexpr int NW = WM * WN, FM = BM / (32 * WM);
@@ -332,35 +335,39 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
   // (there: whether this is a stage at all; f16 weights: `out` is set where one is no
   // f16 value)
   bool out = false;
-  auto convert = [&](const Raw& w, int s, auto kind, bool there) {
-    uint32_t c[8][2];
+  // channels 2 r and 2 r + 1 of a share: word r of its four columns' operands
+  auto pair_up = [&](u32x4 (&v)[4], const Raw& w, int r, auto kind, bool there) {
+    uint32_t c[2][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float by = mx_scale(w.s[i]);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t q = w.q[2 * r + i];
+      const float by = mx_scale(w.s[2 * r + i]);
       if constexpr (decltype(kind)::value) {
         out |= there && !mx_f16_scale(by);
-        c[i][0] = __builtin_bit_cast(
-            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 0));
-        c[i][1] = __builtin_bit_cast(
-            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w.q[i], by, 1));
+        c[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, by, 0));
+        c[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, by, 1));
       } else {
-        c[i][0] = __builtin_bit_cast(
-            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.q[i], by, 0));
-        c[i][1] = __builtin_bit_cast(
-            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.q[i], by, 1));
+        c[i][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, by, 0));
+        c[i][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, by, 1));
       }
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j][r] = j & 1 ? hi_halves(c[0][j / 2], c[1][j / 2]) : lo_halves(c[0][j / 2], c[1][j / 2]);
+  };
+  auto put_w = [&](const u32x4 (&v)[4], int s) {
     lds_u8* const to = wbuf + (s & 1) * L::kW;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      u32x4 v;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        v[r] = j & 1 ? hi_halves(c[2 * r][j / 2], c[2 * r + 1][j / 2])
-                     : lo_halves(c[2 * r][j / 2], c[2 * r + 1][j / 2]);
       const int row = u / 16 * 64 + j * 16 + u % 16;
-      *(__attribute__((address_space(3))) u32x4*)(to + row * 128 + (g ^ mx_turn(row)) * 16) = v;
+      *(__attribute__((address_space(3))) u32x4*)(to + row * 128 + (g ^ mx_turn(row)) * 16) = v[j];
     }
+  };
+  auto convert = [&](const Raw& w, int s, auto kind, bool there) {
+    u32x4 v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) pair_up(v, w, r, kind, there);
+    put_w(v, s);
   };
 
   // F x FN operands a wave
@@ -449,27 +456,46 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
         if constexpr (kDirect) {
           issue_x(1);
           read(even, 0, 0);
+          read_w(raw, 1);
           // (no branch between MFMAs, as in the products)
           if (tile.r0 + wm * 32 * F < tile.r1) {
+            // (the next stage's conversion spread over this one's MFMAs: 4096^3 f16 128 us in
+            // one piece, 122 so)
+            auto mix = [&] {
+#pragma unroll
+              for (int i = 0; i < F * FN; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // an MFMA
+                __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);  // VALU instructions
+              }
+            };
             for (int s = 0; s < full; ++s) {
+              const bool there = s + 1 < full;
+              u32x4 v[4];
               read(odd, s, 1);
               __builtin_amdgcn_sched_barrier(0);
+              pair_up(v, raw, 0, kind, there);
               multiply(even, kind);
+              mix();
               __builtin_amdgcn_sched_barrier(0);
               read(even, s, 2);
-              read_w(raw, s + 1);
               __builtin_amdgcn_sched_barrier(0);
+              pair_up(v, raw, 1, kind, there);
+              pair_up(v, raw, 2, kind, there);
               multiply(odd, kind);
+              mix();
               __builtin_amdgcn_sched_barrier(0);
               read(odd, s, 3);
               __builtin_amdgcn_sched_barrier(0);
-              convert(raw, s + 1, kind, s + 1 < full);
+              pair_up(v, raw, 3, kind, there);
+              put_w(v, s + 1);
               multiply(even, kind);
+              mix();
               __builtin_amdgcn_sched_barrier(0);
               arrive();
               issue_w(s + 3);
               issue_x(s + 2);
               read(even, s + 1, 0);
+              read_w(raw, s + 2);
               __builtin_amdgcn_sched_barrier(0);
               multiply(odd, kind);
               __builtin_amdgcn_sched_barrier(0);
