@@ -61,14 +61,14 @@ constexpr MxCost kW4Shapes[] = {
     {kMxTile256x256, 256, 256, 103.0, 100.0, 100.0, "tile256x256"},
 };
 // The same of f32 rows: 16 x 4096 14.1, 14.8, 15.4, 16.6; 16 x 11008 38, 34, 19.6, 20.8; 64 x
-// 11008 112, 84, 58, 52, 128 x 128 tiles 125; 128 x 4096 78, 56, 40, 33, 121; 4096 x 4096 tiles
-// 510.
+// 11008 112, 84, 58, 52; 128 x 4096 78, 56, 40, 33; 128 x 128 tiles 512 x 4096 109, 1024 x 4096
+// 115, 4096 x 4096 454.
 constexpr MxCost kW4ShapesF32[] = {
     {kMxRows16x16, 16, 16, 14.1, 9.2, 9.2, "rows16x16"},
     {kMxRows16x32, 16, 32, 15.2, 13.5, 13.5, "rows16x32"},
     {kMxRows16x48, 16, 48, 16.0, 13.5, 13.5, "rows16x48"},
     {kMxRows16x64, 16, 64, 17.5, 16.0, 16.0, "rows16x64"},
-    {kMxTile128x128, 128, 128, 122.0, 125.0, 125.0, "tile128x128"},
+    {kMxTile128x128, 128, 128, 111.0, 111.0, 111.0, "tile128x128"},
 };
 
 }  // namespace

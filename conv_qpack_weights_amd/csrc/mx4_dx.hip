@@ -511,17 +511,32 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
             }
           }
         } else {
+          // two pieces of the next stage's rows are cut and put down and two of the stage after
+          // it loaded with each of the first two steps (4096^3 f32: all at the stage's ends
+          // 600 us, so 556)
+          static_assert(kDirect || kA == 4, "pieces of a step");
+          fetch_full(f, full > 1 ? 1 : 0);
           for (int s = 0; s < full; ++s) {
-            fetch_full(f, s + 1 < full ? s + 1 : s);
+            const int after = s + 2 < full ? s + 2 : full - 1;
             read_w(raw, s + 1);
-            convert(raw, s + 1, kind, s + 1 < full);
+            read(even, s, 0);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              read(even, s, t);
-              multiply(even, kind);
-            }
+              if (t < 3) read(t % 2 ? even : odd, s, t + 1);
+              __builtin_amdgcn_sched_barrier(0);
+              multiply(t % 2 ? odd : even, kind);
+              if (t < 2) {
 #pragma unroll
-            for (int j = 0; j < kA; ++j) put(f[j], s + 1, j);
+                for (int p = 0; p < 2; ++p) {
+                  const int j = (2 * t + p) % kA;
+                  put(f[j], s + 1, j);
+                  f[j].load(px[kDirect ? 0 : j] + (int64_t)after * 64 + piece(j) * 8);
+                }
+              } else if (t == 2) {
+                convert(raw, s + 1, kind, s + 1 < full);
+              }
+              __builtin_amdgcn_sched_barrier(0);
+            }
             arrive();
             issue_w(s + 3);
           }
@@ -646,7 +661,7 @@ qp_status launch_dx_tile(const char* what, const MxDxArgs& a, hipStream_t stream
 //
 // Measured, bf16, 4096 x 4096 weights, cold: 16 rows 11.6 us by the few-row kernel (128 x
 // 128 tiles 46), 256 37 (47), 512 71 (49; 256 x 256 tiles 96), 1024 132 (52), 2048 248 (81, 97),
-// 4096 456 (156, 119); of 11008 columns 1024 rows 332 (118, 100).  f32 rows: 256 56 (147), 768
+// 4096 456 (156, 119); of 11008 columns 1024 rows 332 (118, 100).  f32 rows: 256 53, 512 94, 768 147; tiles 1024 137, 4096 556.
 // 147 (149), 4096 682 (572).
 constexpr int kDxWaves = 8;
 struct DxPlan {
@@ -673,7 +688,7 @@ DxPlan dx_plan(int32_t dtype, int64_t M, const qp_mx4* w) {
   };
   const bool f32 = dtype == QP_F32;
   const double c0 = f32 ? 9.0 + 21.5 * few : 9.0 + 15.0 * few;
-  const double c128 = f32 ? cost(t128, 142.0, 10.0, 140.0) : cost(t128, 46.0, 6.0, 36.0);
+  const double c128 = f32 ? cost(t128, 127.0, 10.0, 138.0) : cost(t128, 46.0, 6.0, 36.0);
   const double c256 = f32 ? 1e300 : cost(t256, 94.0, 25.0, 115.0);
   DxPlan p{0, 1};
   if (c128 < c0 || c256 < c0) {

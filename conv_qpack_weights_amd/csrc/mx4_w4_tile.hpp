@@ -240,21 +240,22 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
       for (int j = 0; j < kSlots; ++j)
         f[j].load(px[kDirect ? 0 : j] + (int64_t)s * 64 + piece(j) * 8);
     };
-    auto put = [&](const MxFrag<T> (&f)[kSlots], int s) {
-      lds_u8* const to = xbuf + (s % D) * L::kX;
+    auto put_one = [&](const MxFrag<T>& f, int s, int j) {
+      lds_u8* const at = xbuf + (s % D) * L::kX + ((wave * kSlots + j) * 8 + lrow) * 128 +
+                         (lane & 7) * 16;
+      if constexpr (NP == 1) {
+        *(__attribute__((address_space(3))) u32x4*)at = f.v;
+      } else {
+        bf16x8 v[NP];
+        f.split(v);
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
-        lds_u8* const at = to + ((wave * kSlots + j) * 8 + lrow) * 128 + (lane & 7) * 16;
-        if constexpr (NP == 1) {
-          *(__attribute__((address_space(3))) u32x4*)at = f[j].v;
-        } else {
-          bf16x8 v[NP];
-          f[j].split(v);
-#pragma unroll
-          for (int i = 0; i < NP; ++i)
-            *(__attribute__((address_space(3))) bf16x8*)(at + i * BM * 128) = v[i];
-        }
+        for (int i = 0; i < NP; ++i)
+          *(__attribute__((address_space(3))) bf16x8*)(at + i * BM * 128) = v[i];
       }
+    };
+    auto put = [&](const MxFrag<T> (&f)[kSlots], int s) {
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) put_one(f[j], s, j);
     };
 
     using P0 = std::integral_constant<int, 0>;
@@ -268,7 +269,10 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
     // everyone has read all of this one.
     auto arrive = [&](auto place) {
       constexpr int P = decltype(place)::value;
-      wait_vmcnt<D == 2 ? 0 : 2 * (kA + 1) + (P < 2 ? 1 : 0)>();
+      // (rows through registers: their loads are left under way, and the weights' are only
+      // awaited where their 256 K begin)
+      if constexpr (kDirect || P == 3)
+        wait_vmcnt<D == 2 ? 0 : 2 * (kA + 1) + (P < 2 ? 1 : 0)>();
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     };
     MxFrag<T> f[kSlots];
@@ -377,18 +381,27 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
           each(steps);
         }
       } else {
+        // a piece of the next stage's rows is cut and put down and one of the stage after it
+        // loaded with every step (4096^3 f32: all at the stage's ends 543 us, so 454)
+        static_assert(kDirect || kSlots == 4, "pieces of a step");
+        if (full > 0) fetch_full(f, full > 1 ? 1 : 0);
         each([&](int s, auto place) {
-          fetch_full(f, s + 1 < full ? s + 1 : s);
+          const int after = s + 2 < full ? s + 2 : full - 1;
           read_w(now, s);
+          read_x(even, s, 0);
           look();
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
+            Rows& here = t % 2 ? odd : even;
+            if (t < 3) read_x(t % 2 ? even : odd, s, t + 1);
+            __builtin_amdgcn_sched_barrier(0);
             u32x4 v[FN];
-            read_x(even, s, t);
             unpack(v, now, t, kind);
-            multiply(even, v, kind);
+            multiply(here, v, kind);
+            put_one(f[t % kSlots], s + 1, t % kSlots);
+            f[t % kSlots].load(px[kDirect ? 0 : t] + (int64_t)after * 64 + piece(t) * 8);
+            __builtin_amdgcn_sched_barrier(0);
           }
-          put(f, s + 1);
           arrive(place);
           issue(s, place);
         });
