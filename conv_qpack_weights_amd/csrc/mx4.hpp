@@ -177,6 +177,16 @@ inline bool mx_tile_reaches(const W4Rows& rows, int64_t row_bytes) {
   return row_bytes <= kMost / 256 && (!rows.map || rows.x_rows <= kMost / row_bytes);
 }
 
+// How many tiles of 16 rows the rows have, about: one of every expert that has any, or what
+// all of them take.
+inline int64_t mx_row_tiles(const MxArgs& a) {
+  const int64_t tiles = ceil_div(a.rows.M, 16);
+  const int64_t parts = !a.rows.offsets           ? 1
+                        : a.rows.experts < a.rows.M ? (int64_t)a.rows.experts
+                                                    : a.rows.M;
+  return tiles > parts ? tiles : parts;
+}
+
 // Whether tiles of `tile` rows are about one a matrix, so that each reads its weights alone.
 inline bool mx_read_once(const MxArgs& a, int64_t tile) {
   return a.rows.M <= tile * (a.rows.offsets ? a.rows.experts : 1);

@@ -496,7 +496,13 @@ qp_status mx_run_16bit(const MxArgs& a, hipStream_t stream) {
     case kMxRows16x16: return mx_launch_stream<T, 1, 4>(a, stream);
     case kMxRows16x32: return mx_launch_stream<T, 2, 4>(a, stream);
     case kMxRows16x48: return mx_launch_stream<T, 3, 4>(a, stream);
-    case kMxRows16x64: return mx_launch_stream<T, 4, 4>(a, stream);
+    // Several rounds of workgroups: two waves each, two to a CU, so that one finds its tile
+    // and rows while the other's loads are under way (16 tokens x 2 of 16 experts of 11008 x
+    // 4096 bf16 86 and 103 us, 8 experts of 4096 x 4096 with 4 tokens 17.9 and 13.0).
+    case kMxRows16x64:
+      return mx_row_tiles(a) * ceil_div(a.w.rows, 64) > 512
+                 ? mx_launch_stream<T, 4, 2>(a, stream)
+                 : mx_launch_stream<T, 4, 4>(a, stream);
     // (loads for once: 32 x 11008 x 4096 bf16 16.1 -> 15.6 us, 256 tokens x 4 of 32 experts of
     // 4096 x 2048 70.4 -> 67.6; 128 x 4096 x 11008 31.2 -> 33.3)
     case kMxTile32x64:

@@ -120,7 +120,8 @@ EXPERTS = [  # product, kernel, slots, experts, channels (the gradient's columns
     ("a4w4", "tile64x64", 600, 3, 2000), ("a4w4", "tile128x128", 2600, 3, 2000),
     ("a4w4", "tile256x256", 7000, 3, 4000),
     ("w4", "rows16x16", 40, 8, 200), ("w4", "rows16x64", 64, 8, 4000),
-    ("w4", "tile32x128", 128, 16, 5500), ("w4", "tile128x128", 2600, 3, 2000),
+    ("w4", "rows16x64", 128, 16, 5500), ("w4", "tile32x128", 256, 16, 5500),
+    ("w4", "tile128x128", 2600, 3, 2000),
     ("w4", "tile256x256", 7000, 3, 4000),
     ("w4_dx", "rows16x128", 300, 3, 300), ("w4_dx", "tile128x128", 2600, 3, 2000),
     ("w4_dx", "tile256x256", 6000, 3, 2000)]

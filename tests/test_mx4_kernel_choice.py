@@ -37,7 +37,8 @@ CHOICES = [
     ("w4", "bf16", 512, 4096, 4096, 1, "tile32x128"),
     ("w4", "bf16", 1024, 4096, 4096, 1, "tile128x128"),
     ("w4", "f16", 8192, 11008, 4096, 1, "tile256x256"),
-    ("w4", "bf16", 128, 11008, 4096, 16, "tile32x128"),
+    ("w4", "bf16", 128, 11008, 4096, 16, "rows16x64"),
+    ("w4", "bf16", 256, 11008, 4096, 16, "tile32x128"),
     ("w4", "bf16", 8192, 11008, 4096, 8, "tile256x256"),
     ("w4", "f32", 1, 4096, 4096, 1, "rows16x16"),
     ("w4", "f32", 32, 4096, 4096, 1, "rows16x32"),
