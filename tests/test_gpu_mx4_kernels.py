@@ -69,6 +69,8 @@ PRODUCTS = (
     + [("w4", t, k, M, N) for t in ("bf16", "f16") for k, M, N in SMALL +
        [("tile32x64", 146, 4900), ("tile32x128", 500, 4010), ("tile128x128", 1100, 4010),
         ("tile256x256", 4090, 4090)]]
+    + [("w4", t, "rows16x64", 13, 49000) for t in ("bf16", "f16")]  # several rounds
+    + [("w4", t, "tile128x128", 1000, 4010) for t in ("bf16", "f16")]  # one to a CU
     + [("w4", "f32", k, M, N) for k, M, N in SMALL + [("tile128x128", 1100, 4010)]])
 
 
@@ -121,7 +123,7 @@ EXPERTS = [  # product, kernel, slots, experts, channels (the gradient's columns
     ("a4w4", "tile256x256", 7000, 3, 4000),
     ("w4", "rows16x16", 40, 8, 200), ("w4", "rows16x64", 64, 8, 4000),
     ("w4", "rows16x64", 128, 16, 5500), ("w4", "tile32x128", 256, 16, 5500),
-    ("w4", "tile128x128", 2600, 3, 2000),
+    ("w4", "tile128x128", 2600, 3, 2000), ("w4", "tile128x128", 1200, 3, 2000),
     ("w4", "tile256x256", 7000, 3, 4000),
     ("w4_dx", "rows16x128", 300, 3, 300), ("w4_dx", "tile128x128", 2600, 3, 2000),
     ("w4_dx", "tile256x256", 6000, 3, 2000)]
@@ -318,6 +320,7 @@ def test_a_last_round_in_half_tiles(qp, product, dtype):
 @pytest.mark.parametrize("product,kernel,M,N", [
     ("w4", "rows16x16", 5, 300), ("w4", "rows16x64", 61, 4030), ("w4", "tile32x64", 146, 4900),
     ("w4", "tile32x128", 500, 4010), ("w4", "tile128x128", 1100, 4010),
+    ("w4", "tile128x128", 1000, 4010),
     ("w4", "tile256x256", 4090, 4090), ("w4_dx", "rows16x128", 5, 300),
     ("w4_dx", "tile128x128", 2100, 4010), ("w4_dx", "tile256x256", 4090, 4090)])
 def test_one_block_that_is_no_f16_values(qp, product, kernel, M, N):
