@@ -156,8 +156,8 @@ enum MxShape {
 // microseconds for up to one workgroup a CU (256); `cold` for every further round of
 // workgroups that bring weights of their own, `more` for one that finds its weights in
 // the caches (further row tiles of the same matrix).  Rounds are whole ones for the
-// few-row kernels, whose workgroups all wait for memory alike, and for the largest
-// tile, one to a CU.
+// few-row kernels, whose workgroups all wait for memory alike; the largest tile is one
+// to a CU, its last round in halves where it is half empty.
 struct MxCost {
   MxShape shape;
   int rows, channels;

@@ -9,9 +9,11 @@
 // l/32) and converts a word for each of the stage's four steps; the rows' operand of
 // step t is piece 4 (l/32) + t of the row.  Weights are the MFMA's first operand.
 //
-// 4096^3 bf16, 256 x 256 tiles: 104 us, 1.32 PFLOP/s (the library's product of bf16
-// matrices of 8192^3 reaches 1.49), the MFMAs busy for 59% of its cycles; 32 x 176128 x
-// 4096 by 32 x 128 tiles 99 us, 3.9 TB/s of weights.
+// 4096^3 bf16, 256 x 256 tiles: 105 us, 1.31 PFLOP/s, the MFMAs busy for 62% of its
+// cycles; with K it grows at 1.47 PFLOP/s (the library's product of bf16 matrices of 8192^3
+// reaches 1.49), the rest are launch, first loads and the sums' way out.  1024 x 4096 x
+// 4096 by 128 x 128 tiles 38 us, 32 x 176128 x 4096 by 32 x 128 99, 3.9 TB/s of weights;
+// 4096^3 f32 454 (128 x 128, three MFMAs a term: 0.91 PFLOP/s of them).
 //
 // f16 rows: the weights go in as f16 and the rows as they are; where one of a
 // workgroup's scales turns out to be out of f16's reach (mx_f16_scale) it begins
