@@ -404,3 +404,30 @@ def test_bounds_in_every_kernel(qp, product, dtype, kernel, M, N):
     for lo, hi in ((-0.5, inf), (-inf, 0.25), (-0.5, 0.25), (0.0, 0.0)):
         got = run(X, W, bias, lo, hi, out_dtype=_dt(dtype))
         assert torch.equal(got, free.clamp(lo, hi).to(_dt(dtype))), (lo, hi)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("product,kernel,M,N", [
+    ("a4w4", "rows16x32", 45, 4010), ("a4w4", "tile64x64", 250, 4010),
+    ("a4w4", "tile128x128", 1100, 4010), ("a4w4", "tile256x256", 4090, 4090),
+    ("w4", "tile32x128", 500, 4010), ("w4", "tile128x128", 1100, 4010),
+    ("w4", "tile256x256", 4090, 4090), ("w4_dx", "rows16x128", 5, 300),
+    ("w4_dx", "tile128x128", 2100, 4010), ("w4_dx", "tile256x256", 4090, 4090)])
+def test_outputs_at_odd_places(qp, product, kernel, M, N, dtype):
+    """Rows of the result an odd number of elements apart and from an odd one on: the same
+    results, and nothing beside them."""
+    import torch
+    g = torch.Generator().manual_seed(N)
+    K = 330
+    W, _ = _matrix(qp, g, K, N) if product == "w4_dx" else _matrix(qp, g, N, K)
+    name = qp.qgemm_mx_kernel_name(product, M, W, _dt(dtype)).split("/")[0]
+    assert dtype == "f32" or name == kernel
+    print("mx4 odd outputs", product, dtype, name, M, N, flush=True)
+    X = _matrix(qp, g, M, K)[0] if product == "a4w4" else _rows(g, M, K, dtype)[0]
+    run = {"a4w4": qp.qgemm_a4w4_mx, "w4": qp.qgemm_w4_mx, "w4_dx": qp.qgemm_w4_mx_dx}[product]
+    kw = {"out_dtype": _dt(dtype)} if product == "a4w4" else {}
+    want = run(X, W, **kw)
+    wide = torch.full((M + 1, N + 3 - N % 2), 7.0, dtype=_dt(dtype), device="cuda")
+    run(X, W, out=wide[:M, 1:1 + N])
+    assert torch.equal(wide[:M, 1:1 + N], want)
+    assert (wide[M] == 7).all() and (wide[:, 0] == 7).all() and (wide[:, 1 + N:] == 7).all()
