@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "mx4_rows.hpp"
+#include "mx4_scales.hpp"
 #include "mx4_stream.hpp"
 #include "mx4_tile.hpp"
 
@@ -40,11 +41,11 @@ __device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, uint32_t sa, u32x4 b, uint3
 template <int BM, int BN, int WM, int WN, int D>
 struct A4Tile {
   static constexpr int NW = WM * WN, FM = BM / (32 * WM), FN = BN / (32 * WN);
-  static constexpr int kStage = (BM + BN) * 128, kScales = (BM + BN) * 16;
+  static constexpr int kStage = (BM + BN) * 128, kScales = (BM + BN) * kMxScaleRow;
   static constexpr int kSpans = D == 2 ? 2 : 4;  // of 512 K: D / 2 + 1 are live
   static constexpr int kOutLd = mx_out_ld(FN);
   static constexpr int kOut = NW * 32 * kOutLd * 4;
-  static constexpr int kRing = D * kStage + kSpans * kScales;
+  static constexpr int kRing = D * kStage + kSpans * kScales + kMxScaleRoom;
   static constexpr int kLds = kRing > kOut ? kRing : kOut;
 };
 
@@ -127,8 +128,8 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   // for nothing: its buffers' range is empty, so that every round of the loop has the
   // same loads to wait for.
   const int G = (int)a.w.G, full = G / 8, stages = (G + 7) / 8, words = (G + 3) / 4;
-  const int over = (words + 3) / 4 * 16 - words * 4;  // bytes that the last 512 K lack
-  auto late = [&](int s) { return kWide && (s >> 1) * 4 + 4 > words ? over : 0; };
+  const int over = mx_scales_over(words);
+  auto late = [&](int s) { return kWide && mx_scales_end(s) > words ? over : 0; };
   auto issue = [&](int s, auto with_scales) {
     lds_u8* const to = ring + (s % D) * L::kStage;
     const int range = s < stages ? 0x7fffffff : 0;
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
     };
     auto read_scales = [&](Scales& o, int s) {
       const lds_u8* const st =
-          scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8 + late(s);
+          scales + ((s >> 1) % L::kSpans) * L::kScales + mx_scales_at(s) + late(s);
 #pragma unroll
       for (int j = 0; j < F; ++j) o.a[j] = mine(st + (arow + j * 32) * 16);
 #pragma unroll
@@ -286,7 +287,8 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
       const int left = G - s * 8;
       if (left < 8) {
         lds_u8* const to = ring + (s % D) * L::kStage;
-        lds_u8* const st = scales + ((s >> 1) % L::kSpans) * L::kScales + (s & 1) * 8 + late(s);
+        lds_u8* const st =
+            scales + ((s >> 1) % L::kSpans) * L::kScales + mx_scales_at(s) + late(s);
         for (int i = threadIdx.x; i < (BM + BN) * 8; i += NW * 64) {
           if (((i & 7) ^ mx_turn(i >> 3)) >= left)
             *(__attribute__((address_space(3))) u32x4*)(to + i * 16) = u32x4{0, 0, 0, 0};
