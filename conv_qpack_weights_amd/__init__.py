@@ -964,23 +964,42 @@ class MX4:
     """An MXFP4 matrix [rows, K], or one an expert [experts, rows, K]: ``codes``
     uint8 [.., rows, 16*ceil(K/32)] (two values a byte, the first in the low bits)
     and ``scales`` uint8 [.., rows, ceil(K/32)].  Made by :func:`mx4_tensor` and
-    :func:`qquantize_rows_mx4`; an expert's matrix is ``m[e]``."""
+    :func:`qquantize_rows_mx4`, or MX4(codes, scales, K) of tensors as the kernels read
+    them, rows of wider buffers too (places at multiples of 16 and 4 bytes, and the
+    bytes up to the next multiple of 4 behind a row's scales there); an expert's matrix
+    is ``m[e]``."""
     __slots__ = ("codes", "scales", "K", "desc")
 
     def __init__(self, codes, scales, K):
         self.codes, self.scales, self.K = codes, scales, K
+        self._describe()
+
+    def _describe(self):
+        codes, scales, K = self.codes, self.scales, self.K
+        _mx4_shapes(codes, scales, K)
         *lead, rows, G = scales.shape
+        padded = -(-G // 4) * 4
         if rows < 2:
             # (the stride of a single row means nothing to torch: the library gets the
             # row's length)
-            ldc, lds = 16 * G, -(-G // 4) * 4
+            ldc, lds = 16 * G, padded
         else:
             ldc, lds = codes.stride(-2), scales.stride(-2)
+        assert codes.stride(-1) == 1 and (G == 1 or scales.stride(-1) == 1), \
+            "the bytes of a row's codes and scales must lie side by side"
+        assert ldc >= 16 * G and lds >= padded, \
+            "rows of codes or scales overlap (mx4_tensor lays them out)"
         if lead:
-            self.desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), rows, K, ldc, lds, lead[0],
-                                codes.stride(0), scales.stride(0))
+            E, cstride, sstride = lead[0], codes.stride(0), scales.stride(0)
         else:
-            self.desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), rows, K, ldc, lds, 1, 0, 0)
+            E, cstride, sstride = 1, 0, 0
+        if G != padded and rows and E:
+            # (a row of scales is read in words)
+            end = scales.storage_offset() + (E - 1) * sstride + (rows - 1) * lds + padded
+            assert end <= scales.untyped_storage().nbytes(), \
+                "the scales end before the last row's last word (mx4_tensor lays them out)"
+        self.desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), rows, K, ldc, lds, E, cstride,
+                            sstride)
 
     @property
     def shape(self):
@@ -993,6 +1012,17 @@ class MX4:
     def __getitem__(self, e):
         assert self.codes.dim() == 3, "one matrix only"
         return MX4(self.codes[e], self.scales[e], self.K)
+
+
+def _mx4_shapes(codes, scales, K):
+    """Codes and scales of one matrix, or one an expert, whose rows have K values."""
+    assert codes.dtype == torch.uint8 and scales.dtype == torch.uint8, \
+        "codes and scales must be uint8"
+    assert codes.dim() in (2, 3) and codes.shape[:-1] == scales.shape[:-1], \
+        "codes and scales must be [rows, bytes] or [experts, rows, bytes] alike"
+    G = scales.shape[-1]
+    assert G > 0 and codes.shape[-1] == 16 * G, "codes must hold 16 bytes a block, scales one"
+    assert 32 * (G - 1) < K <= 32 * G, "K=%d does not fit %d blocks of 32" % (K, G)
 
 
 def _mx4_codes(t, rows_shape, G):
@@ -1015,14 +1045,9 @@ def mx4_tensor(codes: torch.Tensor, scales: torch.Tensor, K=None) -> MX4:
     and scales uint8 [.., rows, ceil(K/32)], as checkpoints hold them: taken as they
     are where the kernels can read them, else laid out anew (once, at load time).  The
     values that fill up the last block of a ``K`` not a multiple of 32 must be zeros."""
-    assert codes.dtype == torch.uint8 and scales.dtype == torch.uint8, \
-        "codes and scales must be uint8"
-    assert codes.dim() in (2, 3) and codes.shape[:-1] == scales.shape[:-1], \
-        "codes and scales must be [rows, bytes] or [experts, rows, bytes] alike"
-    G = scales.shape[-1]
-    assert G > 0 and codes.shape[-1] == 16 * G, "codes must hold 16 bytes a block, scales one"
+    G = scales.shape[-1] if scales.dim() else 0
     K = 32 * G if K is None else int(K)
-    assert 32 * (G - 1) < K <= 32 * G, "K=%d does not fit %d blocks of 32" % (K, G)
+    _mx4_shapes(codes, scales, K)
     assert codes.device == scales.device, "codes and scales must be on one device"
     lead = codes.shape[:-1]
     codes = _mx4_codes(codes, lead, G)
