@@ -193,8 +193,13 @@ def _stream(device=None):
 
 
 def _stream_of(t):
-    return _raw_stream(t.get_device()) if _raw_stream is not None and t.is_cuda \
-        else _stream(t.device)
+    """The current stream on a tensor's GPU, or on the one of that number."""
+    if _raw_stream is not None:
+        if type(t) is int:
+            return _raw_stream(t)
+        if t.is_cuda:
+            return _raw_stream(t.get_device())
+    return _stream(torch.device("cuda", t) if type(t) is int else t.device)
 
 
 def _ptr(t):
@@ -686,7 +691,7 @@ def _rows(t, what):
 def _out(t, M, n, dtype, like, what):
     """The output `t` checked, or a new one; its type's number and row stride."""
     if t is None:
-        t = like.new_empty((M, n)) if dtype is like.dtype else like.new_empty((M, n), dtype=dtype)
+        t = torch.empty_strided((M, n), (n, 1), dtype=dtype, device=like.device)
         return t, _FLOAT[dtype], n
     dt, m, k, ld = _rows(t, what)
     assert m == M and k == n, "%s must have the shape [%d, %d]" % (what, M, n)
@@ -967,15 +972,43 @@ class MX4:
     :func:`qquantize_rows_mx4`, or MX4(codes, scales, K) of tensors as the kernels read
     them, rows of wider buffers too (places at multiples of 16 and 4 bytes, and the
     bytes up to the next multiple of 4 behind a row's scales there); an expert's matrix
-    is ``m[e]``."""
-    __slots__ = ("codes", "scales", "K", "desc")
+    is ``m[e]``.  Every call looks where the tensors lie: the parameters that a matrix
+    was made of may move (``module.to()``)."""
+    __slots__ = ("_codes", "_scales", "K", "_desc", "_seen", "_gpu")
 
     def __init__(self, codes, scales, K):
-        self.codes, self.scales, self.K = codes, scales, K
+        self._codes, self._scales, self.K = codes, scales, K
         self._describe()
 
+    # (codes and scales that no one else has been given cannot move: `_seen` is None)
+    @property
+    def codes(self):
+        if self._seen is None:
+            self._look()
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._seen is None:
+            self._look()
+        return self._scales
+
+    @property
+    def desc(self):
+        """Where the matrix lies now: tensors of a module move under it."""
+        seen = self._seen
+        if seen is not None:
+            c, s = self._codes, self._scales
+            if (c.data_ptr(), s.data_ptr(), c.stride(), s.stride(), c.shape, s.shape) != seen:
+                self._describe()
+        return self._desc
+
+    def _look(self):
+        c, s = self._codes, self._scales
+        self._seen = c.data_ptr(), s.data_ptr(), c.stride(), s.stride(), c.shape, s.shape
+
     def _describe(self):
-        codes, scales, K = self.codes, self.scales, self.K
+        codes, scales, K = self._codes, self._scales, self.K
         _mx4_shapes(codes, scales, K)
         *lead, rows, G = scales.shape
         padded = -(-G // 4) * 4
@@ -998,20 +1031,47 @@ class MX4:
             end = scales.storage_offset() + (E - 1) * sstride + (rows - 1) * lds + padded
             assert end <= scales.untyped_storage().nbytes(), \
                 "the scales end before the last row's last word (mx4_tensor lays them out)"
-        self.desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), rows, K, ldc, lds, E, cstride,
-                            sstride)
+        self._desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), rows, K, ldc, lds, E, cstride,
+                             sstride)
+        gpu = codes.get_device()
+        self._gpu = gpu if scales.get_device() == gpu else -1
+        self._look()
+
+    @classmethod
+    def _new(cls, like, lead, rows, K):
+        """Room for a matrix on like's GPU, rows of scales of whole words."""
+        G = -(-K // 32)
+        padded = -(-G // 4) * 4
+        m = cls.__new__(cls)
+        m._codes = codes = like.new_empty((*lead, rows, 16 * G), dtype=torch.uint8)
+        m._scales = scales = _mx4_scales((*lead, rows), G, like)
+        m.K, m._seen, m._gpu = K, None, codes.get_device()
+        if lead:
+            m._desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), rows, K, 16 * G, padded, lead[0],
+                              16 * G * rows, padded * rows)
+        else:
+            m._desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), rows, K, 16 * G, padded, 1, 0, 0)
+        return m
 
     @property
     def shape(self):
-        return (*self.codes.shape[:-1], self.K)
+        return (*self._codes.shape[:-1], self.K)
 
     @property
     def device(self):
-        return self.codes.device
+        return self._codes.device
 
     def __getitem__(self, e):
-        assert self.codes.dim() == 3, "one matrix only"
-        return MX4(self.codes[e], self.scales[e], self.K)
+        d = self.desc
+        assert self._codes.dim() == 3, "one matrix only"
+        codes, scales = self._codes[e], self._scales[e]
+        if type(e) is not int:
+            return MX4(codes, scales, self.K)
+        m = MX4.__new__(MX4)
+        m._codes, m._scales, m.K, m._seen, m._gpu = codes, scales, d.K, None, self._gpu
+        m._desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), d.rows, d.K, d.ld_codes, d.ld_scales,
+                          1, 0, 0)
+        return m
 
 
 def _mx4_shapes(codes, scales, K):
@@ -1064,24 +1124,41 @@ def _several_gpus():
     return torch.cuda.device_count() > 1
 
 
-def _mx_call(name, t, *args):
-    """The library's `name` on t's GPU and its current stream there."""
+def _mx_call(name, gpu, *args):
+    """The library's `name` on a GPU and its current stream there."""
     f = getattr(_lib, name)
     if _several_gpus():
-        with torch.cuda.device(t.get_device()):
-            status = f(*args, _stream_of(t))
+        with torch.cuda.device(gpu):
+            status = f(*args, _stream_of(gpu))
     else:
-        status = f(*args, _stream_of(t))
-    _check(status, name)
+        status = f(*args, _stream_of(gpu))
+    if status:
+        _check(status, name)
+
+
+def _mx_gpu(what, gpu, w, *tensors):
+    """The GPU of a call, `gpu` (of its rows), where the matrix w and the tensors must be."""
+    assert gpu >= 0, "%s: its tensors must be on the GPU" % what
+    assert w._gpu == gpu, "%s: its tensors must be on one GPU" % what
+    for t in tensors:
+        assert t is None or t.get_device() == gpu, "%s: its tensors must be on one GPU" % what
+    return gpu
 
 
 _MX_RULES = {"floor": QP_MX_FLOOR, "ceil": QP_MX_CEIL}
 
 
 def _is_mx4(m, what, dims=2):
+    """The matrix's description, asked for once a call."""
     assert isinstance(m, MX4), "%s must be an MX4 (mx4_tensor, qquantize_rows_mx4)" % what
-    assert m.codes.dim() == dims, "%s must be %s" % (
+    c, seen = m._codes, m._seen
+    if seen is not None:  # (m.desc, without its call)
+        s = m._scales
+        if (c.data_ptr(), s.data_ptr(), c.stride(), s.stride(), c.shape, s.shape) != seen:
+            m._describe()
+    assert c.dim() == dims, "%s must be %s" % (
         what, "one matrix" if dims == 2 else "a matrix an expert")
+    return m._desc
 
 
 def qquantize_rows_mx4(X: torch.Tensor, rule="floor", out=None) -> MX4:
@@ -1094,64 +1171,65 @@ def qquantize_rows_mx4(X: torch.Tensor, rule="floor", out=None) -> MX4:
         assert X.is_contiguous(), "the matrices must be contiguous"
         X = X.view(-1, K)
     dt, M, K, ldx = _rows(X, "X")
-    G = -(-K // 32)
     if out is None:
-        out = MX4(X.new_empty((*lead, 16 * G), dtype=torch.uint8), _mx4_scales(lead, G, X), K)
+        out = MX4._new(X, lead[:-1], lead[-1], K)
+        d = out._desc
     else:
         assert isinstance(out, MX4) and out.shape == (*lead, K), "out must be of X's shape"
-        assert out.codes.dim() == 2 or (out.codes.is_contiguous() and
-                                        out.desc.scales_stride == out.desc.rows * out.desc.ld_scales), \
+        d = out.desc
+        assert out._codes.dim() == 2 or (out._codes.is_contiguous() and
+                                         d.scales_stride == d.rows * d.ld_scales), \
             "out's matrices must follow each other"
-    d = out.desc
-    _one_gpu("qquantize_rows_mx4", X, out.codes, out.scales)
-    _mx_call("qquantize_rows_mx4", X, _ptr(X), dt, M, K, ldx, _MX_RULES[rule], d.codes,
+    gpu = _mx_gpu("qquantize_rows_mx4", X.get_device(), out)
+    _mx_call("qquantize_rows_mx4", gpu, X.data_ptr(), dt, M, K, ldx, _MX_RULES[rule], d.codes,
              d.ld_codes, d.scales, d.ld_scales)
     return out
 
 
 def qdequantize_rows_mx4(a: MX4, dtype=torch.float32, out=None):
     """The values of an MXFP4 matrix, [rows, K] in `dtype`."""
-    _is_mx4(a, "a")
+    d = _is_mx4(a, "a")
     assert dtype in _FLOAT, "dtype must be float32, bfloat16 or float16"
-    M, K = a.shape
-    out, odt, ldy = _out(out, M, K, dtype, a.codes, "out")
-    _one_gpu("qdequantize_rows_mx4", a.codes, a.scales, out)
-    _mx_call("qdequantize_rows_mx4", a.codes, C.byref(a.desc), _ptr(out), odt, ldy)
+    out, odt, ldy = _out(out, d.rows, d.K, dtype, a._codes, "out")
+    gpu = _mx_gpu("qdequantize_rows_mx4", a._gpu, a, out)
+    _mx_call("qdequantize_rows_mx4", gpu, d, out.data_ptr(), odt, ldy)
     return out
 
 
 def _mx_bias(bias, n, what):
-    if bias is not None:
-        _f32(bias, "bias")
-        assert bias.numel() == n, "bias must hold %s values" % what
+    """The bias checked, and its address."""
+    if bias is None:
+        return None
+    assert bias.dtype == torch.float32 and bias.is_contiguous(), \
+        "bias must be a contiguous float32 tensor"
+    assert bias.numel() == n, "bias must hold %s values" % what
+    return bias.data_ptr()
 
 
 def qgemm_a4w4_mx(A: MX4, W: MX4, bias=None, clamp_lo=-float("inf"), clamp_hi=float("inf"),
                   out=None, out_dtype=torch.float32):
     """Y = clamp(A @ W^T + bias), both MXFP4: A [M, K], W [N, K]; outputs f32, bf16
     or f16."""
-    _is_mx4(A, "A")
-    _is_mx4(W, "W")
-    M, N = A.desc.rows, W.desc.rows
+    a, w = _is_mx4(A, "A"), _is_mx4(W, "W")
+    M, N = a.rows, w.rows
     assert out_dtype in _FLOAT, "out_dtype must be float32, bfloat16 or float16"
-    out, odt, ldy = _out(out, M, N, out_dtype, A.codes, "out")
-    _mx_bias(bias, N, "N")
-    _one_gpu("qgemm_a4w4_mx", A.codes, A.scales, W.codes, W.scales, bias, out)
-    _mx_call("qgemm_a4w4_mx", A.codes, C.byref(A.desc), C.byref(W.desc), _ptr(bias), clamp_lo,
-             clamp_hi, _ptr(out), odt, ldy)
+    out, odt, ldy = _out(out, M, N, out_dtype, A._codes, "out")
+    b = _mx_bias(bias, N, "N")
+    gpu = _mx_gpu("qgemm_a4w4_mx", A._gpu, W, bias, out)
+    _mx_call("qgemm_a4w4_mx", gpu, a, w, b, clamp_lo, clamp_hi, out.data_ptr(), odt, ldy)
     return out
 
 
 def _mx_experts(W, offsets, bias, rows, x_rows):
-    _is_mx4(W, "W", 3)
+    w = _is_mx4(W, "W", 3)
     _ints(offsets, "offsets")
-    E, N = W.desc.matrices, W.desc.rows
+    E, N = w.matrices, w.rows
     assert offsets.numel() == E + 1, "offsets must hold experts + 1 values"
-    _mx_bias(bias, E * N, "experts x N")
+    b = _mx_bias(bias, E * N, "experts x N")
     if rows is None:
-        return x_rows, N
+        return w, x_rows, N, b
     _ints(rows, "rows")
-    return rows.numel(), N
+    return w, rows.numel(), N, b
 
 
 def qgemm_a4w4_mx_experts(A: MX4, W: MX4, offsets: torch.Tensor, bias=None, rows=None, row_div=1,
@@ -1160,13 +1238,13 @@ def qgemm_a4w4_mx_experts(A: MX4, W: MX4, offsets: torch.Tensor, bias=None, rows
     """The product with rows [offsets[e], offsets[e+1]) on W[e] [E, N, K] and bias
     [E, N]; ``rows`` and ``row_div`` as in :func:`qgemm_w4_experts` (tokens
     quantized once, read through slot_of_row)."""
-    _is_mx4(A, "A")
-    M, N = _mx_experts(W, offsets, bias, rows, A.desc.rows)
+    a = _is_mx4(A, "A")
+    w, M, N, b = _mx_experts(W, offsets, bias, rows, a.rows)
     assert out_dtype in _FLOAT, "out_dtype must be float32, bfloat16 or float16"
-    out, odt, ldy = _out(out, M, N, out_dtype, A.codes, "out")
-    _one_gpu("qgemm_a4w4_mx_experts", A.codes, A.scales, W.codes, W.scales, offsets, bias, rows, out)
-    _mx_call("qgemm_a4w4_mx_experts", A.codes, C.byref(A.desc), _ptr(rows), row_div, M,
-             C.byref(W.desc), _ptr(offsets), _ptr(bias), clamp_lo, clamp_hi, _ptr(out), odt, ldy)
+    out, odt, ldy = _out(out, M, N, out_dtype, A._codes, "out")
+    gpu = _mx_gpu("qgemm_a4w4_mx_experts", A._gpu, W, offsets, bias, rows, out)
+    _mx_call("qgemm_a4w4_mx_experts", gpu, a, _ptr(rows), row_div, M, w, offsets.data_ptr(),
+             b, clamp_lo, clamp_hi, out.data_ptr(), odt, ldy)
     return out
 
 
@@ -1175,14 +1253,14 @@ def qgemm_w4_mx(X: torch.Tensor, W: MX4, bias=None, clamp_lo=-float("inf"),
     """Y = clamp(X @ W^T + bias): float rows (f32, bf16 or f16, not quantized) times
     MXFP4 weights; outputs in X's type or `out_dtype` float32."""
     dt, M, K, ldx = _rows(X, "X")
-    _is_mx4(W, "W")
-    N = W.desc.rows
+    w = _is_mx4(W, "W")
+    N = w.rows
     assert out_dtype is None or out_dtype in _FLOAT, "out_dtype must be X's type or float32"
     out, odt, ldy = _out(out, M, N, out_dtype or X.dtype, X, "out")
-    _mx_bias(bias, N, "N")
-    _one_gpu("qgemm_w4_mx", X, W.codes, W.scales, bias, out)
-    _mx_call("qgemm_w4_mx", X, _ptr(X), dt, M, K, ldx, C.byref(W.desc), _ptr(bias), clamp_lo,
-             clamp_hi, _ptr(out), odt, ldy)
+    b = _mx_bias(bias, N, "N")
+    gpu = _mx_gpu("qgemm_w4_mx", X.get_device(), W, bias, out)
+    _mx_call("qgemm_w4_mx", gpu, X.data_ptr(), dt, M, K, ldx, w, b, clamp_lo, clamp_hi,
+             out.data_ptr(), odt, ldy)
     return out
 
 
@@ -1192,28 +1270,32 @@ def qgemm_w4_mx_experts(X: torch.Tensor, W: MX4, offsets: torch.Tensor, bias=Non
     """The product with rows [offsets[e], offsets[e+1]) on W[e] [E, N, K] and bias
     [E, N]; ``rows`` and ``row_div`` as in :func:`qgemm_w4_experts`."""
     dt, x_rows, K, ldx = _rows(X, "X")
-    M, N = _mx_experts(W, offsets, bias, rows, x_rows)
+    w, M, N, b = _mx_experts(W, offsets, bias, rows, x_rows)
     assert out_dtype is None or out_dtype in _FLOAT, "out_dtype must be X's type or float32"
     out, odt, ldy = _out(out, M, N, out_dtype or X.dtype, X, "out")
-    _one_gpu("qgemm_w4_mx_experts", X, W.codes, W.scales, offsets, bias, rows, out)
-    _mx_call("qgemm_w4_mx_experts", X, _ptr(X), dt, x_rows, K, ldx, _ptr(rows), row_div, M,
-             C.byref(W.desc), _ptr(offsets), _ptr(bias), clamp_lo, clamp_hi, _ptr(out), odt, ldy)
+    gpu = _mx_gpu("qgemm_w4_mx_experts", X.get_device(), W, offsets, bias, rows, out)
+    _mx_call("qgemm_w4_mx_experts", gpu, X.data_ptr(), dt, x_rows, K, ldx, _ptr(rows), row_div, M, w,
+             offsets.data_ptr(), b, clamp_lo, clamp_hi, out.data_ptr(), odt, ldy)
     return out
 
 
-def qgemm_w4_mx_dx_ws_size(M: int, W: MX4) -> int:
+def _mx_dx_ws_size(M, w):
     n = C.c_size_t()
-    _check(_lib.qgemm_w4_mx_dx_ws_size(M, C.byref(W.desc), C.byref(n)), "qgemm_w4_mx_dx_ws_size")
+    _check(_lib.qgemm_w4_mx_dx_ws_size(M, w, C.byref(n)), "qgemm_w4_mx_dx_ws_size")
     return n.value
 
 
-def _mx_dx_buffers(dY, W, out, ws):
+def qgemm_w4_mx_dx_ws_size(M: int, W: MX4) -> int:
+    return _mx_dx_ws_size(M, W.desc)
+
+
+def _mx_dx_buffers(dY, w, out, ws):
     dt, M, N, lddy = _rows(dY, "dY")
-    assert N == W.desc.rows, "dY must have N columns"
-    out, odt, lddx = _out(out, M, W.K, dY.dtype, dY, "out")
+    assert N == w.rows, "dY must have N columns"
+    out, odt, lddx = _out(out, M, w.K, dY.dtype, dY, "out")
     assert odt == dt, "out must be of dY's type"
     if ws is None:
-        n = qgemm_w4_mx_dx_ws_size(M, W)
+        n = _mx_dx_ws_size(M, w)
         ws = _alloc_bytes(n, dY.device) if n else None
     return dt, M, lddy, out, lddx, ws, _ws_bytes(ws)
 
@@ -1221,23 +1303,22 @@ def _mx_dx_buffers(dY, W, out, ws):
 def qgemm_w4_mx_dx(dY: torch.Tensor, W: MX4, out=None, ws=None):
     """The gradient of qgemm_w4_mx (and of qgemm_a4w4_mx, past the quantization) to
     the rows: dX = dY @ W."""
-    _is_mx4(W, "W")
-    dt, M, lddy, out, lddx, ws, n = _mx_dx_buffers(dY, W, out, ws)
-    _one_gpu("qgemm_w4_mx_dx", dY, W.codes, W.scales, out, ws)
-    _mx_call("qgemm_w4_mx_dx", dY, _ptr(dY), dt, M, lddy, C.byref(W.desc), _ptr(out), lddx,
-             _ptr(ws), n)
+    w = _is_mx4(W, "W")
+    dt, M, lddy, out, lddx, ws, n = _mx_dx_buffers(dY, w, out, ws)
+    gpu = _mx_gpu("qgemm_w4_mx_dx", dY.get_device(), W, out, ws)
+    _mx_call("qgemm_w4_mx_dx", gpu, dY.data_ptr(), dt, M, lddy, w, out.data_ptr(), lddx, _ptr(ws), n)
     return out
 
 
 def qgemm_w4_mx_experts_dx(dY: torch.Tensor, W: MX4, offsets: torch.Tensor, out=None, ws=None):
     """The gradient of qgemm_w4_mx_experts to its (sorted) rows."""
-    _is_mx4(W, "W", 3)
+    w = _is_mx4(W, "W", 3)
     _ints(offsets, "offsets")
-    assert offsets.numel() == W.desc.matrices + 1, "offsets must hold experts + 1 values"
-    dt, M, lddy, out, lddx, ws, n = _mx_dx_buffers(dY, W, out, ws)
-    _one_gpu("qgemm_w4_mx_experts_dx", dY, W.codes, W.scales, offsets, out, ws)
-    _mx_call("qgemm_w4_mx_experts_dx", dY, _ptr(dY), dt, M, lddy, C.byref(W.desc), _ptr(offsets),
-             _ptr(out), lddx, _ptr(ws), n)
+    assert offsets.numel() == w.matrices + 1, "offsets must hold experts + 1 values"
+    dt, M, lddy, out, lddx, ws, n = _mx_dx_buffers(dY, w, out, ws)
+    gpu = _mx_gpu("qgemm_w4_mx_experts_dx", dY.get_device(), W, offsets, out, ws)
+    _mx_call("qgemm_w4_mx_experts_dx", gpu, dY.data_ptr(), dt, M, lddy, w, offsets.data_ptr(),
+             out.data_ptr(), lddx, _ptr(ws), n)
     return out
 
 
@@ -1245,6 +1326,6 @@ def qgemm_mx_kernel_name(product: str, M: int, W: MX4, dtype=torch.bfloat16) -> 
     """Which kernel "a4w4", "w4" or "w4_dx" takes for M rows (of `dtype`) and W."""
     which = {"a4w4": QP_MX_A4W4, "w4": QP_MX_W4, "w4_dx": QP_MX_W4_DX}[product]
     name = C.create_string_buffer(32)
-    _check(_lib.qgemm_mx_kernel_name(which, M, C.byref(W.desc), _FLOAT[dtype], name, len(name)),
+    _check(_lib.qgemm_mx_kernel_name(which, M, W.desc, _FLOAT[dtype], name, len(name)),
            "qgemm_mx_kernel_name")
     return name.value.decode()
