@@ -58,9 +58,16 @@ __device__ __forceinline__ bf16x8 mx_unpack(uint32_t w, float scale) {
 }
 
 // Whether a block's weights are f16 values, exactly: its scale one of 2^-23 .. 2^13
-// (then 0.5 and 6 times it are), which the weights of layers have.
+// (then 0.5 and 6 times it are), which the weights of layers have, or all its codes
+// zeros under any scale but NaN's (the quantizer gives zeros the smallest).  The kernels
+// ask for the scales alone at their steps; the tiles, which begin again where one is out
+// of range, look at its codes before they do.
 __device__ __forceinline__ bool mx_f16_scale(float scale) {
   return __builtin_bit_cast(uint32_t, scale) - (104u << 23) <= (36u << 23);
+}
+__device__ __forceinline__ bool mx_f16_block(u32x4 codes, float scale) {
+  return mx_f16_scale(scale) || (((codes[0] | codes[1] | codes[2] | codes[3]) & 0x77777777u) == 0 &&
+                                 __builtin_bit_cast(uint32_t, scale) < (255u << 23));
 }
 // The eight values of a word of codes as f16, where they are.
 __device__ __forceinline__ f16x8 mx_unpack_f16(uint32_t w, float scale) {

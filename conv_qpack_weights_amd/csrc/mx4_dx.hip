@@ -189,7 +189,7 @@ __global__ __launch_bounds__(256) void mx_dx_sum_kernel(const float* __restrict_
 // bytes, to the other of two buffers, so that every weight is converted once in a
 // workgroup.  In that buffer column 4u + j of a wave's 64 is row 16 j + u: 16 threads
 // then write 16 rows, whose places meet every bank alike (mx_turn).
-// f16 rows: as there, again from the start where a weight turns out to be no f16 value.
+// f16 rows: as there, again from the start where a weight turned out to be no f16 value.
 // 4096^3, 256 x 256 tiles: bf16 117 us (1.17 PFLOP/s), f16 122; 1024 x 4096 x 4096 by 128 x 128
 // 49 (rows loaded further ahead: no faster, one wave a SIMD has the conversion, 16 small LDS
 // reads and 4 writes, between its MFMAs).
@@ -567,7 +567,10 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_dx_tile_kernel(MxDxArgs a, ui
     };
     if constexpr (kF16) {
       all(true_type{});
-      if (__syncthreads_or(out)) all(false_type{});
+      out = __syncthreads_or(out);
+      if (out) out = __syncthreads_or(mx_no_f16_among(codes, a.w.ldc, scales, a.w.lds, N, blocks,
+                                                      NW * 64));
+      if (out) all(false_type{});
     } else {
       all(false_type{});
     }

@@ -16,9 +16,9 @@
 // 4096^3 f32 454 (128 x 128, three MFMAs a term: 0.91 PFLOP/s of them).
 //
 // f16 rows: the weights go in as f16 and the rows as they are; where one of a
-// workgroup's scales turns out to be out of f16's reach (mx_f16_scale) it begins
-// again, with the weights as bf16 and the rows as two bf16 pieces, twice the MFMAs and
-// the cuts.  (Deciding stage by stage instead doubled the registers; a look over all
+// workgroup's scales turned out to be out of f16's reach and not to be of a block of
+// zeros (mx_no_f16_among) it begins again, with the weights as bf16 and the rows as two
+// bf16 pieces, twice the MFMAs and the cuts.  (Deciding stage by stage instead doubled the registers; a look over all
 // scales first took 64 tokens x 2 of 16 experts of 11008 x 4096 from 110 to 122 us.)
 #pragma once
 
@@ -412,7 +412,13 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_w4_tile_kernel(MxArgs a, uint
       return out;
     };
     if constexpr (kF16) {
-      if (__syncthreads_or(pass(true_type{}))) pass(false_type{});
+      bool out = __syncthreads_or(pass(true_type{}));
+      if (out) {
+        const int64_t rows = last_n + 1 < BN ? last_n + 1 : BN;
+        out = __syncthreads_or(mx_no_f16_among(wbase, a.w.ldc, swbase, a.w.lds, rows, 2 * full,
+                                               NW * 64));
+      }
+      if (out) pass(false_type{});
     } else {
       pass(false_type{});
     }
