@@ -671,6 +671,11 @@ struct DxPlan {
   int tile;         // rows of a tile, 0: few rows
   uint32_t splits;
 };
+constexpr int64_t kDxSplitGroups = 512;  // workgroups that splits may make
+int64_t dx_most_splits(const qp_mx4* w) {
+  const int64_t most = ceil_div(ceil_div(w->rows, 32), kDxWaves);
+  return most > 16 ? 16 : most < 1 ? 1 : most;
+}
 DxPlan dx_plan(int32_t dtype, int64_t M, const qp_mx4* w) {
   const int64_t parts = w->matrices < M ? w->matrices : M;
   // row tiles of an expert: its last one is half empty on average
@@ -699,12 +704,24 @@ DxPlan dx_plan(int32_t dtype, int64_t M, const qp_mx4* w) {
     return p;
   }
   const int64_t wgs = (M / 16 + parts) * ceil_div(w->K, 128);
-  const int64_t most = ceil_div(ceil_div(w->rows, 32), kDxWaves);
-  int64_t s = 512 / wgs;
-  s = s > most ? most : s;
-  s = s > 16 ? 16 : s;
-  p.splits = s < 1 ? 1u : (uint32_t)s;
+  const int64_t s = kDxSplitGroups / wgs, most = dx_most_splits(w);
+  p.splits = s > most ? (uint32_t)most : s < 1 ? 1u : (uint32_t)s;
   return p;
+}
+
+// What the splits of any call of up to M rows of any type can need: for every number of
+// splits the most rows that dx_plan gives it (its row tiles are M / 16 + the experts).
+size_t dx_ws(int64_t M, const qp_mx4* w) {
+  const int64_t E = w->matrices, cols = ceil_div(w->K, 128), splits = dx_most_splits(w);
+  int64_t most = 0;
+  for (int64_t s = 2; s <= splits; ++s) {
+    const int64_t tiles = kDxSplitGroups / s / cols;
+    int64_t m = tiles >= E + E / 16 ? 16 * (tiles - E) + 15
+                                    : 16 * (tiles / 17) + (tiles % 17 < 15 ? tiles % 17 : 15);
+    m = m < M ? m : M;
+    most = most > s * m ? most : s * m;
+  }
+  return (size_t)(4 * most * w->K);
 }
 
 template <typename T>
@@ -727,18 +744,6 @@ qp_status run_dx_tile(const char* what, const MxDxArgs& a, int tile, hipStream_t
   }
 }
 
-// (the workspace does not depend on the row type: with f32 rows the few-row kernel
-// reaches further)
-size_t dx_ws(int64_t M, const qp_mx4* w) {
-  size_t most = 0;
-  for (int32_t dtype : {(int32_t)QP_F32, (int32_t)QP_BF16}) {
-    const DxPlan p = M > 0 ? dx_plan(dtype, M, w) : DxPlan{0, 1};
-    const size_t n = p.splits > 1 ? (size_t)(4 * (int64_t)p.splits * M * w->K) : 0;
-    most = n > most ? n : most;
-  }
-  return most;
-}
-
 qp_status run_dx(const char* what, const void* dY, int32_t dtype, int64_t M, int64_t lddy,
                  const qp_mx4* w, const int32_t* offsets, void* dX, int64_t lddx, void* ws,
                  size_t ws_bytes, hipStream_t stream) {
@@ -753,7 +758,7 @@ qp_status run_dx(const char* what, const void* dY, int32_t dtype, int64_t M, int
   if ((st = w4_check_float(what, "dX", dX, dtype, lddx, w->K))) return st;
   const DxPlan plan = dx_plan(dtype, M, w);
   const uint32_t splits = plan.splits;
-  const size_t need = dx_ws(M, w);
+  const size_t need = splits > 1 ? dx_ws(M, w) : 0;
   QP_REQUIRE(ws_bytes >= need, QP_ESIZE, "%s: needs a workspace of %zu bytes, has %zu", what, need,
              ws_bytes);
   QP_REQUIRE(!need || (ws && (uintptr_t)ws % 256 == 0), QP_EALIGN,

@@ -616,7 +616,8 @@ qp_status qgemm_w4_experts(const void* X, int32_t dtype, int64_t x_rows, int64_t
  *            both of `dtype`.
  *   offsets  as qgemm_w4_experts; rows of no expert get zeros.
  *   ws       device workspace of qgemm_w4_dx_ws_size bytes (0: may be NULL),
- *            256-byte aligned.  experts = 1 for the dense product.
+ *            256-byte aligned, asked for with the call's own M (more rows can need
+ *            less).  experts = 1 for the dense product.
  * Each term dY * W is formed to within 2^-15 of itself (2^-22 for f32 rows;
  * terms below 2^-100 have fewer bits), sums are f32.  A row of dY with an
  * infinity or a NaN gives infinities or NaNs in that row of dX, not always which
@@ -806,7 +807,9 @@ qp_status qgemm_w4_mx_experts(const void* X, int32_t dtype, int64_t x_rows, int6
  *            both of `dtype`.
  *   offsets  as qgemm_w4_experts; rows of no expert get zeros.
  *   ws       device workspace of qgemm_w4_mx_dx_ws_size bytes (0: may be NULL),
- *            256-byte aligned.
+ *            256-byte aligned.  The size grows with M, up to 4 MiB: one for the most
+ *            rows serves every call of fewer, of any type.  (Calls of many rows use
+ *            none and may be given NULL.)
  */
 qp_status qgemm_w4_mx_dx_ws_size(int64_t M, const qp_mx4* w, size_t* bytes);
 qp_status qgemm_w4_mx_dx(const void* dY, int32_t dtype, int64_t M, int64_t lddy, const qp_mx4* w,
