@@ -51,7 +51,9 @@ struct A4Tile {
 
 // kWide (four words of scales a row and more): a row's scales of 512 K come by one
 // lane's 16 bytes; those of the last 512 K end with the row's last word.
-template <int BM, int BN, int WM, int WN, int D, bool kWide>
+// kFar: rows further from each other, or from the first, than 32-bit offsets reach; each
+// lane has addresses of its own for them.
+template <int BM, int BN, int WM, int WN, int D, bool kWide, bool kFar>
 __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, uint32_t row_slots,
                                                                    uint32_t col_groups) {
   using L = A4Tile<BM, BN, WM, WN, D>;
@@ -59,6 +61,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW, kSRows = kWide ? 64 : 16,
                 kSI = (BM + BN) / kSRows, kS = (kSI + NW - 1) / NW;
   static_assert(kA * 8 * NW == BM && kB * 8 * NW == BN && BM % kSRows == 0, "shares");
+  static_assert(!kFar || D == 2, "waits of the far loads");
   extern __shared__ __attribute__((aligned(16))) uint8_t mx_lds[];
   lds_u8* const ring = (lds_u8*)mx_lds;
   lds_u8* const scales = ring + D * L::kStage;
@@ -94,6 +97,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   const uint8_t* const swbase = a.w.scales + tile.expert * a.w.sstride + n0 * a.w.lds;
   const int64_t last_n = N - 1 - n0;
   uint32_t va[kA], vb[kB], vs[kS];
+  const uint8_t *pa[kFar ? kA : 1], *ps[kFar ? kS : 1];
 #pragma unroll
   for (int j = 0; j < kB; ++j) {
     const int64_t n = (wave * kB + j) * 8 + lrow;
@@ -110,12 +114,20 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
     return i < kA ? (wave * kA + i) * 8 + lrow : scale_part(i - kA) * kSRows + srow;
   }, x);
 #pragma unroll
-  for (int j = 0; j < kA; ++j) va[j] = (uint32_t)(x[j] * a.a.ldc) + piece(j) * 16;
+  for (int j = 0; j < kA; ++j) {
+    if constexpr (kFar)
+      pa[j] = abase + x[j] * a.a.ldc + piece(j) * 16;
+    else
+      va[j] = (uint32_t)(x[j] * a.a.ldc) + piece(j) * 16;
+  }
 #pragma unroll
   for (int j = 0; j < kS; ++j) {
     const int i = scale_part(j);
     if (i * kSRows < BM) {
-      vs[j] = (uint32_t)(x[kA + j] * a.a.lds) + sdw * 4;
+      if constexpr (kFar)
+        ps[j] = sabase + x[kA + j] * a.a.lds + sdw * 4;
+      else
+        vs[j] = (uint32_t)(x[kA + j] * a.a.lds) + sdw * 4;
     } else {
       const int64_t n = i * kSRows + srow - BM;
       vs[j] = (uint32_t)((n < last_n ? n : last_n) * a.w.lds) + sdw * 4;
@@ -126,28 +138,40 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
   // Pieces past the row's last block and words past its last scale are read from the
   // stage's first (the cut stage puts them to zero).  A stage past the last one asks
   // for nothing: its buffers' range is empty, so that every round of the loop has the
-  // same loads to wait for.
+  // same loads to wait for (far rows: for the first stage's, which no one reads there).
   const int G = (int)a.w.G, full = G / 8, stages = (G + 7) / 8, words = (G + 3) / 4;
   const int over = mx_scales_over(words);
   auto late = [&](int s) { return kWide && mx_scales_end(s) > words ? over : 0; };
   auto issue = [&](int s, auto with_scales) {
     lds_u8* const to = ring + (s % D) * L::kStage;
     const int range = s < stages ? 0x7fffffff : 0;
-    auto back = [&](int j) { return s * 8 + piece(j) < G ? 0u : piece(j) * 16u; };
+    const int from = kFar && s >= stages ? 0 : s;
+    auto back = [&](int j) { return from * 8 + piece(j) < G ? 0u : piece(j) * 16u; };
 #pragma unroll
-    for (int j = 0; j < kA; ++j)
-      dma_to_lds<16>(abase, range, to + (wave * kA + j) * 1024, va[j] - back(j),
-                     s * 128);
+    for (int j = 0; j < kA; ++j) {
+      if constexpr (kFar)
+        far_to_lds<16>(pa[j] + (from * 128 - (int)back(j)), to + (wave * kA + j) * 1024);
+      else
+        dma_to_lds<16>(abase, range, to + (wave * kA + j) * 1024, va[j] - back(j),
+                       s * 128);
+    }
 #pragma unroll
     for (int j = 0; j < kB; ++j)
       dma_to_lds<16>(wbase, range, to + BM * 128 + (wave * kB + j) * 1024, vb[j] - back(j),
                      s * 128);
     if constexpr (decltype(with_scales)::value) {
       lds_u8* const st = scales + ((s >> 1) % L::kSpans) * L::kScales;
-      const uint32_t sback = kWide || s * 2 + sdw < words ? 0u : sdw * 4u;
+      const uint32_t sback = kWide || from * 2 + sdw < words ? 0u : sdw * 4u;
 #pragma unroll
       for (int j = 0; j < kS; ++j) {
         const int i = scale_part(j);
+        if constexpr (kFar) {
+          if (i * kSRows < BM) {
+            far_to_lds<kWide ? 16 : 4>(ps[j] + (from * 8 - late(from) - (int)sback),
+                                       st + i * kSRows * 16);
+            continue;
+          }
+        }
         dma_to_lds<kWide ? 16 : 4>(i * kSRows < BM ? sabase : swbase, range,
                                    st + i * kSRows * 16, vs[j] - sback, s * 8 - late(s));
       }
@@ -320,14 +344,14 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_a4w4_tile_kernel(MxArgs a, ui
     run(std::integral_constant<int, FM>{});
 }
 
-template <int BM, int BN, int WM, int WN, int D, bool kWide>
+template <int BM, int BN, int WM, int WN, int D, bool kWide, bool kFar>
 qp_status launch_tile_of(const MxArgs& a, hipStream_t stream) {
   using L = A4Tile<BM, BN, WM, WN, D>;
   const int64_t slots = w4_tile_slots(a.rows, BM), groups = ceil_div(a.w.rows, BN);
   const int64_t grid = mx_tile_grid(slots, groups, BM >= 256);
   QP_REQUIRE(grid * L::NW * 64 < (INT64_C(1) << 32), QP_EUNSUPPORTED,
              "qgemm_a4w4_mx: rows and channels for more than 2^32 threads");
-  auto kern = mx_a4w4_tile_kernel<BM, BN, WM, WN, D, kWide>;
+  auto kern = mx_a4w4_tile_kernel<BM, BN, WM, WN, D, kWide, kFar>;
   static std::atomic<uint64_t> reserved{0};
   if (qp_status st =
           mx_reserve_lds("qgemm_a4w4_mx", reinterpret_cast<const void*>(kern), L::kLds, reserved))
@@ -337,10 +361,10 @@ qp_status launch_tile_of(const MxArgs& a, hipStream_t stream) {
   return check_launch("qgemm_a4w4_mx (many rows)");
 }
 
-template <int BM, int BN, int WM, int WN, int D>
+template <int BM, int BN, int WM, int WN, int D, bool kFar = false>
 qp_status launch_tile(const MxArgs& a, hipStream_t stream) {
-  return a.w.G > 12 ? launch_tile_of<BM, BN, WM, WN, D, true>(a, stream)
-                    : launch_tile_of<BM, BN, WM, WN, D, false>(a, stream);
+  return a.w.G > 12 ? launch_tile_of<BM, BN, WM, WN, D, true, kFar>(a, stream)
+                    : launch_tile_of<BM, BN, WM, WN, D, false, kFar>(a, stream);
 }
 
 // Which kernel (MxCost, mx_choose).  Measured, cold weights: e.g. 16 x 4096 rows of 16 / 32
@@ -364,9 +388,17 @@ const MxCost& mx_a4w4_shape(int64_t M, int64_t parts, int64_t N) {
 
 qp_status run_mx_a4w4(const MxArgs& a, hipStream_t stream) {
   const int64_t apart = a.a.ldc > a.a.lds ? a.a.ldc : a.a.lds;
-  if (!mx_tile_reaches(a.rows, apart) || a.w.ldc >= kMxMaxLd || a.w.lds >= kMxMaxLd)
+  const MxShape shape =
+      mx_a4w4_shape(a.rows.M, a.rows.offsets ? a.rows.experts : 1, a.w.rows).shape;
+  const bool weights = a.w.ldc < kMxMaxLd && a.w.lds < kMxMaxLd;
+  // Rows past the offsets' reach, by tiles of 128 rows and by 16: 64 x 11008 x 4096 13 and 34
+  // us, 128 x 4096 x 4096 16 and 27, 1024 rows 26 and 131, 4096 tokens x 2 of 8 experts of
+  // 11008 x 4096 346 and 2917 (268 within reach).
+  if (!mx_tile_reaches(a.rows, apart) || !weights) {
+    if (shape >= kMxTile64x64 && weights) return launch_tile<128, 128, 2, 2, 2, true>(a, stream);
     return mx_launch_rows<mx4_t, 1, 1, 8, 4>(a, stream);
-  switch (mx_a4w4_shape(a.rows.M, a.rows.offsets ? a.rows.experts : 1, a.w.rows).shape) {
+  }
+  switch (shape) {
     case kMxTile256x256: return launch_tile<256, 256, 2, 4, 2>(a, stream);
     case kMxTile128x128: return launch_tile<128, 128, 2, 2, 2>(a, stream);
     case kMxTile64x64: return launch_tile<64, 64, 2, 2, 4>(a, stream);

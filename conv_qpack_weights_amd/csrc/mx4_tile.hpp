@@ -29,6 +29,17 @@ __device__ __forceinline__ void dma_to_lds(const void* base, int range, lds_u8* 
 #endif
 }
 
+// The same from an address of the lane's own, anywhere in memory.
+template <int kBytes>
+__device__ __forceinline__ void far_to_lds(const uint8_t* from, lds_u8* dst) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (kBytes == 16)
+    __builtin_amdgcn_global_load_lds((const glb_void_t*)from, (lds_void_t*)dst, 16, 0, 0);
+  else
+    __builtin_amdgcn_global_load_lds((const glb_void_t*)from, (lds_void_t*)dst, 4, 0, 0);
+#endif
+}
+
 // Rows of 128 bytes in LDS: the 16-byte piece c of row r lies at place c ^ mx_turn(r)
 // of the row's eight, so that the 16 rows whose pieces are read at a time are at 16
 // different places of the banks' 256 bytes.
