@@ -785,8 +785,11 @@ qp_status qgemm_a4w4_mx_experts(const qp_mx4* a, const int32_t* rows, int64_t ro
  *   weights; arguments as qgemm_w4_blockwise and qgemm_w4_experts with w (one
  *   matrix, or one an expert) in place of the blob.  The weights are exact, the
  *   rows keep their own type's accuracy, the sums are f32.
- * Range: a weight above the f32 range (s of 253 and more) is an infinity; f32 rows
- * are held to 2^-133.
+ * Range: weights of every scale below 253 are exact, and above it those below 2^128
+ * (products of MXFP4 rows: all, no value is formed alone).  A weight of 2^128 and more
+ * counts as an infinity: its outputs, and its column of the gradient, are infinities or
+ * NaN -- f32 and f16 rows are multiplied in pieces, and a piece that is zero makes it a
+ * NaN.  f32 rows are held to 2^-133.
  */
 qp_status qgemm_w4_mx(const void* X, int32_t dtype, int64_t M, int64_t K, int64_t ldx,
                       const qp_mx4* w, const float* bias, float clamp_lo, float clamp_hi, void* Y,
