@@ -974,7 +974,7 @@ class MX4:
     bytes up to the next multiple of 4 behind a row's scales there); an expert's matrix
     is ``m[e]``.  Every call looks where the tensors lie: the parameters that a matrix
     was made of may move (``module.to()``)."""
-    __slots__ = ("_codes", "_scales", "K", "_desc", "_seen", "_gpu")
+    __slots__ = ("_codes", "_scales", "K", "_desc", "_seen", "_gpu", "_dims")
 
     def __init__(self, codes, scales, K):
         self._codes, self._scales, self.K = codes, scales, K
@@ -1035,6 +1035,7 @@ class MX4:
                              sstride)
         gpu = codes.get_device()
         self._gpu = gpu if scales.get_device() == gpu else -1
+        self._dims = len(lead) + 2
         self._look()
 
     @classmethod
@@ -1045,7 +1046,7 @@ class MX4:
         m = cls.__new__(cls)
         m._codes = codes = like.new_empty((*lead, rows, 16 * G), dtype=torch.uint8)
         m._scales = scales = _mx4_scales((*lead, rows), G, like)
-        m.K, m._seen, m._gpu = K, None, codes.get_device()
+        m.K, m._seen, m._gpu, m._dims = K, None, codes.get_device(), len(lead) + 2
         if lead:
             m._desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), rows, K, 16 * G, padded, lead[0],
                               16 * G * rows, padded * rows)
@@ -1063,12 +1064,12 @@ class MX4:
 
     def __getitem__(self, e):
         d = self.desc
-        assert self._codes.dim() == 3, "one matrix only"
+        assert self._dims == 3, "one matrix only"
         codes, scales = self._codes[e], self._scales[e]
         if type(e) is not int:
             return MX4(codes, scales, self.K)
         m = MX4.__new__(MX4)
-        m._codes, m._scales, m.K, m._seen, m._gpu = codes, scales, d.K, None, self._gpu
+        m._codes, m._scales, m.K, m._seen, m._gpu, m._dims = codes, scales, d.K, None, self._gpu, 2
         m._desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), d.rows, d.K, d.ld_codes, d.ld_scales,
                           1, 0, 0)
         return m
@@ -1156,7 +1157,7 @@ def _is_mx4(m, what, dims=2):
         s = m._scales
         if (c.data_ptr(), s.data_ptr(), c.stride(), s.stride(), c.shape, s.shape) != seen:
             m._describe()
-    assert c.dim() == dims, "%s must be %s" % (
+    assert m._dims == dims, "%s must be %s" % (
         what, "one matrix" if dims == 2 else "a matrix an expert")
     return m._desc
 
@@ -1177,8 +1178,8 @@ def qquantize_rows_mx4(X: torch.Tensor, rule="floor", out=None) -> MX4:
     else:
         assert isinstance(out, MX4) and out.shape == (*lead, K), "out must be of X's shape"
         d = out.desc
-        assert out._codes.dim() == 2 or (out._codes.is_contiguous() and
-                                         d.scales_stride == d.rows * d.ld_scales), \
+        assert out._dims == 2 or (out._codes.is_contiguous() and
+                                   d.scales_stride == d.rows * d.ld_scales), \
             "out's matrices must follow each other"
     gpu = _mx_gpu("qquantize_rows_mx4", X.get_device(), out)
     _mx_call("qquantize_rows_mx4", gpu, X.data_ptr(), dt, M, K, ldx, _MX_RULES[rule], d.codes,
