@@ -396,7 +396,7 @@ qp_status run_mx_a4w4(const MxArgs& a, hipStream_t stream) {
   // 11008 x 4096 346 and 2917 (268 within reach).
   if (!mx_tile_reaches(a.rows, apart) || !weights) {
     if (shape >= kMxTile64x64 && weights) return launch_tile<128, 128, 2, 2, 2, true>(a, stream);
-    return mx_launch_rows<mx4_t, 1, 1, 8, 4>(a, stream);
+    return mx_launch_rows<mx4_t, 1, 8>(a, stream);
   }
   switch (shape) {
     case kMxTile256x256: return launch_tile<256, 256, 2, 4, 2>(a, stream);

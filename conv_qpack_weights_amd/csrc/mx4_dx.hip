@@ -53,11 +53,11 @@ __device__ __forceinline__ void mx_columns(const uint32_t (&w)[8], const float (
 }
 
 // ---- few rows ------------------------------------------------------------------
-// A workgroup owns 16 kFM rows and 128 columns of one split of the channels; its
+// A workgroup owns 16 rows and 128 columns of one split of the channels; its
 // waves take every kWaves-th step of 32 channels and meet in LDS in a fixed
 // order.  More than one split: the sums go to `part`, added up by the kernel
 // below.
-template <typename T, int kFM, int kWaves>
+template <typename T, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) void mx_dx_rows_kernel(MxDxArgs a, uint32_t row_slots,
                                                                  uint32_t splits) {
   constexpr int NP = MxFrag<T>::kPieces;
@@ -69,26 +69,20 @@ __global__ __launch_bounds__(kWaves * 64) void mx_dx_rows_kernel(MxDxArgs a, uin
   const uint32_t id = xcd_run(blockIdx.x, gridDim.x);
   const uint32_t slot = id % row_slots, rest = id / row_slots;
   const uint32_t cb = rest % cols, split = rest / cols;
-  const W4Tile tile = w4_find_tile<16 * kFM>(a.rows, slot);
+  const W4Tile tile = w4_find_tile<16>(a.rows, slot);
   if (tile.expert < 0) return;
   const int64_t k0 = (int64_t)cb * 128, N = a.w.rows, K = a.w.K;
   const bool none = a.rows.offsets && tile.expert == a.rows.experts;
   const int ch = lane & 15, quad = lane >> 4;
 
-  f32x4 acc[kFM][8];
+  f32x4 acc[8];
 #pragma unroll
-  for (int f = 0; f < kFM; ++f)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[f][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j = 0; j < 8; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   if (!none) {
-    const T* dy[kFM];
-#pragma unroll
-    for (int f = 0; f < kFM; ++f) {
-      int64_t r = tile.r0 + f * 16 + ch;
-      r = r < tile.r1 ? r : tile.r1 - 1;
-      dy[f] = static_cast<const T*>(a.dY) + r * a.lddy;
-    }
+    int64_t r = tile.r0 + ch;
+    r = r < tile.r1 ? r : tile.r1 - 1;
+    const T* const dy = static_cast<const T*>(a.dY) + r * a.lddy;
     // columns past K's last block read the row's first word: not stored
     const bool col_in = k0 / 32 + ch / 4 < a.w.G;
     const uint8_t* codes = a.w.codes + tile.expert * a.w.cstride + (col_in ? k0 / 2 + 4 * ch : 0);
@@ -99,7 +93,7 @@ __global__ __launch_bounds__(kWaves * 64) void mx_dx_rows_kernel(MxDxArgs a, uin
     for (int64_t s = (int64_t)split * kWaves + wave; s < steps; s += (int64_t)splits * kWaves) {
       const int64_t n0 = s * 32 + quad * 8;
       uint32_t w[8], sc[8];
-      MxFrag<T> x[kFM];
+      MxFrag<T> x;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t n = n0 + i < N ? n0 + i : N - 1;
@@ -108,50 +102,42 @@ __global__ __launch_bounds__(kWaves * 64) void mx_dx_rows_kernel(MxDxArgs a, uin
       }
       const int64_t left = N - n0;
       const int n = left > 8 ? 8 : left < 0 ? 0 : (int)left;
-#pragma unroll
-      for (int f = 0; f < kFM; ++f) x[f].load_n(dy[f] + (n > 0 ? n0 : 0), n);
+      x.load_n(dy + (n > 0 ? n0 : 0), n);
       float by[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)  // (a channel past the last: its scale could be a NaN)
         by[i] = mx_scale(i < n ? (sc[i] >> shift) & 0xffu : 0u);
       bf16x8 o[8];
       mx_columns(w, by, o);
+      bf16x8 xv[NP];
+      x.split(xv);
 #pragma unroll
-      for (int f = 0; f < kFM; ++f) {
-        bf16x8 xv[NP];
-        x[f].split(xv);
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int p = 0; p < NP; ++p) acc[f][j] = mfma32(xv[p], o[j], acc[f][j]);
-      }
+        for (int p = 0; p < NP; ++p) acc[j] = mfma32(xv[p], o[j], acc[j]);
     }
   }
 
   // thread: 8 columns of a row
 #pragma unroll
-  for (int f = 0; f < kFM; ++f) {
-    if (f) __syncthreads();
+  for (int j = 0; j < 8; ++j) red[wave][j][lane] = acc[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 256; i += kWaves * 64) {
+    const int m = i >> 4, c = i & 15;
+    const int64_t r = tile.r0 + m, col = k0 + 8 * c;
+    if (r >= tile.r1 || col >= K) continue;
+    float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) red[wave][j][lane] = acc[f][j];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 256; i += kWaves * 64) {
-      const int m = i >> 4, c = i & 15;
-      const int64_t r = tile.r0 + f * 16 + m, col = k0 + 8 * c;
-      if (r >= tile.r1 || col >= K) continue;
-      float y[8];
+    for (int j = 0; j < 8; ++j) {
+      y[j] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        y[j] = 0.0f;
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) y[j] += red[v][j][(m >> 2) * 16 + c][m & 3];
-      }
-      const int n = K - col < 8 ? (int)(K - col) : 8;
-      if (splits > 1)
-        w4_store8(a.part + (int64_t)split * a.rows.M * K, QP_F32, r * K + col, y, n);
-      else
-        w4_store8(a.dX, a.dtype, r * a.lddx + col, y, n);
+      for (int v = 0; v < kWaves; ++v) y[j] += red[v][j][(m >> 2) * 16 + c][m & 3];
     }
+    const int n = K - col < 8 ? (int)(K - col) : 8;
+    if (splits > 1)
+      w4_store8(a.part + (int64_t)split * a.rows.M * K, QP_F32, r * K + col, y, n);
+    else
+      w4_store8(a.dX, a.dtype, r * a.lddx + col, y, n);
   }
 }
 
@@ -727,7 +713,7 @@ size_t dx_ws(int64_t M, const qp_mx4* w) {
 template <typename T>
 void launch_dx(const MxDxArgs& a, uint32_t slots, uint32_t splits, hipStream_t stream) {
   const int64_t cols = ceil_div(a.w.K, 128);
-  hipLaunchKernelGGL((mx_dx_rows_kernel<T, 1, kDxWaves>), dim3((unsigned)(slots * cols * splits)),
+  hipLaunchKernelGGL((mx_dx_rows_kernel<T, kDxWaves>), dim3((unsigned)(slots * cols * splits)),
                      dim3(kDxWaves * 64), 0, stream, a, slots, splits);
 }
 

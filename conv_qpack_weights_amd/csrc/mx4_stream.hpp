@@ -47,7 +47,7 @@ __global__ __launch_bounds__(kWaves * 64) void mx_stream_kernel(MxArgs a, uint32
   const W4Tile tile = w4_find_tile<16>(a.rows, slot);
   if (tile.expert < 0) return;
   const int64_t n0 = (int64_t)group * kTiles * 16, N = a.w.rows;
-  if (mx_rows_of_none<1, kTiles, kWaves>(a, tile, n0)) return;
+  if (mx_rows_of_none<kTiles, kWaves>(a, tile, n0)) return;
 
   // what a lane loads: a piece of row lane / 8 of eight; rows past the tile's end
   // repeat its last row
@@ -111,22 +111,22 @@ __global__ __launch_bounds__(kWaves * 64) void mx_stream_kernel(MxArgs a, uint32
   };
 
   const int ch = lane & 15, quad = lane >> 4;
-  f32x4 acc[1][kTiles];
+  f32x4 acc[kTiles];
 #pragma unroll
-  for (int c = 0; c < kTiles; ++c) acc[0][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  typedef MxStage<T, 1, kTiles> Stage;
+  for (int c = 0; c < kTiles; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  typedef MxStage<T, kTiles> Stage;
   auto at = [&](int c) { return (ch & 7) * 128 + (c ^ mx_turn(ch)) * 16; };
   auto read = [&](Stage (&st)[2], int g) {
     const lds_u8* from = mine + (g & 1) * L::kBuf + (ch >> 3) * kParts * 1024;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if constexpr (kA4) {
-        st[j].x[0] = *(const __attribute__((address_space(3))) u32x4*)(from + at(4 * j + quad));
+        st[j].x = *(const __attribute__((address_space(3))) u32x4*)(from + at(4 * j + quad));
       } else {
         // elements 128 j + 32 quad + 8 t ..: piece 4 (quad & 1) + t of part 2 j + quad / 2
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          st[j].x[0][t].v = *(const __attribute__((address_space(3))) u32x4*)(
+          st[j].x[t].v = *(const __attribute__((address_space(3))) u32x4*)(
               from + (2 * j + (quad >> 1)) * 1024 + at(4 * (quad & 1) + t));
       }
     }
@@ -145,8 +145,8 @@ __global__ __launch_bounds__(kWaves * 64) void mx_stream_kernel(MxArgs a, uint32
     if constexpr (kA4) {
       const u32x2 v =
           *(const __attribute__((address_space(3))) u32x2*)(s + L::kScaleLoads * 256);
-      st[0].xs[0] = v.x;
-      st[1].xs[0] = v.y;
+      st[0].xs = v.x;
+      st[1].xs = v.y;
     }
   };
 
@@ -159,14 +159,14 @@ __global__ __launch_bounds__(kWaves * 64) void mx_stream_kernel(MxArgs a, uint32
     read(st, g);
     // (the next round loads into what is read here)
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    mx_step<T, 1, kTiles>(st[0], quad, acc);
-    mx_step<T, 1, kTiles>(st[1], quad, acc);
+    mx_step<T, kTiles>(st[0], quad, acc);
+    mx_step<T, kTiles>(st[1], quad, acc);
   }
   if (wave == kWaves - 1 && (int64_t)groups * 256 < a.w.K)
-    mx_rows_tail<T, 1, kTiles>(a, tile, n0, (int64_t)groups * 2, acc);
+    mx_rows_tail<T, kTiles>(a, tile, n0, (int64_t)groups * 2, acc);
   wait_vmcnt<0>();
   __syncthreads();
-  mx_rows_store<1, kTiles, kWaves>(acc, a, tile, n0, reinterpret_cast<f32x4*>(mx_lds));
+  mx_rows_store<kTiles, kWaves>(acc, a, tile, n0, reinterpret_cast<f32x4*>(mx_lds));
 }
 
 template <typename T, int kTiles, int kWaves, bool kOnce>

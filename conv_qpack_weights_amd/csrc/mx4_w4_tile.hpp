@@ -498,7 +498,7 @@ qp_status mx_run_16bit(const MxArgs& a, hipStream_t stream) {
   if ((uintptr_t)a.X % 4 || a.ldx % 2 || !mx_tile_reaches(a.rows, a.ldx * 2) || !weights) {
     if (shape >= kMxTile128x128 && weights)
       return mx_launch_w4_tile<T, false, 128, 128, 2, 2, 2>(a, stream);
-    return mx_launch_rows<T, 1, 2, 8, 4>(a, stream);
+    return mx_launch_rows<T, 2, 8>(a, stream);
   }
   switch (shape) {
     case kMxRows16x16: return mx_launch_stream<T, 1, 4>(a, stream);
