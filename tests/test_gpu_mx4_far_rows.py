@@ -3,6 +3,8 @@ rows 8 MiB apart -- in products of many rows: the same results as from rows that
 together, as far as 2^31 outputs and more.  Tolerances as in test_gpu_mx4.py."""
 import pytest
 
+import mx4_card as card
+
 pytestmark = pytest.mark.gpu
 
 
@@ -12,24 +14,6 @@ def qp():
     assert torch.cuda.is_available(), "GPU tests need an MI355X"
     import conv_qpack_weights_amd as qp
     return qp
-
-
-def _matrix(qp, g, *shape):
-    """A random MX4, and its values in f64 on the card."""
-    import torch
-    *lead, K = shape
-    G = -(-K // 32)
-    codes = torch.randint(0, 256, (*lead, 16 * G), generator=g, dtype=torch.uint8)
-    if K % 32:
-        both = torch.stack((codes & 15, codes >> 4), -1).reshape(*lead, 32 * G)
-        both[..., K:] = 0
-        codes = both[..., 0::2] | (both[..., 1::2] << 4)
-    scales = torch.randint(118, 130, (*lead, G), generator=g, dtype=torch.uint8)
-    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
-    grid = torch.cat((grid, -grid))
-    v = grid[torch.stack((codes & 15, codes >> 4), -1).long()].reshape(*lead, 32 * G)
-    v = v * torch.pow(2.0, scales.double() - 127).repeat_interleave(32, -1)
-    return qp.mx4_tensor(codes.cuda(), scales.cuda(), K), v[..., :K].cuda()
 
 
 def _apart(qp, m, ldc, lds):
@@ -42,15 +26,6 @@ def _apart(qp, m, ldc, lds):
     return qp.MX4(c, s, m.K)
 
 
-def _close(got, want, A, K, what):
-    import torch
-    got = got.double()
-    assert torch.isfinite(got).all(), what
-    tol = (3 * K / 32 + 64) * 2.0 ** -23 * A
-    off = (got - want).abs()
-    assert (off <= tol).all(), "%s: %d outputs off" % (what, int((off > tol).sum()))
-
-
 # one to eight stages of K, whole and cut, few and many words of scales
 @pytest.mark.parametrize("K", [31, 256, 330, 416, 770, 1500, 2048])
 @pytest.mark.parametrize("kernel,M,N", [("tile64x64", 600, 2000), ("tile128x128", 2600, 2000)])
@@ -59,8 +34,8 @@ def test_rows_through_the_map(qp, kernel, M, N, K):
     g = torch.Generator().manual_seed(M + K)
     T = 300
     ldc = 1 << 23 if K == 330 else ((1 << 31) // T + 16) // 16 * 16
-    W, w = _matrix(qp, g, 3, N, K)
-    A, a = _matrix(qp, g, T, K)
+    W, w = card.matrix(qp, g, 3, N, K)
+    A, a = card.matrix(qp, g, T, K)
     assert qp.qgemm_mx_kernel_name("a4w4", M, W, torch.float32) == kernel
     far = _apart(qp, A, ldc, 2048)
     off = torch.tensor([0, M // 5, M // 5, M - 9])
@@ -75,8 +50,8 @@ def test_rows_through_the_map(qp, kernel, M, N, K):
     for e in range(3):
         s = slice(int(off[e]), int(off[e + 1]))
         b = bias[e].double()
-        _close(got[s], x[s] @ w[e].t().contiguous() + b,
-               x[s].abs() @ w[e].abs().t().contiguous() + b.abs(), K, "expert %d" % e)
+        card.close(got[s], x[s] @ card.t(w[e]) + b,
+               x[s].abs() @ card.t(w[e]).abs() + b.abs(), K, "f32", "expert %d" % e)
     assert (got[M - 9:] == 0).all()
 
 
@@ -86,13 +61,13 @@ def test_rows_far_apart_in_tiles(qp, K):
     import torch
     g = torch.Generator().manual_seed(K)
     M, N, far = 300, 4010, 1 << 23
-    W, w = _matrix(qp, g, N, K)
-    A, a = _matrix(qp, g, M, K)
+    W, w = card.matrix(qp, g, N, K)
+    A, a = card.matrix(qp, g, M, K)
     assert qp.qgemm_mx_kernel_name("a4w4", M, W, torch.float32).startswith("tile")
-    want, size = a @ w.t().contiguous(), a.abs() @ w.abs().t().contiguous()
+    want, size = a @ card.t(w), a.abs() @ card.t(w).abs()
     for ldc, lds in ((far, 64), (-(-K // 32) * 16, far)):
         print("mx4 far apart in tiles", K, ldc, lds, flush=True)
-        _close(qp.qgemm_a4w4_mx(_apart(qp, A, ldc, lds), W), want, size, K, "far")
+        card.close(qp.qgemm_a4w4_mx(_apart(qp, A, ldc, lds), W), want, size, K, "f32", "far")
 
 
 def test_more_outputs_than_a_launch_of_small_tiles(qp):
@@ -100,15 +75,15 @@ def test_more_outputs_than_a_launch_of_small_tiles(qp):
     import torch
     g = torch.Generator().manual_seed(9)
     M, N, K, T = 1 << 20, 2064, 64, 2100
-    W, w = _matrix(qp, g, 1, N, K)
-    A, a = _matrix(qp, g, T, K)
+    W, w = card.matrix(qp, g, 1, N, K)
+    A, a = card.matrix(qp, g, T, K)
     far = _apart(qp, A, 1 << 20, 64)
     rows = torch.randint(0, T, (M,), generator=g).cuda()
     rows[:T] = torch.arange(T, device="cuda")
     offsets = torch.tensor([0, M], dtype=torch.int32, device="cuda")
     print("mx4 far rows, many outputs", flush=True)
     got = qp.qgemm_a4w4_mx_experts(far, W, offsets, rows=rows.int(), out_dtype=torch.float32)
-    _close(got[:T], a @ w[0].t().contiguous(), a.abs() @ w[0].abs().t().contiguous(), K, "first rows")
+    card.close(got[:T], a @ card.t(w[0]), a.abs() @ card.t(w[0]).abs(), K, "f32", "first rows")
     for r in range(0, M, 1 << 17):
         s = slice(r, r + (1 << 17))
         assert torch.equal(got[s], got[rows[s]]), r

@@ -6,9 +6,10 @@ code) a weight counts as infinite.  Tolerances as in test_gpu_mx4.py: rows are s
 that no term and no sum leaves the normal f32 range."""
 import pytest
 
+import mx4_card as card
+
 pytestmark = pytest.mark.gpu
 
-ROUND = {"f32": 0.0, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}
 LOW, HIGH = (0, 3), (236, 253)
 
 
@@ -20,45 +21,11 @@ def qp():
     return qp
 
 
-def _dt(name):
-    import torch
-    return {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[name]
-
-
-def _matrix(qp, g, rows, K, scales):
-    """A random MX4 with scales of a range, and its values in f64 on the card."""
-    import torch
-    G = -(-K // 32)
-    codes = torch.randint(0, 256, (rows, 16 * G), generator=g, dtype=torch.uint8)
-    if K % 32:
-        both = torch.stack((codes & 15, codes >> 4), -1).reshape(rows, 32 * G)
-        both[..., K:] = 0
-        codes = both[..., 0::2] | (both[..., 1::2] << 4)
-    s = torch.randint(*scales, (rows, G), generator=g, dtype=torch.uint8)
-    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
-    grid = torch.cat((grid, -grid))
-    v = grid[torch.stack((codes & 15, codes >> 4), -1).long()].reshape(rows, 32 * G)
-    v = v * torch.pow(2.0, s.double() - 127).repeat_interleave(32, -1)
-    return qp.mx4_tensor(codes.cuda(), s.cuda(), K), v[:, :K].cuda()
-
-
 def _rows(g, M, K, dtype, exponent, odd):
     """Rows of about 2^exponent, none of their values below a 64th of it."""
     import torch
     x = torch.randn(M, K + 3, generator=g)
-    x = (torch.copysign(x.abs().clamp_min(2.0 ** -6), x) * 2.0 ** exponent).to(_dt(dtype)).cuda()
-    x = x[:, 1:1 + K] if odd else x[:, :K].contiguous()
-    return x, x.double()
-
-
-def _close(got, want, A, terms, dtype, what):
-    import torch
-    got = got.double()
-    assert torch.isfinite(got).all(), what
-    tol = (3 * terms / 32 + 64) * 2.0 ** -23 * A + ROUND[dtype] * want.abs() * 1.01
-    off = (got - want).abs()
-    assert (off <= tol).all(), "%s: %d outputs off, worst by %.3g of its tolerance" % (
-        what, int((off > tol).sum()), float((off / tol.clamp_min(1e-300)).max()))
+    return card.rows(torch.copysign(x.abs().clamp_min(2.0 ** -6), x) * 2.0 ** exponent, dtype, odd)
 
 
 KERNELS = [("rows16x16", 5, 300), ("rows16x32", 30, 4010), ("rows16x48", 13, 9000),
@@ -73,8 +40,8 @@ def test_products(qp, kernel, M, N, dtype, end):
     import torch
     g = torch.Generator().manual_seed(M)
     K = 330
-    W, w = _matrix(qp, g, N, K, LOW if end == "low" else HIGH)
-    name = qp.qgemm_mx_kernel_name("w4", M, W, _dt(dtype))
+    W, w = card.matrix(qp, g, N, K, scales=LOW if end == "low" else HIGH)
+    name = qp.qgemm_mx_kernel_name("w4", M, W, card.DTYPE[dtype])
     assert name == kernel or (dtype == "f32" and kernel.startswith("tile"))
     print("mx4 ends", name, M, N, dtype, end, flush=True)
     # (f16 rows at the low end: terms from 2^-128 2^3 on, sums of about 2^-114, whose
@@ -83,8 +50,8 @@ def test_products(qp, kernel, M, N, dtype, end):
         {"f32": -60, "bf16": -60, "f16": -8}[dtype]
     for odd in (False, True):
         X, x = _rows(g, M, K, dtype, exponent, odd)
-        want, size = x @ w.t().contiguous(), x.abs() @ w.abs().t().contiguous()
-        _close(qp.qgemm_w4_mx(X, W, out_dtype=torch.float32), want, size, K, "f32", "odd=%s" % odd)
+        want, size = x @ card.t(w), x.abs() @ card.t(w).abs()
+        card.close(qp.qgemm_w4_mx(X, W, out_dtype=torch.float32), want, size, K, "f32", "odd=%s" % odd)
 
 
 @pytest.mark.parametrize("end", ["low", "high"])
@@ -95,13 +62,13 @@ def test_gradient(qp, kernel, M, K, dtype, end):
     import torch
     g = torch.Generator().manual_seed(K)
     N = 330
-    W, w = _matrix(qp, g, N, K, LOW if end == "low" else HIGH)
-    name = qp.qgemm_mx_kernel_name("w4_dx", M, W, _dt(dtype)).split("/")[0]
+    W, w = card.matrix(qp, g, N, K, scales=LOW if end == "low" else HIGH)
+    name = qp.qgemm_mx_kernel_name("w4_dx", M, W, card.DTYPE[dtype]).split("/")[0]
     assert name == kernel or dtype == "f32"
     print("mx4 gradient ends", name, M, K, dtype, end, flush=True)
     for odd in (False, True):
         dY, dy = _rows(g, M, N, dtype, 60 if end == "low" else -60, odd)
-        _close(qp.qgemm_w4_mx_dx(dY, W), dy @ w, dy.abs() @ w.abs(), N, dtype, "odd=%s" % odd)
+        card.close(qp.qgemm_w4_mx_dx(dY, W), dy @ w, dy.abs() @ w.abs(), N, dtype, "odd=%s" % odd)
 
 
 @pytest.mark.parametrize("a_scales,w_scales", [((0, 3), (252, 255)), ((252, 255), (0, 3)),
@@ -114,11 +81,11 @@ def test_both_operands_at_their_ends(qp, kernel, M, N, a_scales, w_scales):
     import torch
     g = torch.Generator().manual_seed(N)
     K = 330
-    W, w = _matrix(qp, g, N, K, w_scales)
-    A, a = _matrix(qp, g, M, K, a_scales)
+    W, w = card.matrix(qp, g, N, K, scales=w_scales)
+    A, a = card.matrix(qp, g, M, K, scales=a_scales)
     assert qp.qgemm_mx_kernel_name("a4w4", M, W) == kernel
     print("mx4 both ends", kernel, M, N, a_scales, w_scales, flush=True)
-    _close(qp.qgemm_a4w4_mx(A, W), a @ w.t().contiguous(), a.abs() @ w.abs().t().contiguous(), K,
+    card.close(qp.qgemm_a4w4_mx(A, W), a @ card.t(w), a.abs() @ card.t(w).abs(), K,
            "f32", "a4w4")
 
 
@@ -130,7 +97,7 @@ def test_weights_above_the_range(qp, kernel, M, N, dtype):
     import torch
     g = torch.Generator().manual_seed(M)
     K = 330
-    W, w = _matrix(qp, g, N, K, (118, 130))
+    W, w = card.matrix(qp, g, N, K)
     out = torch.tensor([1, N // 2, N - 1], device="cuda")
     W.scales[out, 3] = torch.tensor([253, 254, 254], dtype=torch.uint8, device="cuda")
     W.codes[out, 48:64] = 0
@@ -145,7 +112,7 @@ def test_weights_above_the_range(qp, kernel, M, N, dtype):
         assert torch.equal(y[:, out], (sign * float("inf")).float())
     rest = torch.ones(N, dtype=torch.bool, device="cuda")
     rest[out] = False
-    _close(y[:, rest], x @ w[rest].t().contiguous(), x.abs() @ w[rest].abs().t().contiguous(), K,
+    card.close(y[:, rest], x @ card.t(w[rest]), x.abs() @ card.t(w[rest]).abs(), K,
            "f32", "others")
     dY, dy = _rows(g, 20, N, dtype, -8, False)
     d = qp.qgemm_w4_mx_dx(dY, W)
@@ -153,4 +120,4 @@ def test_weights_above_the_range(qp, kernel, M, N, dtype):
     cols = torch.ones(K, dtype=torch.bool, device="cuda")
     cols[96:128] = False
     v = w[:, cols]
-    _close(d[:, cols], dy @ v, dy.abs() @ v.abs(), N, dtype, "other columns")
+    card.close(d[:, cols], dy @ v, dy.abs() @ v.abs(), N, dtype, "other columns")
