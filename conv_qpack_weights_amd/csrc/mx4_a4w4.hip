@@ -33,9 +33,10 @@ __device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, uint32_t sa, u32x4 b, uint3
 // rows an operand takes piece c of meet every bank alike.  The weights are the
 // MFMA's first operand: a lane ends with one row and runs of four channels.
 //
-// 8192^3, 256 x 256 tiles, on random codes: 297 us, 3.7 PFLOP/s.  Its matrix instructions
-// alone, in a loop of nothing else, take 217 (the card holds them to half its clock),
-// with the LDS reads 248; its loads alone 187.  Eight waves of 128 x 64 read 6 operands
+// 8192^3, 256 x 256 tiles, on random codes: 289 to 299 us on different cards, 3.7 PFLOP/s.
+// Its matrix instructions alone, on random codes, took 177 us in one loop of nothing else
+// and 217 in another (the card's clock gives way to them, by the operands), with the LDS
+// reads 248; its loads alone 187.  Eight waves of 128 x 64 read 6 operands
 // for 8 MFMAs; one workgroup fills a CU's LDS.  A step's operands are read ahead of the
 // MFMAs of the step before, over the barrier too.
 template <int BM, int BN, int WM, int WN, int D>

@@ -651,7 +651,8 @@ qp_status launch_dx_tile(const char* what, const MxDxArgs& a, hipStream_t stream
 // Measured, bf16, 4096 x 4096 weights, cold: 16 rows 11.6 us by the few-row kernel (128 x
 // 128 tiles 46), 256 37 (47), 512 71 (49; 256 x 256 tiles 96), 1024 132 (52), 2048 248 (81, 97),
 // 4096 456 (156, 119); of 11008 columns 1024 rows 332 (118, 100).  f32 rows: 256 53,
-// 512 94, 768 147; tiles 1024 137, 4096 556.
+// 512 94, 768 147; tiles 1024 137, 4096 556 to 580.  By expert, 2048 tokens x 2 of 8 of 4096 x
+// 4096: bf16 194 (rows at odd addresses, through registers, 292), f32 730.
 constexpr int kDxWaves = 8;
 struct DxPlan {
   int tile;         // rows of a tile, 0: few rows

@@ -493,7 +493,10 @@ qp_status mx_run_16bit(const MxArgs& a, hipStream_t stream) {
   const MxShape shape = mx_w4_shape(__is_same(T, f16_t) ? QP_F16 : QP_BF16, a.rows.M,
                                     a.rows.offsets ? a.rows.experts : 1, a.w.rows)
                             .shape;
-  // what direct loads cannot take goes through registers
+  // What direct loads cannot take goes through registers: rows at odd addresses or odd
+  // strides (bf16 16 x 4096 x 4096 15.9 us and 6.4 by direct loads, 64 rows 28.8 and 9.8, 256
+  // 104 and 20, 1024 54 and 39, 4096 167 and 105; 64 tokens x 2 of 16 experts of 11008 x 4096
+  // 223 and 93) and rows too far apart.
   const bool weights = a.w.ldc < kMxMaxLd && a.w.lds < kMxMaxLd;
   if ((uintptr_t)a.X % 4 || a.ldx % 2 || !mx_tile_reaches(a.rows, a.ldx * 2) || !weights) {
     if (shape >= kMxTile128x128 && weights)
