@@ -1054,6 +1054,10 @@ class MX4:
             m._desc = Mx4Desc(codes.data_ptr(), scales.data_ptr(), rows, K, 16 * G, padded, 1, 0, 0)
         return m
 
+    def __reduce__(self):
+        # (copies are described from tensors that both have been asked for)
+        return MX4, (self.codes, self.scales, self.K)
+
     @property
     def shape(self):
         return (*self._codes.shape[:-1], self.K)

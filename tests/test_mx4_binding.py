@@ -142,3 +142,19 @@ def test_an_experts_matrix(qp, e):
         W[3]
     single = qp.mx4_tensor(_u(3, 1, 80), _u(3, 1, 5), 150)
     assert _where(single[e].desc) == _where(qp.MX4(single.codes[e], single.scales[e], 150).desc)
+
+
+def test_copies_follow_their_tensors(qp):
+    """A copy shares the tensors of a matrix that the library made; a deep one has its own,
+    the padding behind the rows with them."""
+    import copy
+    made = qp.MX4._new(torch.zeros(1), (3,), 5, 150)
+    made_codes = made._codes
+    other = copy.copy(made)
+    assert other.codes is made_codes and _where(other.desc) == _where(made.desc)
+    made_codes.data = made_codes.data.clone()
+    assert other.desc.codes == made.desc.codes == made_codes.data_ptr()
+    deep = copy.deepcopy(made)
+    d = deep.desc
+    assert (d.codes, d.scales) == (deep.codes.data_ptr(), deep.scales.data_ptr())
+    assert d.codes != made.desc.codes and _where(d)[2:] == _where(made.desc)[2:]
