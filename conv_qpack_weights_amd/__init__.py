@@ -973,7 +973,8 @@ class MX4:
     them, rows of wider buffers too (places at multiples of 16 and 4 bytes, and the
     bytes up to the next multiple of 4 behind a row's scales there); an expert's matrix
     is ``m[e]``.  Every call looks where the tensors lie: the parameters that a matrix
-    was made of may move (``module.to()``)."""
+    was made of may move (``module.to()``).  ``m[e]`` and what :func:`mx4_tensor` laid
+    out anew stay where they are."""
     __slots__ = ("_codes", "_scales", "K", "_desc", "_seen", "_gpu", "_dims")
 
     def __init__(self, codes, scales, K):
@@ -1108,8 +1109,10 @@ def _mx4_scales(rows_shape, G, like):
 def mx4_tensor(codes: torch.Tensor, scales: torch.Tensor, K=None) -> MX4:
     """An MXFP4 matrix (or one an expert) from codes uint8 [.., rows, 16*ceil(K/32)]
     and scales uint8 [.., rows, ceil(K/32)], as checkpoints hold them: taken as they
-    are where the kernels can read them, else laid out anew (once, at load time).  The
-    values that fill up the last block of a ``K`` not a multiple of 32 must be zeros."""
+    are where the kernels can read them, else laid out anew (once, at load time: a
+    copy, which does not follow its tensor; scales are copied unless K/32 is a multiple
+    of 4).  The values that fill up the last block of a ``K`` not a multiple of 32 must
+    be zeros."""
     G = scales.shape[-1] if scales.dim() else 0
     K = 32 * G if K is None else int(K)
     _mx4_shapes(codes, scales, K)
@@ -1311,7 +1314,8 @@ def qgemm_w4_mx_dx(dY: torch.Tensor, W: MX4, out=None, ws=None):
     w = _is_mx4(W, "W")
     dt, M, lddy, out, lddx, ws, n = _mx_dx_buffers(dY, w, out, ws)
     gpu = _mx_gpu("qgemm_w4_mx_dx", dY.get_device(), W, out, ws)
-    _mx_call("qgemm_w4_mx_dx", gpu, dY.data_ptr(), dt, M, lddy, w, out.data_ptr(), lddx, _ptr(ws), n)
+    _mx_call("qgemm_w4_mx_dx", gpu, dY.data_ptr(), dt, M, lddy, w, out.data_ptr(), lddx, _ptr(ws),
+             n)
     return out
 
 

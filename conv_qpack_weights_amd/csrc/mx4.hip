@@ -45,13 +45,12 @@ qp_status run_float(const char* what, const MxArgs& a, int32_t dtype, hipStream_
 
 // The products of float rows.  Measured with bf16 rows, cold weights, all shapes on one card
 // (those that are taken, on the present kernels: 16 x 4096 6.0 to 6.4 us, 64 x 4096 9.8, 16 x
-// 11008 9.8, 64 x 11008 21.9, 1024 x 4096 39): 16 x 4096 rows of
-// 16 / 32 / 48 / 64 channels 5.6, 6.2, 7.4, 8.2 us, tiles of 32 x 64 / 32 x 128 15.7, 17.1;
-// 16 x 11008 15.7, 13.5, 10.3, 11.0, 18.2, 19.8; 64 x 4096 14.8, 10.1, 12.3, 8.3, 16.5, 17.5;
-// 64 x 11008 47, 31, 28, 24.5, 22, 20.5; 64 tokens x 2 of 16 experts of 11008 (32 channels on)
-// 152, 136, 107, 121, 112, 128 x 128 tiles 161; 4096 tokens x 2 of 8 of them tiles of 128 / 256
-// rows 776, 717; 1024 x 4096 tiles of 32 x 64 / 128 / 256 rows
-// 62, 42, 87; 8192 x 11008 1089, 667, 630.
+// 11008 9.8, 64 x 11008 21.9, 1024 x 4096 39): 16 x 4096 rows of 16 / 32 / 48 / 64 channels 5.6,
+// 6.2, 7.4, 8.2 us, tiles of 32 x 64 / 32 x 128 15.7, 17.1; 16 x 11008 15.7, 13.5, 10.3, 11.0,
+// 18.2, 19.8; 64 x 4096 14.8, 10.1, 12.3, 8.3, 16.5, 17.5; 64 x 11008 47, 31, 28, 24.5, 22,
+// 20.5; 64 tokens x 2 of 16 experts of 11008 (32 channels on) 152, 136, 107, 121, 112, 128 x 128
+// tiles 161; 4096 tokens x 2 of 8 of them tiles of 128 / 256 rows 776, 717; 1024 x 4096 tiles of
+// 32 x 64 / 128 / 256 rows 62, 42, 87; 8192 x 11008 1089, 667, 630.
 constexpr MxCost kW4Shapes[] = {
     {kMxRows16x16, 16, 16, 5.6, 5.0, 3.1, "rows16x16"},
     {kMxRows16x32, 16, 32, 6.3, 7.2, 3.8, "rows16x32"},
@@ -62,10 +61,10 @@ constexpr MxCost kW4Shapes[] = {
     {kMxTile128x128, 128, 128, 34.0, 29.0, 29.0, "tile128x128"},
     {kMxTile256x256, 256, 256, 103.0, 100.0, 100.0, "tile256x256"},
 };
-// The same of f32 rows (64 tokens x 2 of 16 experts of 11008 x 4096 197, 1024 x 2 of 8 of
-// 4096 x 4096 330): 16 x 4096 14.1, 14.8, 15.4, 16.6; 16 x 11008 38, 34, 19.6, 20.8; 64 x
-// 11008 112, 84, 58, 52; 128 x 4096 78, 56, 40, 33; 128 x 128 tiles 512 x 4096 109, 1024 x 4096
-// 115, 4096 x 4096 454.
+// The same of f32 rows (64 tokens x 2 of 16 experts of 11008 x 4096 197, 1024 x 2 of 8 of 4096 x
+// 4096 330): 16 x 4096 14.1, 14.8, 15.4, 16.6; 16 x 11008 38, 34, 19.6, 20.8; 64 x 11008 112,
+// 84, 58, 52; 128 x 4096 78, 56, 40, 33; 128 x 128 tiles 512 x 4096 109, 1024 x 4096 115, 4096 x
+// 4096 454.
 constexpr MxCost kW4ShapesF32[] = {
     {kMxRows16x16, 16, 16, 14.1, 9.2, 9.2, "rows16x16"},
     {kMxRows16x32, 16, 32, 15.2, 13.5, 13.5, "rows16x32"},

@@ -159,12 +159,12 @@ enum MxShape {
   kMxTile256x256
 };
 
-// What a shape takes at K = 4096, the only length it was measured at (the choice does not
-// look at K): `first` microseconds for up to one workgroup a CU (256); `cold` for every further round of
-// workgroups that bring weights of their own, `more` for one that finds its weights in
-// the caches (further row tiles of the same matrix).  Rounds are whole ones for the
-// few-row kernels, whose workgroups all wait for memory alike; the largest tile is one
-// to a CU, its last round in halves where it is half empty.
+// What a shape takes at K = 4096, the only length it was measured at (the choice does
+// not look at K): `first` microseconds for up to one workgroup a CU (256); `cold` for
+// every further round of workgroups that bring weights of their own, `more` for one that
+// finds its weights in the caches (further row tiles of the same matrix).  Rounds are
+// whole ones for the few-row kernels, whose workgroups all wait for memory alike; the
+// largest tile is one to a CU, its last round in halves where it is half empty.
 struct MxCost {
   MxShape shape;
   int rows, channels;

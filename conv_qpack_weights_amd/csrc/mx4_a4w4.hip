@@ -33,7 +33,7 @@ __device__ __forceinline__ f32x16 mx_mfma32(u32x4 a, uint32_t sa, u32x4 b, uint3
 // rows an operand takes piece c of meet every bank alike.  The weights are the
 // MFMA's first operand: a lane ends with one row and runs of four channels.
 //
-// 8192^3, 256 x 256 tiles, on random codes: 289 to 299 us on different cards, 3.7 PFLOP/s.
+// 8192^3, 256 x 256 tiles, on random codes: 289 to 309 us on different cards, 3.7 PFLOP/s.
 // Its matrix instructions alone, on random codes, took 177 us in one loop of nothing else
 // and 217 in another (the card's clock gives way to them, by the operands), with the LDS
 // reads 248; its loads alone 187.  Eight waves of 128 x 64 read 6 operands

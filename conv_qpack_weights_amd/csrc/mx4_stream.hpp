@@ -6,12 +6,12 @@
 // takes 128 bytes of each of eight rows, where a load of an operand takes 64 or 32
 // bytes of each of 16, and the card looks up a line at a time.
 //
-// Bound by the weights' way from memory where they are large: cold weights of 176128 x
-// 4096 (383 MB) times 1 / 8 bf16 rows 84 / 87 us, 4.6 / 4.4 TB/s.  Smaller ones take 1.6 times
+// Bound by the weights' way from memory where they are large: cold weights of 176128 x 4096
+// (383 MB) times 1 / 8 bf16 rows 84 / 87 us, 4.6 / 4.4 TB/s.  Smaller ones take 1.6 times
 // what a kernel that only reads as many bytes does, and for what is not known: 4096 x 4096
-// (8.9 MB; reading 10.5 MB 3.4 us) times 1 / 16 rows 5.2 / 6.0 to 6.4 us, times MXFP4 rows 4.9;
-// 11008 x 4096 (24 MB; reading 28 MB 5.9) 8.3 to 8.6 / 9.6 to 9.8.  With operands straight from memory
-// (mx4_rows.hpp) 16 x 4096 x 4096 took 8.3.
+// (8.9 MB; reading 10.5 MB 3.4 us) times 1 / 16 rows 5.2 / 6.0 to 6.4 us, times MXFP4 rows
+// 4.9; 11008 x 4096 (24 MB; reading 28 MB 5.9) 8.3 to 8.6 / 9.6 to 9.8.  With operands
+// straight from memory (mx4_rows.hpp) 16 x 4096 x 4096 took 8.3.
 #pragma once
 
 #include "mx4_rows.hpp"

@@ -18,8 +18,9 @@
 // f16 rows: the weights go in as f16 and the rows as they are; where one of a
 // workgroup's scales turned out to be out of f16's reach and not to be of a block of
 // zeros (mx_no_f16_among) it begins again, with the weights as bf16 and the rows as two
-// bf16 pieces, twice the MFMAs and the cuts.  (Deciding stage by stage instead doubled the registers; a look over all
-// scales first took 64 tokens x 2 of 16 experts of 11008 x 4096 from 110 to 122 us.)
+// bf16 pieces, twice the MFMAs and the cuts.  (Deciding stage by stage instead doubled
+// the registers; a look over all scales first took 64 tokens x 2 of 16 experts of 11008
+// x 4096 from 110 to 122 us.)
 #pragma once
 
 #include <type_traits>
